@@ -209,8 +209,9 @@ GDN_API gdn_status_t gdn_chunk_forward_noalloc(const gdn_shape_t *shape,
                                        void *o, float *final_state,
                                        void *stream);
 
-/* Reads the device status word that gdn_chunk_forward, gdn_kda_forward or
- * gdn_chunk_backward left in `workspace` into *device_status: GDN_OK, or
+/* Reads the device status word that gdn_chunk_forward, gdn_kda_forward,
+ * gdn_chunk_backward, gdn_decay_forward or gdn_decay_backward left in
+ * `workspace` into *device_status: GDN_OK, or
  * GDN_ERR_DEVICE_CHECK when the schedule rejected cu_seqlens or a
  * tensor-core kernel's bounded wait timed out (the outputs are then not, or
  * not all, written).  Synchronises `stream`.  This and
@@ -467,6 +468,131 @@ GDN_API gdn_status_t gdn_short_conv(int32_t num_seqs, int32_t seq_len, const int
                                     int32_t channels, int32_t width, int32_t dtype, const void *x,
                                     const float *weight, const float *state_in, float *state_out, void *y,
                                     uint32_t flags, void *stream);
+
+/* Linear attention with a decay for each value head: the recurrence of the
+ * gated delta rule without its delta,
+ *     S_t = alpha_t S_{t-1} + v_t k_t^T,   o_t = S_t q_t,   alpha_t = exp(g_t)
+ * ("Gated Attention Architectures", section 1: linear attention's state
+ * and the decay-masked chunk output).  Layouts, groups of value heads, the
+ * floor on g and the states are gdn_chunk_forward's; there is no beta and no
+ * normalisation of q and k.  g has one of two layouts:
+ *   GDN_DECAY_PER_TOKEN   g [tokens, Hv] fp32 (decode: [N, Hv])
+ *   GDN_DECAY_PER_HEAD    g [Hv] fp32, one decay a head for every token     */
+#define GDN_DECAY_PER_TOKEN 0
+#define GDN_DECAY_PER_HEAD 1
+
+/* Prefill.  shape->chunk_size must be 64 and shape->flags 0 or
+ * GDN_FLAG_FORCE_SIMT (GDN_ERR_UNSUPPORTED otherwise); d_k, d_v <= 128.
+ *   q, k           [tokens, Hk, d_k] dtype;  v, o [tokens, Hv, d_v] dtype
+ *   initial_state  [N, Hv, d_v, d_k] fp32, or NULL for zeros
+ *   cu_seqlens     [N + 1] int32 device array, or NULL (batched), checked on
+ *                  the device as for gdn_chunk_forward: a violation leaves o
+ *                  and final_state as they were and is read back with
+ *                  gdn_read_device_status
+ *   out_side       the output side, applied as a second pass over o, or NULL
+ *   final_state    [N, Hv, d_v, d_k] fp32 or NULL; may alias initial_state
+ *   workspace      gdn_decay_forward_workspace_size bytes, 256-byte aligned:
+ *                  the segment table, and the states at the cuts of sequences
+ *                  that are split because whole ones would leave SMs idle.
+ *                  Calls that may overlap on the GPU need one each.
+ * A sequence without tokens gets its initial state as its final state. */
+GDN_API gdn_status_t gdn_decay_forward_workspace_size(const gdn_shape_t *shape, size_t *bytes);
+GDN_API gdn_status_t gdn_decay_forward(const gdn_shape_t *shape,
+                               const void *q, const void *k, const void *v,
+                               const float *g, int32_t g_layout,
+                               const float *initial_state,
+                               const int32_t *cu_seqlens,
+                               const gdn_output_side_t *out_side,
+                               void *o, float *final_state,
+                               void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/* One token for each of N sequences, state updated in place (one read and
+ * one write of S).  Shapes as for gdn_decode_step; d_k <= 256.  out_side
+ * (or NULL) is applied as a second pass over o. */
+GDN_API gdn_status_t gdn_decay_decode_step(int32_t num_seqs, int32_t num_qk_heads, int32_t num_v_heads,
+                                 int32_t head_dim_k, int32_t head_dim_v, int32_t dtype,
+                                 const void *q, const void *k, const void *v,
+                                 const float *g, int32_t g_layout,
+                                 float *state, const gdn_output_side_t *out_side,
+                                 void *o, void *stream);
+
+/* Gradients of L = sum d_o . o + sum d_final_state . S_final for
+ * gdn_decay_forward (without an output side):
+ *   dq, dk           [tokens, Hk, d_k] dtype: summed over the value heads of
+ *                    each group in 32 bits, rounded once
+ *   dv               [tokens, Hv, d_v] dtype
+ *   dg               g's layout, fp32, or NULL where the decays are not
+ *                    learned (saves the pairwise sums); zero where g < -20
+ *   d_initial_state  [N, Hv, d_v, d_k] fp32, or NULL
+ *   d_final_state    NULL = zero
+ * Every sum is taken in a fixed order: the same call gives the same bits.
+ * A rejected cu_seqlens leaves the gradients as they were. */
+GDN_API gdn_status_t gdn_decay_backward_workspace_size(const gdn_shape_t *shape, size_t *bytes);
+GDN_API gdn_status_t gdn_decay_backward(const gdn_shape_t *shape,
+                                const void *q, const void *k, const void *v,
+                                const float *g, int32_t g_layout,
+                                const float *initial_state,
+                                const int32_t *cu_seqlens,
+                                const void *d_o, const float *d_final_state,
+                                void *dq, void *dk, void *dv, float *dg,
+                                float *d_initial_state,
+                                void *workspace, size_t workspace_bytes,
+                                void *stream);
+
+/* The norms around a block, fused with its gate and the residual connection
+ * (the output side above is the per-head norm inside the mixer; this is the
+ * step from the mixer's output projection to the next block's input).  Per
+ * row of `width` values, in fp32:
+ *     b = post(x) * act(z),   h = residual_scale r + branch_scale s * b,
+ *     y = pre(h),
+ *     post(x) = x / sqrt(mean(x^2) + eps) * w1   with GDN_BLOCK_POST_NORM,
+ *               else x;
+ *     pre(h)  = h / sqrt(mean(h^2) + eps) * w2   with GDN_BLOCK_PRE_NORM,
+ *               else there is no y.
+ * The weights w1, w2 and the per-channel scale s are fp32 [width]; NULL reads
+ * as a unit weight.  With GDN_BLOCK_ZERO_CENTRED the weights w1 and w2 hold
+ * offsets from 1.  y is taken from h before h is rounded.                   */
+#define GDN_BLOCK_POST_NORM 1u
+#define GDN_BLOCK_PRE_NORM 2u
+#define GDN_BLOCK_GATE_SILU 4u
+#define GDN_BLOCK_GATE_SIGMOID 8u
+#define GDN_BLOCK_ZERO_CENTRED 16u
+typedef struct {
+    const float *post_weight; /* w1 (needs GDN_BLOCK_POST_NORM), or NULL     */
+    const float *scale;       /* s, or NULL                                  */
+    const float *pre_weight;  /* w2 (needs GDN_BLOCK_PRE_NORM), or NULL      */
+    float eps;                /* finite and > 0                              */
+    float residual_scale;     /* finite                                      */
+    float branch_scale;       /* finite                                      */
+    uint32_t flags;           /* GDN_BLOCK_* bits                            */
+} gdn_block_norm_t;
+
+/* Forward.  x, gate (z, or NULL) and y are [rows, width] of `dtype`; residual
+ * (r, or NULL for none) and h of `residual_dtype`, which is `dtype` or
+ * GDN_DTYPE_F32.  With a gate exactly one of the gate flags is set.  h may be
+ * NULL; h may be residual and y may be x (in place), other overlaps are not
+ * allowed.  1 <= width <= 16384. */
+GDN_API gdn_status_t gdn_block_norm_forward(int64_t rows, int32_t width, int32_t dtype, int32_t residual_dtype,
+                                    const void *x, const void *residual, const void *gate,
+                                    const gdn_block_norm_t *norm, void *h, void *y, void *stream);
+
+/* Gradients for upstream gradients d_h (of h, residual_dtype) and d_y (of y,
+ * dtype); either may be NULL (zero).  The inputs are the forward's (residual
+ * as it was before the call); h and the norms are recomputed.  Outputs, each
+ * NULL where it is not wanted: dx and d_gate of `dtype`, d_residual of
+ * `residual_dtype`, d_post_weight, d_scale and d_pre_weight fp32 [width]
+ * (gradients of the weights as stored).  Outputs overlap nothing.  The sums
+ * over rows are taken in a fixed order.  workspace:
+ * gdn_block_norm_backward_workspace_size bytes, 256-byte aligned; calls that
+ * may overlap on the GPU need one each. */
+GDN_API gdn_status_t gdn_block_norm_backward_workspace_size(int64_t rows, int32_t width, size_t *bytes);
+GDN_API gdn_status_t gdn_block_norm_backward(int64_t rows, int32_t width, int32_t dtype, int32_t residual_dtype,
+                                     const void *x, const void *residual, const void *gate,
+                                     const gdn_block_norm_t *norm, const void *d_h, const void *d_y,
+                                     void *dx, void *d_residual, void *d_gate,
+                                     float *d_post_weight, float *d_scale, float *d_pre_weight,
+                                     void *workspace, size_t workspace_bytes, void *stream);
 
 /* Static text for a status code. */
 GDN_API const char *gdn_status_string(gdn_status_t status);

@@ -11,7 +11,8 @@ __all__ = ["gdn", "inputs", "build"]
 
 
 def __getattr__(name):
-    if name in ("chunk_forward", "decode_step", "workspace_size", "read_device_status", "launch_count"):
+    if name in ("chunk_forward", "decode_step", "workspace_size", "read_device_status", "launch_count",
+                "decay_forward", "decay_decode_step", "decay_backward", "block_norm_forward", "block_norm_backward"):
         from . import gdn
         return getattr(gdn, name)
     raise AttributeError(name)

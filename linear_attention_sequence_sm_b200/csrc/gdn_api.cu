@@ -15,7 +15,7 @@ void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 
 static thread_local char g_msg[512] = "";
 
-static gdn_status_t fail(gdn_status_t st, const char *fmt, ...) {
+gdn_status_t fail(gdn_status_t st, const char *fmt, ...) {
     va_list ap;
     va_start(ap, fmt);
     vsnprintf(g_msg, sizeof(g_msg), fmt, ap);
@@ -23,19 +23,21 @@ static gdn_status_t fail(gdn_status_t st, const char *fmt, ...) {
     return st;
 }
 
+void clear_error() { g_msg[0] = 0; }
+
 // Records the per-thread error text for entry points defined in other files.
 gdn_status_t set_error(gdn_status_t st, const char *text) {
     snprintf(g_msg, sizeof(g_msg), "%s", text);
     return st;
 }
 
-static gdn_status_t cuda_fail(cudaError_t e, const char *what) {
+gdn_status_t cuda_fail(cudaError_t e, const char *what) {
     return fail(GDN_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
-static bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-static int device_sm_count(int *major) {
+int device_sm_count(int *major) {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return -1;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
@@ -43,7 +45,7 @@ static int device_sm_count(int *major) {
     return sms;
 }
 
-static gdn_status_t check_shape(const gdn_shape_t *s) {
+gdn_status_t check_shape(const gdn_shape_t *s) {
     if (!s) return fail(GDN_ERR_INVALID_ARGUMENT, "shape is NULL");
     if (s->batch < 0 || s->seq_len < 0 || s->num_seqs < 0)
         return fail(GDN_ERR_INVALID_ARGUMENT, "negative batch/seq_len/num_seqs");
@@ -93,7 +95,7 @@ static int32_t select_path(const gdn_shape_t &s, int major, bool out_side, size_
     return GDN_PATH_SIMT;
 }
 
-static gdn_status_t check_output_side(const gdn_output_side_t *os, OutSide *out) {
+gdn_status_t check_output_side(const gdn_output_side_t *os, OutSide *out) {
     *out = OutSide{nullptr, nullptr, 0.f, 0u};
     if (!os) return GDN_OK;
     const uint32_t known = GDN_OUT_GATE_SILU | GDN_OUT_GATE_SIGMOID | GDN_OUT_ZERO_CENTRED | GDN_OUT_WEIGHT_PER_HEAD;

@@ -1,0 +1,457 @@
+// gdn_block_norm.cu -- the norms around a block, fused with its gate and the
+// residual connection (gdn_block_norm_forward, gdn_block_norm_backward).
+//
+// Per row of `width` values, with mean-square norms (fp32 throughout):
+//     n1 = x / sqrt(mean(x^2) + eps)                (x itself without POST_NORM)
+//     b  = n1 * w1 * act(z)
+//     h  = rho r + c s * b
+//     n2 = h / sqrt(mean(h^2) + eps),   y = n2 * w2
+// and, for upstream gradients dh and dy, with dn2 = dy * w2,
+//     e   = dh + (dn2 - n2 mean(dn2 . n2)) / rms(h)         (h's whole gradient)
+//     dr  = rho e,     db = c s e,     du = db act(z),   dz = db n1 w1 act'(z),
+//     dn1 = du w1,     dx = (dn1 - n1 mean(dn1 . n1)) / rms(x),
+//     dw2 = sum dy n2, ds = sum c e b, dw1 = sum du n1      (sums over rows)
+//
+// Both are bound by memory: each input row is read once into registers, h and
+// the norms are recomputed in the backward instead of kept.
+#include <algorithm>
+
+#include "gdn_block_norm.cuh"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kMaxThreads = 1024;
+
+template <typename T> __device__ __forceinline__ void load8(const T *p, float (&v)[8]);
+template <> __device__ __forceinline__ void load8<float>(const float *p, float (&v)[8]) {
+    const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+template <> __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16 *p, float (&v)[8]) {
+    const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p));
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void load8w(const float *p, float (&v)[8]) {  // weights: cached
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+template <typename T> __device__ __forceinline__ void store8(T *p, const float (&v)[8]);
+template <> __device__ __forceinline__ void store8<float>(float *p, const float (&v)[8]) {
+    __stcs(reinterpret_cast<float4 *>(p), make_float4(v[0], v[1], v[2], v[3]));
+    __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
+}
+template <> __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16 *p, const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&t);
+    }
+    __stcs(reinterpret_cast<uint4 *>(p), make_uint4(w[0], w[1], w[2], w[3]));
+}
+
+// A thread's values of a row: group i holds columns 8 (i n + t) .. + 7 (n
+// threads a row) where rows are 16-byte multiples (kVec), else columns
+// (8 i + e) n + t.
+template <bool kVec, typename T>
+__device__ __forceinline__ void row_load(const T *row, int i, int t, int n, int width, float (&v)[8]) {
+    if constexpr (kVec) {
+        const int c = 8 * (i * n + t);
+        if (c < width) {
+            load8(row + c, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = 0.f;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int c = (8 * i + e) * n + t;
+            v[e] = c < width ? to_f32(row[c]) : 0.f;
+        }
+    }
+}
+// Weights of the same columns; `none` where the pointer is NULL.
+template <bool kVec>
+__device__ __forceinline__ void weight_load(const float *w, float none, float add, int i, int t, int n, int width,
+                                            float (&v)[8]) {
+    if (!w) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = none;
+        return;
+    }
+    if constexpr (kVec) {
+        const int c = 8 * (i * n + t);
+        if (c < width) {
+            load8w(w + c, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = 0.f;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int c = (8 * i + e) * n + t;
+            v[e] = c < width ? __ldg(w + c) : 0.f;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += add;
+}
+template <bool kVec, typename T>
+__device__ __forceinline__ void row_store(T *row, int i, int t, int n, int width, const float (&v)[8]) {
+    if constexpr (kVec) {
+        const int c = 8 * (i * n + t);
+        if (c < width) store8(row + c, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int c = (8 * i + e) * n + t;
+            if (c < width) row[c] = from_f32<T>(v[e]);
+        }
+    }
+}
+
+// Sums of kN values over the n threads of a row (n a multiple of 32; the
+// block's rows reduce together).  `red` has kN * 32 floats per row.
+template <int kN>
+__device__ __forceinline__ void row_sum(float (&v)[kN], float *red, int t, int n) {
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1)
+#pragma unroll
+        for (int j = 0; j < kN; ++j) v[j] += __shfl_xor_sync(0xffffffffu, v[j], m);
+    if (n == 32) return;
+    const int warps = n >> 5, w = t >> 5, lane = t & 31;
+    __syncthreads();  // the previous use of `red` has been read
+    if (lane == 0)
+#pragma unroll
+        for (int j = 0; j < kN; ++j) red[32 * j + w] = v[j];
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+        float s = lane < warps ? red[32 * j + lane] : 0.f;
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+        v[j] = s;
+    }
+}
+
+// Sigmoid: the exact exponential for fp32 rows; for bf16 rows the fast one,
+// about 1e-6 off relative to the result, far below their rounding.
+template <typename T> __device__ __forceinline__ float gate_sigmoid(float z) {
+    if constexpr (sizeof(T) == 4) return sigmoid(z);
+    return sigmoid_fast(z);
+}
+
+template <typename T, typename R, bool kVec, int kGroups>
+__global__ void __launch_bounds__(kMaxThreads)
+block_norm_forward_kernel(const BlockNormArgs a) {
+    __shared__ float red_all[32 * 8];
+    const int n = blockDim.x, t = threadIdx.x, width = a.width;
+    const int64_t row = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
+    const bool live = row < a.rows;
+    float *red = red_all + 32 * threadIdx.y;
+    const int64_t at = (live ? row : 0) * width;
+    const T *x = static_cast<const T *>(a.x) + at, *z = a.gate ? static_cast<const T *>(a.gate) + at : nullptr;
+    const R *r = a.residual ? static_cast<const R *>(a.residual) + at : nullptr;
+    const float zc = (a.flags & GDN_BLOCK_ZERO_CENTRED) ? 1.f : 0.f;
+    const float none = zc != 0.f ? 0.f : 1.f;
+    float xv[kGroups][8], hv[kGroups][8];
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) row_load<kVec>(x, i, t, n, width, xv[i]);
+    float scale1 = 1.f;
+    const bool post = a.flags & GDN_BLOCK_POST_NORM;
+    if (post) {
+        float ss[1] = {0.f};
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss[0] = fmaf(xv[i][e], xv[i][e], ss[0]);
+        row_sum(ss, red, t, n);
+        scale1 = 1.f / sqrtf(ss[0] / float(width) + a.eps);
+    }
+    float ss[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+        float w1[8], s[8], zv[8], rv[8];
+        weight_load<kVec>(post ? a.post_weight : nullptr, post ? none : 1.f, post ? zc : 0.f, i, t, n, width, w1);
+        weight_load<kVec>(a.scale, 1.f, 0.f, i, t, n, width, s);
+        if (z) row_load<kVec>(z, i, t, n, width, zv);
+        if (r) row_load<kVec>(r, i, t, n, width, rv);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float b = xv[i][e] * scale1 * w1[e];
+            if (z) {
+                const float sg = gate_sigmoid<T>(zv[e]);
+                b *= (a.flags & GDN_BLOCK_GATE_SILU) ? zv[e] * sg : sg;
+            }
+            b *= a.branch_scale * s[e];
+            hv[i][e] = r ? fmaf(a.residual_scale, rv[e], b) : b;
+            ss[0] = fmaf(hv[i][e], hv[i][e], ss[0]);
+        }
+    }
+    if (live && a.h)
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) row_store<kVec>(static_cast<R *>(a.h) + at, i, t, n, width, hv[i]);
+    if (!(a.flags & GDN_BLOCK_PRE_NORM)) return;
+    row_sum(ss, red, t, n);
+    const float scale2 = 1.f / sqrtf(ss[0] / float(width) + a.eps);
+    if (!live) return;
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+        float w2[8];
+        weight_load<kVec>(a.pre_weight, none, zc, i, t, n, width, w2);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w2[e] *= hv[i][e] * scale2;
+        row_store<kVec>(static_cast<T *>(a.y) + at, i, t, n, width, w2);
+    }
+}
+
+// A block row-group (threadIdx.y) walks rows with a stride; its columns' sums
+// stay in registers and go to its own line of the workspace.
+template <typename T, typename R, bool kVec, int kGroups>
+__global__ void __launch_bounds__(512)
+block_norm_backward_kernel(const BlockNormArgs a) {
+    __shared__ float red_all[64 * 8];
+    const int n = blockDim.x, t = threadIdx.x, width = a.width;
+    float *red = red_all + 64 * threadIdx.y;
+    const int64_t lines = int64_t(gridDim.x) * blockDim.y, line = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
+    const float zc = (a.flags & GDN_BLOCK_ZERO_CENTRED) ? 1.f : 0.f;
+    const float none = zc != 0.f ? 0.f : 1.f;
+    const bool post = a.flags & GDN_BLOCK_POST_NORM, pre = (a.flags & GDN_BLOCK_PRE_NORM) && a.d_y;
+    const bool silu = a.flags & GDN_BLOCK_GATE_SILU;
+    float sw1[kGroups][8], sw2[kGroups][8], ssc[kGroups][8];
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sw1[i][e] = sw2[i][e] = ssc[i][e] = 0.f;
+    const int64_t turns = (a.rows + lines - 1) / lines;
+    for (int64_t turn = 0; turn < turns; ++turn) {
+        const int64_t row = turn * lines + line;
+        const bool live = row < a.rows;
+        const int64_t at = (live ? row : 0) * width;
+        const T *x = static_cast<const T *>(a.x) + at, *z = a.gate ? static_cast<const T *>(a.gate) + at : nullptr;
+        const R *r = a.residual ? static_cast<const R *>(a.residual) + at : nullptr;
+        float xv[kGroups][8], zv[kGroups][8], hv[kGroups][8], yv[kGroups][8], ev[kGroups][8];
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            row_load<kVec>(x, i, t, n, width, xv[i]);
+            if (z) row_load<kVec>(z, i, t, n, width, zv[i]);
+            if (r) {
+                row_load<kVec>(r, i, t, n, width, hv[i]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) hv[i][e] = 0.f;
+            }
+            if (pre) row_load<kVec>(static_cast<const T *>(a.d_y) + at, i, t, n, width, yv[i]);
+            if (a.d_h) {
+                row_load<kVec>(static_cast<const R *>(a.d_h) + at, i, t, n, width, ev[i]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ev[i][e] = 0.f;
+            }
+        }
+        float scale1 = 1.f;
+        if (post) {
+            float ss[1] = {0.f};
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ss[0] = fmaf(xv[i][e], xv[i][e], ss[0]);
+            row_sum(ss, red, t, n);
+            scale1 = 1.f / sqrtf(ss[0] / float(width) + a.eps);
+        }
+        // h, and the sums of h^2 and dy w2 h
+        float s2[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            float w1[8], s[8], w2[8];
+            weight_load<kVec>(post ? a.post_weight : nullptr, post ? none : 1.f, post ? zc : 0.f, i, t, n, width, w1);
+            weight_load<kVec>(a.scale, 1.f, 0.f, i, t, n, width, s);
+            if (pre) weight_load<kVec>(a.pre_weight, none, zc, i, t, n, width, w2);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                xv[i][e] *= scale1;  // n1
+                float b = xv[i][e] * w1[e];
+                if (z) {
+                    const float sg = gate_sigmoid<T>(zv[i][e]);
+                    b *= silu ? zv[i][e] * sg : sg;
+                }
+                hv[i][e] = fmaf(a.residual_scale, hv[i][e], a.branch_scale * s[e] * b);
+                if (pre) {
+                    s2[0] = fmaf(hv[i][e], hv[i][e], s2[0]);
+                    s2[1] = fmaf(yv[i][e] * w2[e], hv[i][e], s2[1]);
+                }
+            }
+        }
+        float scale2 = 0.f, mean2 = 0.f;
+        if (pre) {
+            row_sum(s2, red, t, n);
+            scale2 = 1.f / sqrtf(s2[0] / float(width) + a.eps);
+            mean2 = scale2 * s2[1] / float(width);  // mean(dn2 . n2)
+        }
+        float s3[1] = {0.f};
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            float w1[8], s[8], w2[8], dr[8], dzv[8];
+            weight_load<kVec>(post ? a.post_weight : nullptr, post ? none : 1.f, post ? zc : 0.f, i, t, n, width, w1);
+            weight_load<kVec>(a.scale, 1.f, 0.f, i, t, n, width, s);
+            if (pre) weight_load<kVec>(a.pre_weight, none, zc, i, t, n, width, w2);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float g = ev[i][e];
+                if (pre) {
+                    const float n2 = hv[i][e] * scale2;
+                    g = fmaf(scale2, fmaf(-n2, mean2, yv[i][e] * w2[e]), g);
+                    if (live) sw2[i][e] = fmaf(yv[i][e], n2, sw2[i][e]);
+                }
+                dr[e] = a.residual_scale * g;
+                const float n1 = xv[i][e], u = n1 * w1[e], cg = a.branch_scale * g;
+                const float db = cg * s[e];
+                float act = 1.f, du = db;
+                dzv[e] = 0.f;
+                if (z) {
+                    const float zz = zv[i][e], sg = gate_sigmoid<T>(zz);
+                    act = silu ? zz * sg : sg;
+                    du = db * act;
+                    dzv[e] = db * u * (silu ? sg * fmaf(zz, 1.f - sg, 1.f) : sg * (1.f - sg));
+                }
+                if (live) {
+                    ssc[i][e] = fmaf(cg, u * act, ssc[i][e]);
+                    sw1[i][e] = fmaf(du, n1, sw1[i][e]);
+                }
+                ev[i][e] = du * w1[e];  // dn1 (dx without the norm)
+                s3[0] = fmaf(ev[i][e], n1, s3[0]);
+            }
+            if (live && a.d_residual) row_store<kVec>(static_cast<R *>(a.d_residual) + at, i, t, n, width, dr);
+            if (live && a.d_gate) row_store<kVec>(static_cast<T *>(a.d_gate) + at, i, t, n, width, dzv);
+        }
+        if (post) {
+            row_sum(s3, red, t, n);
+            const float mean1 = s3[0] / float(width);
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ev[i][e] = scale1 * fmaf(-xv[i][e], mean1, ev[i][e]);
+        }
+        if (live && a.dx)
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) row_store<kVec>(static_cast<T *>(a.dx) + at, i, t, n, width, ev[i]);
+    }
+    float *out = a.partial + line * 3 * width;
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+        if (a.d_post_weight) row_store<kVec>(out, i, t, n, width, sw1[i]);
+        if (a.d_scale) row_store<kVec>(out + width, i, t, n, width, ssc[i]);
+        if (a.d_pre_weight) row_store<kVec>(out + 2 * width, i, t, n, width, sw2[i]);
+    }
+}
+
+// Column sums of the lines, 16 partial sums per column joined in a fixed order.
+__global__ void __launch_bounds__(512)
+block_norm_columns_kernel(const float *__restrict__ part, int lines, int width, float *dw1, float *ds, float *dw2) {
+    __shared__ float sum[16][33];
+    float *dst = blockIdx.y == 0 ? dw1 : blockIdx.y == 1 ? ds : dw2;
+    if (!dst) return;
+    const int c = blockIdx.x * 32 + threadIdx.x;
+    float s = 0.f;
+    if (c < width) {
+        const float *p = part + size_t(blockIdx.y) * width + c;
+#pragma unroll 8
+        for (int i = threadIdx.y; i < lines; i += 16) s += p[size_t(i) * 3 * width];
+    }
+    sum[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.y == 0 && c < width) {
+        s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s += sum[i][threadIdx.x];
+        dst[c] = s;
+    }
+}
+
+// Threads a row takes (a multiple of 32) with `groups` 8-value groups each.
+int row_threads(int width, int groups) { return ((width + 8 * groups - 1) / (8 * groups) + 31) / 32 * 32; }
+
+template <typename T, typename R>
+bool rows_vectorised(const BlockNormArgs &a) {
+    return a.width % (16 / int(sizeof(T))) == 0 && a.width % 8 == 0;
+}
+
+template <typename T, typename R>
+cudaError_t forward_as(const BlockNormArgs &a, cudaStream_t stream) {
+    const bool vec = rows_vectorised<T, R>(a);
+    const int groups = a.width <= 2048 ? 1 : a.width <= 16384 ? 2 : 4;
+    const int n = row_threads(a.width, groups);
+    const int per = std::max(1, std::min(8, 128 / n));
+    const int64_t grid = (a.rows + per - 1) / per;
+    if (grid > INT32_MAX) return cudaErrorInvalidValue;
+    const dim3 block(n, per);
+#define GDN_NORM_FWD(V, G) block_norm_forward_kernel<T, R, V, G><<<unsigned(grid), block, 0, stream>>>(a)
+    if (vec) {
+        if (groups == 1) GDN_NORM_FWD(true, 1); else if (groups == 2) GDN_NORM_FWD(true, 2); else GDN_NORM_FWD(true, 4);
+    } else {
+        if (groups == 1) GDN_NORM_FWD(false, 1); else if (groups == 2) GDN_NORM_FWD(false, 2); else GDN_NORM_FWD(false, 4);
+    }
+#undef GDN_NORM_FWD
+    count_launch();
+    return cudaGetLastError();
+}
+
+template <typename T, typename R>
+cudaError_t backward_as(const BlockNormArgs &a, cudaStream_t stream) {
+    const bool vec = rows_vectorised<T, R>(a);
+    const int groups = a.width <= 2048 ? 1 : a.width <= 8192 ? 2 : 4;
+    const int n = row_threads(a.width, groups);
+    const int per = std::max(1, std::min(8, 128 / n));
+    const int grid = block_norm_lines(a.rows, a.width) / per;
+    const dim3 block(n, per);
+#define GDN_NORM_BWD(V, G) block_norm_backward_kernel<T, R, V, G><<<unsigned(grid), block, 0, stream>>>(a)
+    if (vec) {
+        if (groups == 1) GDN_NORM_BWD(true, 1); else if (groups == 2) GDN_NORM_BWD(true, 2); else GDN_NORM_BWD(true, 4);
+    } else {
+        if (groups == 1) GDN_NORM_BWD(false, 1); else if (groups == 2) GDN_NORM_BWD(false, 2); else GDN_NORM_BWD(false, 4);
+    }
+#undef GDN_NORM_BWD
+    count_launch();
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    if (a.d_post_weight || a.d_scale || a.d_pre_weight) {
+        block_norm_columns_kernel<<<dim3(unsigned((a.width + 31) / 32), 3), dim3(32, 16), 0, stream>>>(
+            a.partial, grid * per, a.width, a.d_post_weight, a.d_scale, a.d_pre_weight);
+        count_launch();
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+}  // namespace
+
+// Row groups of the backward, each with a line of column sums in the workspace.
+int block_norm_lines(int64_t rows, int32_t width) {
+    const int groups = width <= 2048 ? 1 : width <= 8192 ? 2 : 4;
+    const int n = row_threads(width, groups), per = std::max(1, std::min(8, 128 / n));
+    const int resident = std::max(1, 512 / (n * per));  // blocks an SM holds at the kernel's registers
+    const int64_t blocks = std::min<int64_t>((rows + per - 1) / per, int64_t(148) * resident);
+    return int(std::max<int64_t>(blocks, 1)) * per;
+}
+
+cudaError_t launch_block_norm_forward(const BlockNormArgs &a, int32_t dtype, int32_t rdtype, cudaStream_t stream) {
+    using bf = __nv_bfloat16;
+    if (dtype == GDN_DTYPE_F32) return forward_as<float, float>(a, stream);
+    return rdtype == GDN_DTYPE_F32 ? forward_as<bf, float>(a, stream) : forward_as<bf, bf>(a, stream);
+}
+cudaError_t launch_block_norm_backward(const BlockNormArgs &a, int32_t dtype, int32_t rdtype, cudaStream_t stream) {
+    using bf = __nv_bfloat16;
+    if (dtype == GDN_DTYPE_F32) return backward_as<float, float>(a, stream);
+    return rdtype == GDN_DTYPE_F32 ? backward_as<bf, float>(a, stream) : backward_as<bf, bf>(a, stream);
+}
+
+}  // namespace gdn

@@ -1,0 +1,421 @@
+// gdn_decay_sched.cu -- the decayed linear attention's plan and its small
+// kernels: the segment table, the start states of cut sequences, the decays'
+// gradient from its parts, and sums over grouped heads.
+#include <algorithm>
+
+#include "gdn_decay.cuh"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kSchedThreads = 1024;
+// Above this many sequences the longest-first ranking (quadratic in N) is
+// skipped and sequences keep their given order.
+constexpr int kMaxRankedSeqs = 8192;
+
+// Tokens times heads each SM takes when the work is spread evenly.
+__host__ __device__ inline int64_t balanced_tokens(int64_t tokens, int hv) {
+    return (tokens * hv + kDecayPlanSms - 1) / kDecayPlanSms;
+}
+
+// Exclusive prefix sums over the block of one value per thread; *total gets the sum.
+__device__ int block_scan(int v, int *part, int *total) {
+    part[threadIdx.x] = v;
+    __syncthreads();
+    for (int d = 1; d < kSchedThreads; d <<= 1) {
+        const int add = threadIdx.x >= unsigned(d) ? part[threadIdx.x - d] : 0;
+        __syncthreads();
+        part[threadIdx.x] += add;
+        __syncthreads();
+    }
+    const int mine = part[threadIdx.x] - v;
+    *total = part[kSchedThreads - 1];
+    __syncthreads();
+    return mine;
+}
+
+// Checks cu_seqlens and writes the segment table, longest sequences first.
+// A sequence is a chain of dependent chunks, so a call with few sequences and
+// heads would leave SMs idle: with B = tokens * Hv / 148 (a perfect spread) and
+// the longest sequence at least 2 B, sequences are cut into segments of
+// ceil(longest / floor(longest / B)) tokens, whose start states come from a
+// first sweep over all segments but one end's (k and v are then read twice, a
+// third of the prefill's traffic; the uncut chain would take at least twice as
+// long).  At 1 x 65,536 tokens and 48 heads: 3 segments of 22,528 tokens.
+__global__ void __launch_bounds__(kSchedThreads)
+decay_schedule_kernel(int32_t num_seqs, int32_t tokens, int32_t batched_len, int32_t hv,
+                      const int32_t *__restrict__ cu, DecaySched sc, int32_t *order) {
+    __shared__ int bad, longest;
+    __shared__ int part[kSchedThreads];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    DecayHeader *hdr = sc.hdr;
+    if (threadIdx.x == 0) {
+        bad = -1;
+        longest = 0;
+        hdr->status = GDN_OK;
+        hdr->bad_index = -1;
+        for (int i = 0; i < 6; ++i) hdr->next_unit[i] = 0;
+        hdr->num_segs = hdr->num_split = hdr->num_cks = hdr->total_chunks = 0;
+        hdr->ick = kDecayMaxIck;
+        hdr->seg_len = 0;
+    }
+    __syncthreads();
+    auto start_of = [&](int n) { return cu ? cu[n] : n * batched_len; };
+    auto len_of = [&](int n) { return cu ? cu[n + 1] - cu[n] : batched_len; };
+    int most = 0;
+    for (int n = threadIdx.x; n < num_seqs; n += blockDim.x) {
+        if (cu) {
+            const int s0 = cu[n], s1 = cu[n + 1];
+            const bool ok = s1 >= s0 && s0 >= 0 && s1 <= tokens && (n != 0 || s0 == 0) &&
+                            (n != num_seqs - 1 || s1 == tokens);
+            if (!ok) atomicMax(&bad, n);
+        }
+        most = max(most, len_of(n));
+    }
+    atomicMax(&longest, most);
+    __syncthreads();
+    if (bad >= 0) {
+        if (threadIdx.x == 0) {
+            hdr->status = GDN_ERR_DEVICE_CHECK;
+            hdr->bad_index = bad;
+        }
+        return;
+    }
+    // segment length and checkpoint spacing
+    int seg_len = INT32_MAX, ick = kDecayMaxIck;
+    {
+        const int64_t balanced = balanced_tokens(tokens, hv);
+        const int64_t k = balanced > 0 ? longest / balanced : 1;
+        if (k >= 2 && longest > kDecayMinSeg) {
+            int64_t L = (longest + k - 1) / k;
+            L = L <= kDecayMinSeg ? kDecayMinSeg : L <= 2 * kDecayMinSeg ? 2 * kDecayMinSeg
+                                                                         : (L + kDecayMaxIck - 1) / kDecayMaxIck * kDecayMaxIck;
+            seg_len = int(L);
+            ick = min(seg_len, kDecayMaxIck);
+        }
+    }
+    // longest first, ties by index
+    const bool rank_it = cu != nullptr && num_seqs <= kMaxRankedSeqs;
+    for (int n = threadIdx.x; n < num_seqs; n += blockDim.x) {
+        int r = n;
+        if (rank_it) {
+            const int ln = len_of(n);
+            r = 0;
+            for (int m = 0; m < num_seqs; ++m) {
+                const int lm = len_of(m);
+                r += (lm > ln) || (lm == ln && m < n);
+            }
+        }
+        order[r] = n;
+    }
+    // chunks and checkpoint slots before each sequence: each thread takes a run of sequences
+    const int per = (num_seqs + kSchedThreads - 1) / kSchedThreads;
+    const int n0 = min(num_seqs, int(threadIdx.x) * per), n1 = min(num_seqs, n0 + per);
+    int chunks = 0, cks = 0, total_chunks, total_cks;
+    for (int n = n0; n < n1; ++n) {
+        chunks += (len_of(n) + kDecayChunk - 1) / kDecayChunk;
+        cks += (len_of(n) + ick - 1) / ick;
+    }
+    chunks = block_scan(chunks, part, &total_chunks);
+    cks = block_scan(cks, part, &total_cks);
+    for (int n = n0; n < n1; ++n) {
+        sc.chunk_base[n] = chunks;
+        sc.ck_base[n] = cks;
+        chunks += (len_of(n) + kDecayChunk - 1) / kDecayChunk;
+        cks += (len_of(n) + ick - 1) / ick;
+    }
+    __syncthreads();  // order, ck_base
+    // segments, sequences by rank
+    auto segs_of = [&](int n) { return len_of(n) <= seg_len ? 1 : (len_of(n) + seg_len - 1) / seg_len; };
+    int segs = 0, cut = 0, slots = 0, total_segs, total_cut, total_slots;
+    for (int r = n0; r < n1; ++r) {
+        const int c = segs_of(order[r]);
+        segs += c;
+        cut += c > 1;
+        slots += c > 1 ? c : 0;
+    }
+    segs = block_scan(segs, part, &total_segs);
+    cut = block_scan(cut, part, &total_cut);
+    slots = block_scan(slots, part, &total_slots);
+    for (int r = n0; r < n1; ++r) {
+        const int n = order[r], c = segs_of(n), len = len_of(n);
+        if (c > 1) sc.split[cut++] = segs;
+        for (int i = 0; i < c; ++i) {
+            DecaySeg g;
+            g.pos = i * seg_len * (c > 1);
+            g.len = c > 1 ? min(seg_len, len - g.pos) : len;
+            g.start = start_of(n) + g.pos;
+            g.seq_len = len;
+            g.seq = n;
+            g.slot = c > 1 ? slots++ : -1;
+            g.ck = sc.ck_base[n];
+            g.pad = 0;
+            sc.segs[segs++] = g;
+        }
+    }
+    if (threadIdx.x == 0) {
+        sc.chunk_base[num_seqs] = total_chunks;
+        sc.ck_base[num_seqs] = total_cks;
+        hdr->num_segs = total_segs;
+        hdr->num_split = total_cut;
+        hdr->ick = ick;
+        hdr->seg_len = seg_len;
+        hdr->num_cks = total_cks;
+        hdr->total_chunks = total_chunks;
+    }
+}
+
+// Start states of cut sequences: thread = one element of a (cut sequence,
+// head) state, walking its segments in pass order; each slot's local state
+// becomes the state its segment starts from.
+__global__ void __launch_bounds__(256)
+decay_combine_kernel(DecaySched sc, float *__restrict__ states, const float *__restrict__ seg_dec,
+                     const float *__restrict__ s_in, int s_trans, int hv, int dz, int dy, int reverse) {
+    if (sc.hdr->status != GDN_OK) return;
+    const int h = blockIdx.y;
+    const int el = blockIdx.x * 256 + threadIdx.x;  // of the 128 x 128 padded state
+    const int r = el >> 7, c = el & 127;            // z row, y column
+    for (int j = blockIdx.z; j < sc.hdr->num_split; j += gridDim.z) {
+        const int s0 = sc.split[j];
+        const DecaySeg first = sc.segs[s0];
+        const int n = (first.seq_len + sc.hdr->seg_len - 1) / sc.hdr->seg_len;
+        float run = 0.f;
+        if (s_in && r < dz && c < dy) {
+            const size_t base = (size_t(first.seq) * hv + h) * dz * dy;
+            run = s_in[base + (s_trans ? size_t(c) * dz + r : size_t(r) * dy + c)];
+        }
+        for (int i = 0; i < n; ++i) {
+            const int slot = first.slot + (reverse ? n - 1 - i : i);
+            float *p = states + (size_t(slot) * hv + h) * 16384 + el;
+            const float local = i + 1 < n ? *p : 0.f;  // the last segment's local state is not needed
+            *p = run;
+            run = fmaf(seg_dec[size_t(slot) * hv + h], run, local);
+        }
+    }
+}
+
+// The decays' gradient: one warp per (checkpoint interval, head), its chunks
+// first to last.  For token t of a chunk with both-outside weight Y:
+//   dg_t = intra_t + sum_{i >= t} dot_q_i + sum_{j < t} dot_k_j + Y,
+// Y = (pairs across the chunk's start) - sum dot_q, and the pairs across its
+// end are Y + sum dot_k.  At an interval's start the pairs across are zsum.
+__global__ void __launch_bounds__(128)
+decay_dg_kernel(int num_seqs, int hv, int tokens, const int32_t *__restrict__ cu, int batched_len, DecaySched sc,
+                const float *__restrict__ dot_q, const float *__restrict__ dot_k, const float *__restrict__ intra,
+                const float *__restrict__ zsum, const float *__restrict__ g, int g_const, float *__restrict__ dg_tok,
+                float *__restrict__ dg) {
+    if (sc.hdr->status != GDN_OK) return;
+    const int lane = threadIdx.x & 31;
+    const int ick = sc.hdr->ick;
+    const int64_t units = int64_t(sc.hdr->num_cks) * hv;
+    for (int64_t u = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5); u < units; u += int64_t(gridDim.x) * 4) {
+        const int ck = int(u / hv), h = int(u % hv);
+        const int n = chunk_sequence(sc.ck_base, num_seqs, ck);
+        const int start = cu ? cu[n] : n * batched_len, len = cu ? cu[n + 1] - cu[n] : batched_len;
+        const int p0 = (ck - sc.ck_base[n]) * ick, p1 = min(len, p0 + ick);
+        const float *dq = dot_q + size_t(h) * tokens + start, *dk = dot_k + size_t(h) * tokens + start;
+        const float *in = intra + size_t(h) * tokens + start;
+        float across = zsum[size_t(ck) * hv + h];
+        for (int b = p0; b < p1; b += kDecayChunk) {
+            const int t0 = b + 2 * lane, t1 = t0 + 1;
+            const bool v0 = t0 < p1, v1 = t1 < p1;
+            const float q0 = v0 ? dq[t0] : 0.f, q1 = v1 ? dq[t1] : 0.f;
+            const float k0 = v0 ? dk[t0] : 0.f, k1 = v1 ? dk[t1] : 0.f;
+            float qs = q0 + q1, ks = k0 + k1;  // inclusive: qs from the end, ks from the start
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const float a = __shfl_down_sync(0xffffffffu, qs, d), e = __shfl_up_sync(0xffffffffu, ks, d);
+                if (lane + d < 32) qs += a;
+                if (lane >= d) ks += e;
+            }
+            const float qsum = __shfl_sync(0xffffffffu, qs, 0), ksum = __shfl_sync(0xffffffffu, ks, 31);
+            const float outside = across - qsum;
+            float q_after = __shfl_down_sync(0xffffffffu, qs, 1), k_before = __shfl_up_sync(0xffffffffu, ks, 1);
+            if (lane == 31) q_after = 0.f;  // sums of the lanes after and before this one
+            if (lane == 0) k_before = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int t = t0 + e;
+                if (t >= p1) continue;
+                const float r = e ? q1 + q_after : qs, f = e ? k_before + k0 : k_before;
+                float val = in[t] + r + f + outside;
+                const size_t at = size_t(start + t) * hv + h;
+                if ((g_const ? g[h] : g[at]) < kGFloor) val = 0.f;
+                if (g_const) dg_tok[size_t(h) * tokens + start + t] = val;
+                else dg[at] = val;
+            }
+            across = outside + ksum;
+        }
+    }
+}
+
+// One value per head: the sum of its tokens' gradients, in 64 bits and a fixed order.
+__global__ void __launch_bounds__(512)
+decay_dg_head_kernel(const DecayHeader *hdr, const float *__restrict__ dg_tok, int tokens, float *__restrict__ dg) {
+    __shared__ double part[512];
+    if (hdr->status != GDN_OK) return;
+    double s = 0.0;
+    for (int t = threadIdx.x; t < tokens; t += 512) s += double(dg_tok[size_t(blockIdx.x) * tokens + t]);
+    part[threadIdx.x] = s;
+    __syncthreads();
+    for (int d = 256; d > 0; d >>= 1) {
+        if (int(threadIdx.x) < d) part[threadIdx.x] += part[threadIdx.x + d];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) dg[blockIdx.x] = float(part[0]);
+}
+
+// out[t, hq, :] = the sum over the group's value heads of part[t, h, :], in head order.
+template <typename T>
+__global__ void __launch_bounds__(256)
+decay_group_sum_kernel(const DecayHeader *hdr, const float *__restrict__ part, T *__restrict__ out, int64_t n4,
+                       int group, int d4) {
+    if (hdr->status != GDN_OK) return;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n4; i += int64_t(gridDim.x) * 256) {
+        const int64_t row = i / d4;  // (token, q/k head)
+        const int c = int(i % d4);
+        const float4 *src = reinterpret_cast<const float4 *>(part) + row * group * d4 + c;
+        float4 s = __ldcs(src);
+        for (int j = 1; j < group; ++j) {
+            const float4 x = __ldcs(src + int64_t(j) * d4);
+            s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+        }
+        if constexpr (sizeof(T) == 4) {
+            reinterpret_cast<float4 *>(out)[i] = s;
+        } else {
+            const __nv_bfloat162 a = __floats2bfloat162_rn(s.x, s.y), b = __floats2bfloat162_rn(s.z, s.w);
+            reinterpret_cast<uint2 *>(out)[i] = make_uint2(*reinterpret_cast<const uint32_t *>(&a),
+                                                           *reinterpret_cast<const uint32_t *>(&b));
+        }
+    }
+}
+template <typename T>
+__global__ void __launch_bounds__(256)
+decay_group_sum_any_kernel(const DecayHeader *hdr, const float *__restrict__ part, T *__restrict__ out, int64_t n,
+                           int group, int d) {
+    if (hdr->status != GDN_OK) return;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) {
+        const int64_t row = i / d;
+        const float *src = part + row * group * d + i % d;
+        float s = src[0];
+        for (int j = 1; j < group; ++j) s += src[int64_t(j) * d];
+        out[i] = from_f32<T>(s);
+    }
+}
+
+}  // namespace
+
+DecayLayout decay_layout(const gdn_shape_t &s, bool backward) {
+    const int64_t tokens = int64_t(s.batch) * s.seq_len, N = s.num_seqs, hv = s.num_v_heads;
+    // segments are at least max(256, tokens * hv / 148) tokens long, and a cut
+    // sequence is longer than one: it has at most 2 len / L of them
+    const int64_t balanced = balanced_tokens(tokens, s.num_v_heads);
+    const int64_t shortest = std::max<int64_t>(kDecayMinSeg, balanced);
+    DecayLayout L = {};
+    L.max_slots = tokens > kDecayMinSeg ? 2 * tokens / shortest + 1 : 0;
+    L.max_split = tokens > kDecayMinSeg ? tokens / shortest + 1 : 0;
+    L.max_segs = N + L.max_slots;
+    L.max_chunks = (tokens + 63 * N) / kDecayChunk;
+    // checkpoints are `ick` apart, 1024 unless segments are shorter
+    L.max_cks = tokens / (balanced >= kDecayMaxIck ? kDecayMaxIck : kDecayMinSeg) + N;
+    size_t off = 256;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = align256(off + bytes);
+        return at;
+    };
+    L.segs_off = take(size_t(L.max_segs) * sizeof(DecaySeg));
+    L.split_off = take(size_t(L.max_split) * 4);
+    L.order_off = take(size_t(N) * 4);
+    L.cbase_off = take(size_t(N + 1) * 4);
+    L.ckbase_off = take(size_t(N + 1) * 4);
+    L.segdec_off = take(size_t(L.max_slots) * hv * 4);
+    L.state_off[0] = take(size_t(L.max_slots) * hv * 65536);
+    if (backward) {
+        L.state_off[1] = take(size_t(L.max_slots) * hv * 65536);
+        L.ckpt_off = take(size_t(L.max_cks) * hv * 65536);
+        L.zsum_off = take(size_t(L.max_cks) * hv * 4);
+        for (int i = 0; i < 2; ++i) L.dot_off[i] = take(size_t(tokens) * hv * 4);
+        L.intra_off = take(size_t(tokens) * hv * 4);
+        L.dgtok_off = take(size_t(tokens) * hv * 4);
+        if (s.num_v_heads != s.num_qk_heads)
+            for (int i = 0; i < 2; ++i) L.part_off[i] = take(size_t(tokens) * hv * s.head_dim_k * 4);
+    }
+    L.total = off;
+    return L;
+}
+
+DecaySched decay_sched(char *ws, const DecayLayout &L) {
+    DecaySched sc;
+    sc.hdr = reinterpret_cast<DecayHeader *>(ws);
+    sc.segs = reinterpret_cast<DecaySeg *>(ws + L.segs_off);
+    sc.split = reinterpret_cast<int32_t *>(ws + L.split_off);
+    sc.chunk_base = reinterpret_cast<int32_t *>(ws + L.cbase_off);
+    sc.ck_base = reinterpret_cast<int32_t *>(ws + L.ckbase_off);
+    return sc;
+}
+
+cudaError_t launch_decay_schedule(const gdn_shape_t &s, const int32_t *cu, char *ws, const DecayLayout &L,
+                                  cudaStream_t stream) {
+    decay_schedule_kernel<<<1, kSchedThreads, 0, stream>>>(s.num_seqs, s.batch * s.seq_len, cu ? 0 : s.seq_len,
+                                                           s.num_v_heads, cu, decay_sched(ws, L),
+                                                           reinterpret_cast<int32_t *>(ws + L.order_off));
+    count_launch();
+    return cudaGetLastError();
+}
+
+cudaError_t launch_decay_combine(const gdn_shape_t &s, const DecayLayout &L, const DecaySched &sc, float *states,
+                                 const float *seg_dec, const float *s_in, bool s_trans, int dz, int dy, bool reverse,
+                                 cudaStream_t stream) {
+    if (L.max_split == 0) return cudaSuccess;
+    const int hv = s.num_v_heads;
+    const int deep = int(std::min<int64_t>(L.max_split, std::max(1, 64 / hv)));
+    decay_combine_kernel<<<dim3(64, unsigned(hv), unsigned(deep)), 256, 0, stream>>>(sc, states, seg_dec, s_in,
+                                                                                     s_trans, hv, dz, dy, reverse);
+    count_launch();
+    return cudaGetLastError();
+}
+
+cudaError_t launch_decay_dg(const gdn_shape_t &s, const int32_t *cu, const DecayLayout &L, const DecaySched &sc,
+                            const float *dot_q, const float *dot_k, const float *intra, const float *zsum,
+                            const float *g, bool g_const, float *dg_tok, float *dg, cudaStream_t stream) {
+    const int64_t tokens = int64_t(s.batch) * s.seq_len, units = L.max_cks * s.num_v_heads;
+    const unsigned grid = unsigned(std::min<int64_t>((units + 3) / 4, 148 * 16));
+    if (grid > 0) {
+        decay_dg_kernel<<<grid, 128, 0, stream>>>(s.num_seqs, s.num_v_heads, int(tokens), cu, s.seq_len, sc, dot_q,
+                                                  dot_k, intra, zsum, g, g_const, dg_tok, dg);
+        count_launch();
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    if (g_const) {
+        decay_dg_head_kernel<<<unsigned(s.num_v_heads), 512, 0, stream>>>(sc.hdr, dg_tok, int(tokens), dg);
+        count_launch();
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_decay_group_sum(const DecayHeader *hdr, const float *part, void *out, int64_t tokens, int32_t hk,
+                                   int32_t hv, int32_t d, int32_t dtype, cudaStream_t stream) {
+    const int64_t n = tokens * hk * d;
+    if (n == 0) return cudaSuccess;
+    const int group = hv / hk;
+    const bool by4 = d % 4 == 0;
+    const int64_t items = by4 ? n / 4 : n;
+    const unsigned grid = unsigned(std::min<int64_t>((items + 255) / 256, 148 * 8));
+    using bf = __nv_bfloat16;
+    if (by4 && dtype == GDN_DTYPE_BF16)
+        decay_group_sum_kernel<bf><<<grid, 256, 0, stream>>>(hdr, part, static_cast<bf *>(out), items, group, d / 4);
+    else if (by4)
+        decay_group_sum_kernel<float><<<grid, 256, 0, stream>>>(hdr, part, static_cast<float *>(out), items, group,
+                                                                  d / 4);
+    else if (dtype == GDN_DTYPE_BF16)
+        decay_group_sum_any_kernel<bf><<<grid, 256, 0, stream>>>(hdr, part, static_cast<bf *>(out), items, group, d);
+    else
+        decay_group_sum_any_kernel<float><<<grid, 256, 0, stream>>>(hdr, part, static_cast<float *>(out), items, group, d);
+    count_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace gdn

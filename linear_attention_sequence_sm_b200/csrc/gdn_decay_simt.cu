@@ -1,0 +1,450 @@
+// gdn_decay_simt.cu -- the decayed linear attention's pass on CUDA cores:
+// fp32 or bf16 storage, any head sizes up to 128, all arithmetic in fp32
+// (differences of prefix sums in 64 bits).
+//
+// One block of 256 threads walks a segment for one value head, 64 tokens at a
+// time, with the state (dz x dy) in shared memory.  Per chunk: P = decay mask
+// . (x y^T) as 4 x 4 register tiles, out = P z + decay . (x Sigma^T) as 4 x 8
+// tiles, Sigma = e^G Sigma + z^T (w y) as 8 x 8 tiles.  Shared-memory reads
+// are 16 bytes; rows are padded by 4 floats so that a quarter-warp's rows fall
+// into different banks.
+#include <algorithm>
+
+#include "gdn_decay.cuh"
+
+namespace gdn {
+
+namespace {
+
+constexpr int C = kDecayChunk;
+constexpr int kThreads = 256;
+constexpr int LD = 132;   // row pitch of 128-wide tiles (floats)
+constexpr int LP = 68;    // row pitch of the 64 x 64 mask tile
+
+struct SimtSmem {
+    float x[C * LD], y[C * LD], z[C * LD];
+    float S[128 * LD];
+    float p[C * LP];
+    double G[C];
+    float w_in[C], w_st[C];
+    float red[kThreads / 32];
+    float gamma;
+};
+
+// rows [0, L) of a [tokens, heads, d] tensor's head into a tile, the rest of
+// the 64 rows and of the columns up to a multiple of 8 zero
+template <typename T>
+__device__ void load_tile(float *dst, const T *src, size_t stride, int d, int L, int dpad) {
+    if (d % 4 == 0) {
+        const int n4 = dpad / 4;
+        for (int e = threadIdx.x; e < C * n4; e += kThreads) {
+            const int r = e / n4, c = 4 * (e % n4);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < L && c < d) {
+                if constexpr (sizeof(T) == 4) {
+                    v = *reinterpret_cast<const float4 *>(src + r * stride + c);
+                } else {
+                    const uint2 u = *reinterpret_cast<const uint2 *>(src + r * stride + c);
+                    v = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                                    __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+                }
+            }
+            *reinterpret_cast<float4 *>(dst + r * LD + c) = v;
+        }
+    } else {
+        for (int e = threadIdx.x; e < C * dpad; e += kThreads) {
+            const int r = e / dpad, c = e % dpad;
+            dst[r * LD + c] = (r < L && c < d) ? to_f32(src[r * stride + c]) : 0.f;
+        }
+    }
+}
+
+// Prefix sums of a chunk's floored log-decays (warp 0), and the weights.
+__device__ void load_gates(SimtSmem &sm, const float *g, size_t g_stride, int L, bool reverse) {
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        const float g0 = 2 * lane < L ? fmaxf(g[(2 * lane) * g_stride], kGFloor) : 0.f;
+        const float g1 = 2 * lane + 1 < L ? fmaxf(g[(2 * lane + 1) * g_stride], kGFloor) : 0.f;
+        double s = double(g0) + double(g1);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const double a = __shfl_up_sync(0xffffffffu, s, d);
+            if (lane >= d) s += a;
+        }
+        const double last = __shfl_sync(0xffffffffu, s, 31);
+        const double G0 = s - double(g1), G1 = s;
+        sm.G[2 * lane] = G0;
+        sm.G[2 * lane + 1] = G1;
+        const float a0 = expf(float(G0)), a1 = expf(float(G1));
+        const float b0 = expf(float(last - G0)), b1 = expf(float(last - G1));
+        sm.w_in[2 * lane] = reverse ? b0 : a0;
+        sm.w_in[2 * lane + 1] = reverse ? b1 : a1;
+        sm.w_st[2 * lane] = reverse ? a0 : b0;
+        sm.w_st[2 * lane + 1] = reverse ? a1 : b1;
+        if (lane == 0) sm.gamma = expf(float(last));
+    }
+}
+
+__device__ __forceinline__ float dot4(const float4 &a, const float4 &b, float c) {
+    return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
+}
+__device__ __forceinline__ float4 ld4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+
+// 4 x 4 tile of a 64 x 64 product of rows: acc[i][j] = a[r0 + 16 i] . b[c0 + 16 j]
+__device__ __forceinline__ void gram(float (&acc)[4][4], const float *a, const float *b, int r0, int c0, int d) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    for (int k = 0; k < d; k += 4) {
+        float4 u[4], v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[i] = ld4(a + (r0 + 16 * i) * LD + k);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = ld4(b + (c0 + 16 * j) * LD + k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = dot4(u[i], v[j], acc[i][j]);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+decay_pass_simt_kernel(const DecayPass a) {
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    SimtSmem &sm = *reinterpret_cast<SimtSmem *>(smem_raw);
+    const DecayHeader *hdr = a.sched.hdr;
+    if (hdr->status != GDN_OK) return;
+    const int tid = threadIdx.x, rg = tid >> 4, cg = tid & 15;
+    const int dy = a.dy, dz = a.dz, hv = a.hv;
+    const int dyp = (dy + 7) & ~7, dzp = (dz + 7) & ~7;
+    const int64_t units = int64_t(hdr->num_segs) * hv;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const DecaySeg seg = a.sched.segs[u / hv];
+        const int h = int(u % hv);
+        const bool first = a.reverse ? seg.pos + seg.len == seg.seq_len : seg.pos == 0;
+        const bool last = a.reverse ? seg.pos == 0 : seg.pos + seg.len == seg.seq_len;
+        if (a.state_only && (seg.slot < 0 || last)) continue;
+        const T *x = static_cast<const T *>(a.x) + (size_t(seg.start) * a.hx + h / (hv / a.hx)) * dy;
+        const T *y = static_cast<const T *>(a.y) + (size_t(seg.start) * a.hy + h / (hv / a.hy)) * dy;
+        const T *z = static_cast<const T *>(a.z) + (size_t(seg.start) * a.hz + h / (hv / a.hz)) * dz;
+        const T *aux = a.aux ? static_cast<const T *>(a.aux) + (size_t(seg.start) * a.haux + h / (hv / a.haux)) * dz
+                             : nullptr;
+        const float *g = a.g_const ? a.g + h : a.g + size_t(seg.start) * hv + h;
+        const size_t gs = a.g_const ? 0 : hv;
+        // start state
+        const bool own = seg.slot >= 0 && !a.state_only;
+        const float *src = own ? a.seg_state + (size_t(seg.slot) * hv + h) * 16384
+                               : (a.s_in && first && !a.state_only) ? a.s_in + (size_t(seg.seq) * hv + h) * dz * dy : nullptr;
+        __syncthreads();
+        for (int e = tid; e < dzp * dyp; e += kThreads) {
+            const int r = e / dyp, c = e % dyp;
+            float v = 0.f;
+            if (src && r < dz && c < dy)
+                v = own ? src[a.seg_trans ? c * 128 + r : r * 128 + c] : src[a.s_trans ? c * dz + r : r * dy + c];
+            sm.S[r * LD + c] = v;
+        }
+        const int nch = (seg.len + C - 1) / C;
+        float seg_sum = 0.f;
+        for (int i = 0; i < nch; ++i) {
+            const int n = a.reverse ? nch - 1 - i : i;
+            const int t0 = n * C, L = min(C, seg.len - t0);
+            __syncthreads();
+            load_tile(sm.y, y + size_t(t0) * a.hy * dy, size_t(a.hy) * dy, dy, L, dyp);
+            load_tile(sm.z, z + size_t(t0) * a.hz * dz, size_t(a.hz) * dz, dz, L, dzp);
+            if (!a.state_only) load_tile(sm.x, x + size_t(t0) * a.hx * dy, size_t(a.hx) * dy, dy, L, dyp);
+            load_gates(sm, g + size_t(t0) * gs, gs, L, a.reverse);
+            __syncthreads();
+            seg_sum += float(sm.G[C - 1]);
+            if (a.ckpt && !a.zsum && seg.pos + t0 > 0 && (seg.pos + t0) % hdr->ick == 0) {
+                float *dst = a.ckpt + (size_t(seg.ck + (seg.pos + t0) / hdr->ick) * hv + h) * 16384;
+                for (int q = tid; q < dz * dy; q += kThreads) dst[q] = sm.S[(q / dy) * LD + q % dy];
+            }
+            if (!a.state_only) {
+                {
+                    float acc[4][4];
+                    gram(acc, sm.x, sm.y, rg, cg, dyp);
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int r = rg + 16 * p, c = cg + 16 * q;
+                            const bool in = a.reverse ? c >= r : c <= r;
+                            const double d = a.reverse ? sm.G[c] - sm.G[r] : sm.G[r] - sm.G[c];
+                            sm.p[r * LP + c] = in ? acc[p][q] * expf(float(d)) : 0.f;
+                        }
+                }
+                __syncthreads();
+                // out rows 4 rg .. 4 rg + 3, columns 4 cg .. and 64 + 4 cg ..
+                float in[4][8], ex[4][8];
+#pragma unroll
+                for (int p = 0; p < 4; ++p)
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) in[p][q] = ex[p][q] = 0.f;
+                const bool hi = 64 + 4 * cg < dzp, lo = 4 * cg < dzp;
+                if (lo) {
+                    for (int c = 0; c < C; c += 4) {
+                        float4 pr[4];
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) pr[p] = ld4(sm.p + (4 * rg + p) * LP + c);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float4 z0 = ld4(sm.z + (c + e) * LD + 4 * cg);
+                            const float4 z1 = hi ? ld4(sm.z + (c + e) * LD + 64 + 4 * cg) : make_float4(0, 0, 0, 0);
+#pragma unroll
+                            for (int p = 0; p < 4; ++p) {
+                                const float w = e == 0 ? pr[p].x : e == 1 ? pr[p].y : e == 2 ? pr[p].z : pr[p].w;
+                                in[p][0] = fmaf(w, z0.x, in[p][0]); in[p][1] = fmaf(w, z0.y, in[p][1]);
+                                in[p][2] = fmaf(w, z0.z, in[p][2]); in[p][3] = fmaf(w, z0.w, in[p][3]);
+                                in[p][4] = fmaf(w, z1.x, in[p][4]); in[p][5] = fmaf(w, z1.y, in[p][5]);
+                                in[p][6] = fmaf(w, z1.z, in[p][6]); in[p][7] = fmaf(w, z1.w, in[p][7]);
+                            }
+                        }
+                    }
+                    for (int k = 0; k < dyp; k += 4) {
+                        float4 xr[4];
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) xr[p] = ld4(sm.x + (4 * rg + p) * LD + k);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            if (q >= 4 && !hi) break;
+                            const float4 s = ld4(sm.S + ((q < 4 ? 0 : 64) + 4 * cg + (q & 3)) * LD + k);
+#pragma unroll
+                            for (int p = 0; p < 4; ++p) ex[p][q] = dot4(xr[p], s, ex[p][q]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const int r = 4 * rg + p;
+                    const float w = sm.w_in[r];
+                    const size_t row = size_t(seg.start + t0 + r);
+                    float dot = 0.f;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const int c = (q < 4 ? 0 : 64) + 4 * cg + (q & 3);
+                        const float e = w * ex[p][q];
+                        if (r < L && c < dz) {
+                            const size_t at = (row * hv + h) * dz + c;
+                            if (a.out_f32) static_cast<float *>(a.out)[at] = in[p][q] + e;
+                            else static_cast<T *>(a.out)[at] = from_f32<T>(in[p][q] + e);
+                            if (aux) dot = fmaf(to_f32(aux[(size_t(t0) + r) * a.haux * dz + c]), e, dot);
+                        }
+                    }
+                    if (aux) {
+#pragma unroll
+                        for (int m = 8; m > 0; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+                        if (cg == 0 && r < L) a.dot[size_t(h) * a.tokens + row] = dot;
+                    }
+                }
+                __syncthreads();
+            }
+            // Sigma = gamma Sigma + z^T (w y): z rows 4 rg (and 64 +), y columns 4 cg (and 64 +)
+            for (int zb = 4 * rg; zb < dzp; zb += 64)
+                for (int yb = 4 * cg; yb < dyp; yb += 64) {
+                    float acc[4][4];
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        const float4 s = ld4(sm.S + (zb + p) * LD + yb);
+                        acc[p][0] = sm.gamma * s.x; acc[p][1] = sm.gamma * s.y;
+                        acc[p][2] = sm.gamma * s.z; acc[p][3] = sm.gamma * s.w;
+                    }
+                    for (int c = 0; c < L; ++c) {
+                        const float w = sm.w_st[c];
+                        const float4 zv = ld4(sm.z + c * LD + zb), yv = ld4(sm.y + c * LD + yb);
+                        const float zw[4] = {w * zv.x, w * zv.y, w * zv.z, w * zv.w};
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) {
+                            acc[p][0] = fmaf(zw[p], yv.x, acc[p][0]); acc[p][1] = fmaf(zw[p], yv.y, acc[p][1]);
+                            acc[p][2] = fmaf(zw[p], yv.z, acc[p][2]); acc[p][3] = fmaf(zw[p], yv.w, acc[p][3]);
+                        }
+                    }
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+                        *reinterpret_cast<float4 *>(sm.S + (zb + p) * LD + yb) =
+                            make_float4(acc[p][0], acc[p][1], acc[p][2], acc[p][3]);
+                }
+            if (a.zsum && (seg.pos + t0) % hdr->ick == 0) {
+                // <Sigma, checkpoint> at the chunk's start
+                const int slot = seg.ck + (seg.pos + t0) / hdr->ick;
+                const bool start = seg.pos + t0 == 0;
+                const float *cp = start ? (a.s_first ? a.s_first + (size_t(seg.seq) * hv + h) * dz * dy : nullptr)
+                                        : a.ckpt + (size_t(slot) * hv + h) * 16384;
+                __syncthreads();
+                float s = 0.f;
+                if (cp)
+                    for (int q = tid; q < dz * dy; q += kThreads) {
+                        const bool tr = start && a.s_trans;
+                        s = fmaf(cp[q], sm.S[(tr ? q % dz : q / dy) * LD + (tr ? q / dz : q % dy)], s);
+                    }
+#pragma unroll
+                for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+                if ((tid & 31) == 0) sm.red[tid >> 5] = s;
+                __syncthreads();
+                if (tid == 0) {
+                    s = 0.f;
+                    for (int w = 0; w < kThreads / 32; ++w) s += sm.red[w];
+                    a.zsum[size_t(slot) * hv + h] = s;
+                }
+            }
+        }
+        __syncthreads();
+        if (a.state_only) {
+            float *dst = a.seg_local + (size_t(seg.slot) * hv + h) * 16384;
+            for (int e = tid; e < dz * dy; e += kThreads) dst[(e / dy) * 128 + e % dy] = sm.S[(e / dy) * LD + e % dy];
+            if (tid == 0) a.seg_dec[size_t(seg.slot) * hv + h] = expf(seg_sum);
+            continue;
+        }
+        if (last && a.s_out) {
+            float *dst = a.s_out + (size_t(seg.seq) * hv + h) * dz * dy;
+            for (int e = tid; e < dz * dy; e += kThreads) {
+                const int r = a.s_trans ? e % dz : e / dy, c = a.s_trans ? e / dz : e % dy;
+                dst[e] = sm.S[r * LD + c];
+            }
+        }
+    }
+}
+
+// The pairs inside one chunk: intra_t = sum of W_ij over j < t <= i,
+// W_ij = e^{G_i - G_j} (q_i . k_j) (do_i . v_j).  Row i's running sums over j
+// give X_i,t = sum_{j < t} W_ij; column t then sums X_i,t over i >= t.
+struct IntraSmem {
+    float q[C * LD], k[C * LD], v[C * LD], o[C * LD];
+    float w[C * LP];
+    float part[4 * C];
+    double G[C];
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+decay_intra_simt_kernel(const DecaySched sc, int num_seqs, int hk, int hv, int dk, int dv, int tokens, int batched_len,
+                        const int32_t *__restrict__ cu, const T *__restrict__ q, const T *__restrict__ k,
+                        const T *__restrict__ v, const T *__restrict__ d_o, const float *__restrict__ g, int g_const,
+                        float *__restrict__ intra) {
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    IntraSmem &sm = *reinterpret_cast<IntraSmem *>(smem_raw);
+    if (sc.hdr->status != GDN_OK) return;
+    const int tid = threadIdx.x, rg = tid >> 4, cg = tid & 15;
+    const int dkp = (dk + 7) & ~7, dvp = (dv + 7) & ~7;
+    const int64_t units = int64_t(sc.hdr->total_chunks) * hv;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int gc = int(u / hv), h = int(u % hv), hq = h / (hv / hk);
+        const int n = chunk_sequence(sc.chunk_base, num_seqs, gc);
+        const int start = cu ? cu[n] : n * batched_len, len = cu ? cu[n + 1] - cu[n] : batched_len;
+        const int t0 = (gc - sc.chunk_base[n]) * C, L = min(C, len - t0);
+        const size_t tok = size_t(start) + t0;
+        __syncthreads();
+        load_tile(sm.q, q + (tok * hk + hq) * dk, size_t(hk) * dk, dk, L, dkp);
+        load_tile(sm.k, k + (tok * hk + hq) * dk, size_t(hk) * dk, dk, L, dkp);
+        load_tile(sm.v, v + (tok * hv + h) * dv, size_t(hv) * dv, dv, L, dvp);
+        load_tile(sm.o, d_o + (tok * hv + h) * dv, size_t(hv) * dv, dv, L, dvp);
+        if (tid < 32) {
+            const float *gp = g_const ? g + h : g + tok * hv + h;
+            const size_t gs = g_const ? 0 : hv;
+            const float g0 = 2 * tid < L ? fmaxf(gp[(2 * tid) * gs], kGFloor) : 0.f;
+            const float g1 = 2 * tid + 1 < L ? fmaxf(gp[(2 * tid + 1) * gs], kGFloor) : 0.f;
+            double s = double(g0) + double(g1);
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const double e = __shfl_up_sync(0xffffffffu, s, d);
+                if (tid >= d) s += e;
+            }
+            sm.G[2 * tid] = s - double(g1);
+            sm.G[2 * tid + 1] = s;
+        }
+        __syncthreads();
+        {
+            float A[4][4], B[4][4];
+            gram(A, sm.q, sm.k, rg, cg, dkp);
+            gram(B, sm.o, sm.v, rg, cg, dvp);
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = rg + 16 * p, c = cg + 16 * e;
+                    sm.w[r * LP + c] = c < r ? A[p][e] * B[p][e] * expf(float(sm.G[r] - sm.G[c])) : 0.f;
+                }
+        }
+        __syncthreads();
+        {
+            // thread: row tid / 4, columns 16 (tid % 4) ..; exclusive running sums of the row
+            const int r = tid >> 2, c0 = 16 * (tid & 3);
+            float x[16], run = 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                x[e] = run;
+                run += sm.w[r * LP + c0 + e];
+            }
+            float before = 0.f;
+#pragma unroll
+            for (int m = 0; m < 3; ++m) {
+                const float o = __shfl_sync(0xffffffffu, run, (tid & 28) + m);
+                if ((tid & 3) > m) before += o;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sm.w[r * LP + c0 + e] = x[e] + before;
+        }
+        __syncthreads();
+        {
+            const int t = tid & 63, quarter = tid >> 6;
+            float s = 0.f;
+            for (int r = max(16 * quarter, t); r < 16 * quarter + 16; ++r) s += sm.w[r * LP + t];
+            sm.part[quarter * C + t] = s;
+        }
+        __syncthreads();
+        if (tid < L)
+            intra[size_t(h) * tokens + tok + tid] =
+                (sm.part[tid] + sm.part[C + tid]) + (sm.part[2 * C + tid] + sm.part[3 * C + tid]);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_decay_pass_simt(const DecayPass &p, int32_t dtype, int64_t max_units, cudaStream_t stream) {
+    if (max_units <= 0) return cudaSuccess;
+    const void *kern = dtype == GDN_DTYPE_BF16 ? reinterpret_cast<const void *>(decay_pass_simt_kernel<__nv_bfloat16>)
+                                               : reinterpret_cast<const void *>(decay_pass_simt_kernel<float>);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(SimtSmem)));
+    if (e != cudaSuccess) return e;
+    const unsigned grid = unsigned(std::min<int64_t>(max_units, kDecayPlanSms * 8));
+    if (dtype == GDN_DTYPE_BF16)
+        decay_pass_simt_kernel<__nv_bfloat16><<<grid, kThreads, sizeof(SimtSmem), stream>>>(p);
+    else
+        decay_pass_simt_kernel<float><<<grid, kThreads, sizeof(SimtSmem), stream>>>(p);
+    count_launch();
+    return cudaGetLastError();
+}
+
+cudaError_t launch_decay_intra_simt(const gdn_shape_t &s, const int32_t *cu, const DecayLayout &L, const DecaySched &sc,
+                                    const void *q, const void *k, const void *v, const void *d_o, const float *g,
+                                    bool g_const, float *intra, cudaStream_t stream) {
+    const int64_t units = L.max_chunks * s.num_v_heads;
+    if (units <= 0) return cudaSuccess;
+    const int tokens = s.batch * s.seq_len;
+    const unsigned grid = unsigned(std::min<int64_t>(units, kDecayPlanSms * 8));
+    cudaError_t e;
+    if (s.dtype == GDN_DTYPE_BF16) {
+        using bf = __nv_bfloat16;
+        e = cudaFuncSetAttribute(decay_intra_simt_kernel<bf>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 int(sizeof(IntraSmem)));
+        if (e != cudaSuccess) return e;
+        decay_intra_simt_kernel<bf><<<grid, kThreads, sizeof(IntraSmem), stream>>>(
+            sc, s.num_seqs, s.num_qk_heads, s.num_v_heads, s.head_dim_k, s.head_dim_v, tokens, s.seq_len, cu,
+            static_cast<const bf *>(q), static_cast<const bf *>(k), static_cast<const bf *>(v),
+            static_cast<const bf *>(d_o), g, g_const, intra);
+    } else {
+        e = cudaFuncSetAttribute(decay_intra_simt_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 int(sizeof(IntraSmem)));
+        if (e != cudaSuccess) return e;
+        decay_intra_simt_kernel<float><<<grid, kThreads, sizeof(IntraSmem), stream>>>(
+            sc, s.num_seqs, s.num_qk_heads, s.num_v_heads, s.head_dim_k, s.head_dim_v, tokens, s.seq_len, cu,
+            static_cast<const float *>(q), static_cast<const float *>(k), static_cast<const float *>(v),
+            static_cast<const float *>(d_o), g, g_const, intra);
+    }
+    count_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace gdn

@@ -147,6 +147,19 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
 // (defined in gdn_api.cu) and returns `st`.
 gdn_status_t set_error(gdn_status_t st, const char *text);
 
+// Argument checks shared by the entry points (defined in gdn_api.cu): format
+// an error text and return its status, clear the text, describe a CUDA error,
+// test 16-byte alignment, the current device's SM count (-1 without one), the
+// checks of a shape, and of an output side with its form for the kernels.
+struct OutSide;
+gdn_status_t fail(gdn_status_t st, const char *fmt, ...);
+void clear_error();
+gdn_status_t cuda_fail(cudaError_t e, const char *what);
+bool aligned16(const void *p);
+int device_sm_count(int *major);
+gdn_status_t check_shape(const gdn_shape_t *s);
+gdn_status_t check_output_side(const gdn_output_side_t *os, OutSide *out);
+
 // Launch counter (defined in gdn_api.cu).
 void count_launch();
 

@@ -39,13 +39,23 @@ GDN_OUT_GATE_SIGMOID = 2
 GDN_OUT_ZERO_CENTRED = 4
 GDN_OUT_WEIGHT_PER_HEAD = 8
 GDN_CONV_SILU = 1
+GDN_DECAY_PER_TOKEN = 0
+GDN_DECAY_PER_HEAD = 1
+GDN_BLOCK_POST_NORM = 1
+GDN_BLOCK_PRE_NORM = 2
+GDN_BLOCK_GATE_SILU = 4
+GDN_BLOCK_GATE_SIGMOID = 8
+GDN_BLOCK_ZERO_CENTRED = 16
 
 EXPORTED = ("gdn_chunk_forward_workspace_size", "gdn_chunk_forward", "gdn_read_device_status",
             "gdn_decode_step", "gdn_status_string", "gdn_last_error_message", "gdn_launch_count",
             "gdn_chunk_forward_noalloc", "gdn_decode_step_ex", "gdn_chunk_forward_out", "gdn_decode_step_out",
             "gdn_kda_forward", "gdn_kda_decode_step", "gdn_decode_multi", "gdn_decode_commit",
             "gdn_chunk_backward_workspace_size", "gdn_chunk_backward", "gdn_short_conv",
-            "gdn_chunk_forward_path", "gdn_noalloc_read_device_status", "gdn_kda_forward_workspace_size")
+            "gdn_chunk_forward_path", "gdn_noalloc_read_device_status", "gdn_kda_forward_workspace_size",
+            "gdn_decay_forward_workspace_size", "gdn_decay_forward", "gdn_decay_decode_step",
+            "gdn_decay_backward_workspace_size", "gdn_decay_backward", "gdn_block_norm_forward",
+            "gdn_block_norm_backward_workspace_size", "gdn_block_norm_backward")
 GDN_PATH_SIMT = 0
 GDN_PATH_TC_ONE_KERNEL = 1
 GDN_PATH_TC_SPLIT = 2
@@ -67,6 +77,12 @@ class Shape(ctypes.Structure):
 
 class OutputSideC(ctypes.Structure):
     _fields_ = [("weight", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("flags", ctypes.c_uint32)]
+
+
+class BlockNormC(ctypes.Structure):
+    _fields_ = [("post_weight", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("pre_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float), ("branch_scale", ctypes.c_float),
                 ("flags", ctypes.c_uint32)]
 
 
@@ -117,6 +133,24 @@ def _load(path: str = LIB_PATH):
     lib.gdn_short_conv.argtypes = [i32, i32, vp, ctypes.c_int64, i32, i32, i32, vp, vp, vp, vp, vp,
                                    ctypes.c_uint32, vp]
     lib.gdn_short_conv.restype = st
+    szp = ctypes.POINTER(ctypes.c_size_t)
+    for name in ("gdn_decay_forward_workspace_size", "gdn_decay_backward_workspace_size"):
+        getattr(lib, name).argtypes = [ctypes.POINTER(Shape), szp]
+        getattr(lib, name).restype = st
+    lib.gdn_decay_forward.argtypes = [ctypes.POINTER(Shape), vp, vp, vp, vp, i32, vp, vp, osp, vp, vp, vp,
+                                      ctypes.c_size_t, vp]
+    lib.gdn_decay_forward.restype = st
+    lib.gdn_decay_decode_step.argtypes = [i32] * 6 + [vp] * 4 + [i32, vp, osp, vp, vp]
+    lib.gdn_decay_decode_step.restype = st
+    lib.gdn_decay_backward.argtypes = [ctypes.POINTER(Shape), vp, vp, vp, vp, i32] + [vp] * 10 + [ctypes.c_size_t, vp]
+    lib.gdn_decay_backward.restype = st
+    bnp, i64 = ctypes.POINTER(BlockNormC), ctypes.c_int64
+    lib.gdn_block_norm_forward.argtypes = [i64, i32, i32, i32, vp, vp, vp, bnp, vp, vp, vp]
+    lib.gdn_block_norm_forward.restype = st
+    lib.gdn_block_norm_backward_workspace_size.argtypes = [i64, i32, szp]
+    lib.gdn_block_norm_backward_workspace_size.restype = st
+    lib.gdn_block_norm_backward.argtypes = [i64, i32, i32, i32, vp, vp, vp, bnp] + [vp] * 9 + [ctypes.c_size_t, vp]
+    lib.gdn_block_norm_backward.restype = st
     lib.gdn_status_string.argtypes = [st]
     lib.gdn_status_string.restype = ctypes.c_char_p
     lib.gdn_last_error_message.argtypes = []
@@ -642,6 +676,244 @@ def short_conv(x, weight, cu_seqlens=None, state=None, silu=True, out=None, stat
                                   _ptr(x), _ptr(weight), _ptr(state), _ptr(state_out), _ptr(out),
                                   GDN_CONV_SILU if silu else 0, _stream_handle(stream, dev)))
     return out, state_out
+
+
+def _decay_layout(g, per_token):
+    """GDN_DECAY_PER_HEAD for g [Hv], GDN_DECAY_PER_TOKEN for g shaped
+    ``per_token``; any other shape is an error."""
+    if g.dim() == 1 and len(per_token) > 1:
+        _expect(g, "g", per_token[-1:])
+        return GDN_DECAY_PER_HEAD
+    _expect(g, "g", per_token)
+    return GDN_DECAY_PER_TOKEN
+
+
+def _decay_prefill_shapes(q, k, v, g, initial_state, cu_seqlens):
+    """Shape checks of the decayed linear attention's prefill and backward:
+    _prefill_shapes, with g [..., Hv] or [Hv] and no beta."""
+    full = torch.empty(v.shape[:-1], device="meta")  # stands in for beta, which there is none of
+    n_seqs, hv, dv, dk = _prefill_shapes(q, k, v, full, full, initial_state, cu_seqlens)
+    return n_seqs, hv, dv, dk, _decay_layout(g, tuple(v.shape[:-1]))
+
+
+def decay_forward(q, k, v, g, initial_state=None, cu_seqlens=None, output_final_state=True, out=None,
+                  final_state=None, workspace=None, stream=None, output_norm: OutputNorm | None = None,
+                  force_simt=False):
+    """Linear attention with a decay for each value head, prefill:
+    S_t = e^{g_t} S_{t-1} + v_t k_t^T, o_t = S_t q_t.  Returns (o,
+    final_state or None).  q, k [B, T, Hk, d_k], v [B, T, Hv, d_v] (or packed
+    [T, ...] with ``cu_seqlens``); g fp32, one log-decay per token and head
+    ([B, T, Hv]) or per head ([Hv]).  The other arguments are as for
+    chunk_forward; nothing is normalised inside."""
+    n_seqs, hv, dv, dk, layout = _decay_prefill_shapes(q, k, v, g, initial_state, cu_seqlens)
+    _expect(out, "out", v.shape)
+    _expect(final_state, "final_state", (n_seqs, hv, dv, dk))
+    dev, dt = q.device, q.dtype
+    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+        _need(t, n, dt, dev)
+    _need(g, "g", torch.float32, dev)
+    _need(initial_state, "initial_state", torch.float32, dev)
+    _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
+    shape = make_shape(q, v, cu_seqlens, 64, force_simt)
+    if out is None:
+        out = torch.empty(v.shape, dtype=dt, device=dev)
+    _need(out, "out", dt, dev)
+    if final_state is None and output_final_state:
+        final_state = torch.empty((n_seqs, hv, dv, dk), dtype=torch.float32, device=dev)
+    _need(final_state, "final_state", torch.float32, dev)
+    nbytes = decay_workspace_size(shape)
+    if workspace is None or workspace.numel() < nbytes:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    osc = output_norm.c_struct(out) if output_norm is not None else None
+    with torch.cuda.device(dev):  # the library launches on the current device
+        _check(LIB.gdn_decay_forward(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), layout,
+                                     _ptr(initial_state), _ptr(cu_seqlens), None if osc is None else ctypes.byref(osc),
+                                     _ptr(out), _ptr(final_state), _ptr(workspace), workspace.numel(),
+                                     _stream_handle(stream, dev)))
+    return out, final_state
+
+
+def decay_workspace_size(shape: Shape, backward=False) -> int:
+    """Bytes of workspace gdn_decay_forward (or gdn_decay_backward) needs."""
+    n = ctypes.c_size_t(0)
+    fn = LIB.gdn_decay_backward_workspace_size if backward else LIB.gdn_decay_forward_workspace_size
+    _check(fn(ctypes.byref(shape), ctypes.byref(n)))
+    return n.value
+
+
+def decay_decode_step(q, k, v, g, state, out=None, stream=None, output_norm: OutputNorm | None = None):
+    """One token per sequence of the decayed linear attention: q, k
+    [N, Hk, d_k], v [N, Hv, d_v], g [N, Hv] or [Hv] fp32; ``state``
+    [N, Hv, d_v, d_k] fp32 is updated in place.  Returns o [N, Hv, d_v]."""
+    full = torch.empty(v.shape[:-1], device="meta")
+    _decode_shapes(q, k, v, full, full, state)
+    layout = _decay_layout(g, tuple(v.shape[:-1]))
+    _expect(out, "out", v.shape)
+    dev, dt = q.device, q.dtype
+    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+        _need(t, n, dt, dev)
+    _need(g, "g", torch.float32, dev)
+    _need(state, "state", torch.float32, dev)
+    if out is None:
+        out = torch.empty(v.shape, dtype=dt, device=dev)
+    _need(out, "out", dt, dev)
+    N, hk, dk = q.shape
+    hv, dv = v.shape[1], v.shape[2]
+    osc = output_norm.c_struct(out) if output_norm is not None else None
+    with torch.cuda.device(dev):  # the library launches on the current device
+        _check(LIB.gdn_decay_decode_step(N, hk, hv, dk, dv, _dtype_code(q), _ptr(q), _ptr(k), _ptr(v), _ptr(g), layout,
+                                         _ptr(state), None if osc is None else ctypes.byref(osc), _ptr(out),
+                                         _stream_handle(stream, dev)))
+    return out
+
+
+def decay_backward(q, k, v, g, d_o, d_final_state=None, initial_state=None, cu_seqlens=None, want_dg=True,
+                   want_d_initial_state=True, workspace=None, stream=None, force_simt=False):
+    """Gradients of sum d_o . o + sum d_final_state . S_final for
+    decay_forward.  Returns a dict: dq, dk (shaped and typed like q), dv (like
+    v), dg (like g, fp32; None without ``want_dg``, for decays that are not
+    learned), d_initial_state ([N, Hv, d_v, d_k] fp32, or None)."""
+    n_seqs, hv, dv, dk, layout = _decay_prefill_shapes(q, k, v, g, initial_state, cu_seqlens)
+    _expect(d_o, "d_o", v.shape)
+    _expect(d_final_state, "d_final_state", (n_seqs, hv, dv, dk))
+    dev, dt = q.device, q.dtype
+    for t, n in ((q, "q"), (k, "k"), (v, "v"), (d_o, "d_o")):
+        _need(t, n, dt, dev)
+    _need(g, "g", torch.float32, dev)
+    _need(initial_state, "initial_state", torch.float32, dev)
+    _need(d_final_state, "d_final_state", torch.float32, dev)
+    _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
+    shape = make_shape(q, v, cu_seqlens, 64, force_simt)
+    nbytes = decay_workspace_size(shape, backward=True)
+    if workspace is None or workspace.numel() < nbytes:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    f32 = dict(dtype=torch.float32, device=dev)
+    out = {"dq": torch.empty(q.shape, dtype=dt, device=dev), "dk": torch.empty(k.shape, dtype=dt, device=dev),
+           "dv": torch.empty(v.shape, dtype=dt, device=dev), "dg": torch.empty(g.shape, **f32) if want_dg else None,
+           "d_initial_state": torch.empty((n_seqs, hv, dv, dk), **f32) if want_d_initial_state else None}
+    with torch.cuda.device(dev):  # the library launches on the current device
+        _check(LIB.gdn_decay_backward(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), layout,
+                                      _ptr(initial_state), _ptr(cu_seqlens), _ptr(d_o), _ptr(d_final_state),
+                                      _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dg"]),
+                                      _ptr(out["d_initial_state"]), _ptr(workspace), workspace.numel(),
+                                      _stream_handle(stream, dev)))
+    return out
+
+
+class BlockNorm:
+    """The norms around a block, its residual connection and scales:
+    h = residual_scale * residual + branch_scale * scale * post(x) * act(gate),
+    y = pre(h).
+
+    post_norm, pre_norm    whether post(x) is the RMS norm of x (else x), and
+                           whether there is a y, the RMS norm of h.
+    post_weight, scale, pre_weight
+                           fp32 [width], or None for unit weights; with
+                           ``zero_centred`` the two norms' weights are
+                           offsets from 1.
+    activation             "silu" or "sigmoid" (used with a gate).
+    """
+
+    def __init__(self, post_norm=True, post_weight=None, scale=None, pre_norm=True, pre_weight=None, eps=1e-6,
+                 residual_scale=1.0, branch_scale=1.0, activation="silu", zero_centred=False):
+        if activation not in ("silu", "sigmoid"):
+            raise ValueError(f"activation must be 'silu' or 'sigmoid', got {activation!r}")
+        if post_weight is not None and not post_norm:
+            raise ValueError("post_weight needs post_norm")
+        if pre_weight is not None and not pre_norm:
+            raise ValueError("pre_weight needs pre_norm")
+        self.post_norm, self.post_weight, self.scale = bool(post_norm), post_weight, scale
+        self.pre_norm, self.pre_weight = bool(pre_norm), pre_weight
+        self.eps, self.residual_scale, self.branch_scale = float(eps), float(residual_scale), float(branch_scale)
+        self.activation, self.zero_centred = activation, bool(zero_centred)
+
+    def c_struct(self, x: torch.Tensor, gate) -> BlockNormC:
+        for w, n in ((self.post_weight, "post_weight"), (self.scale, "scale"), (self.pre_weight, "pre_weight")):
+            _expect(w, n, x.shape[-1:])
+            _need(w, n, torch.float32, x.device)
+        flags = ((GDN_BLOCK_POST_NORM if self.post_norm else 0) | (GDN_BLOCK_PRE_NORM if self.pre_norm else 0) |
+                 (GDN_BLOCK_ZERO_CENTRED if self.zero_centred else 0))
+        if gate is not None:
+            flags |= GDN_BLOCK_GATE_SILU if self.activation == "silu" else GDN_BLOCK_GATE_SIGMOID
+        p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        return BlockNormC(p(self.post_weight), p(self.scale), p(self.pre_weight), self.eps, self.residual_scale,
+                          self.branch_scale, flags)
+
+
+def _block_norm_inputs(x, residual, norm, gate, more):
+    """Checks shared by the block norm's two directions; ``more``: (tensor,
+    name, type) of x's shape.  Returns (rows, width, residual type)."""
+    if x.dim() < 1:
+        raise ValueError("x must be [..., width]")
+    rt = x.dtype if residual is None else residual.dtype
+    for t, n, _ in ((residual, "residual", None), (gate, "gate", None), *more):
+        _expect(t, n, x.shape)
+    for w, n in ((norm.post_weight, "post_weight"), (norm.scale, "scale"), (norm.pre_weight, "pre_weight")):
+        _expect(w, n, x.shape[-1:])
+    if rt not in (x.dtype, torch.float32):
+        raise TypeError(f"residual must be {x.dtype} or torch.float32, got {rt}")
+    _need(x, "x", x.dtype, x.device)
+    _need(residual, "residual", rt, x.device)
+    _need(gate, "gate", x.dtype, x.device)
+    for t, n, wide in more:
+        _need(t, n, rt if wide else x.dtype, x.device)
+    width = x.shape[-1]
+    return (x.numel() // width if width else 0), width, rt
+
+
+def block_norm_forward(x, residual, norm: BlockNorm, gate=None, h=None, y=None, stream=None):
+    """h = residual_scale * residual + branch_scale * scale * post(x) *
+    act(gate) and y = pre(h), in one kernel.  x, gate and y are [..., width];
+    residual and h (the residual stream) of the same shape, of x's type or
+    fp32; residual may be None.  ``h`` may be ``residual`` and ``y`` may be
+    ``x`` (in place).  Returns (h, y or None without pre_norm)."""
+    if y is not None and not norm.pre_norm:
+        raise ValueError("y needs pre_norm")
+    rows, width, rt = _block_norm_inputs(x, residual, norm, gate, ((h, "h", True), (y, "y", False)))
+    if h is None:
+        h = torch.empty(x.shape, dtype=rt, device=x.device)
+    if y is None and norm.pre_norm:
+        y = torch.empty_like(x)
+    c = norm.c_struct(x, gate)
+    with torch.cuda.device(x.device):  # the library launches on the current device
+        _check(LIB.gdn_block_norm_forward(rows, width, _dtype_code(x), _dtype_code(h), _ptr(x), _ptr(residual),
+                                          _ptr(gate), ctypes.byref(c), _ptr(h), _ptr(y),
+                                          _stream_handle(stream, x.device)))
+    return h, y
+
+
+def block_norm_workspace_size(rows: int, width: int) -> int:
+    """Bytes of workspace gdn_block_norm_backward needs."""
+    n = ctypes.c_size_t(0)
+    _check(LIB.gdn_block_norm_backward_workspace_size(rows, width, ctypes.byref(n)))
+    return n.value
+
+
+def block_norm_backward(x, residual, norm: BlockNorm, gate=None, d_h=None, d_y=None, workspace=None, stream=None):
+    """Gradients of sum d_h . h + sum d_y . y for block_norm_forward (x and
+    residual as they were before it).  Returns a dict: dx, d_residual, d_gate
+    (None where there is no residual or gate), d_post_weight, d_scale,
+    d_pre_weight (fp32 [width]; None for a weight that is None)."""
+    if d_h is None and d_y is None:
+        raise ValueError("d_h or d_y must be given")
+    if d_y is not None and not norm.pre_norm:
+        raise ValueError("d_y needs pre_norm")
+    rows, width, rt = _block_norm_inputs(x, residual, norm, gate, ((d_h, "d_h", True), (d_y, "d_y", False)))
+    nbytes = block_norm_workspace_size(rows, width)
+    if workspace is None or workspace.numel() < nbytes:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    like = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
+    out = {"dx": torch.empty_like(x), "d_residual": like(residual), "d_gate": like(gate),
+           "d_post_weight": like(norm.post_weight), "d_scale": like(norm.scale), "d_pre_weight": like(norm.pre_weight)}
+    c = norm.c_struct(x, gate)
+    code = GDN_DTYPE_F32 if rt == torch.float32 else GDN_DTYPE_BF16
+    with torch.cuda.device(x.device):  # the library launches on the current device
+        _check(LIB.gdn_block_norm_backward(rows, width, _dtype_code(x), code, _ptr(x), _ptr(residual), _ptr(gate),
+                                           ctypes.byref(c), _ptr(d_h), _ptr(d_y), _ptr(out["dx"]),
+                                           _ptr(out["d_residual"]), _ptr(out["d_gate"]), _ptr(out["d_post_weight"]),
+                                           _ptr(out["d_scale"]), _ptr(out["d_pre_weight"]), _ptr(workspace),
+                                           workspace.numel(), _stream_handle(stream, x.device)))
+    return out
 
 
 def launch_count() -> int:

@@ -1,0 +1,319 @@
+"""The decayed linear attention on the GPU against its recurrence in 64 bits.
+
+Tolerances, relative 2-norms over (sequence, head) slices, counted in half
+steps of the types (fp32: u = 2^-24; bf16: 2^-8).  A token's output sums at
+most 64 + 128 products inside a chunk and a state that came through the
+chunks before it (at most 24 here), each sum within u of its terms: 256 u.
+bf16 outputs add their own rounding and, on the tensor cores, the rounding of
+the masked products and of the state's copy: 3 half steps.  dg adds and takes
+off the one-ended sums of up to 16 chunks on each side, each within 256 u of
+sums no larger than the slice: 32 * 256 u."""
+import pytest
+import torch
+
+import decay_ref as R
+
+pytestmark = pytest.mark.gpu
+
+F32 = 256 * R.U32
+BF16 = 3 * 2.0 ** -8
+DG = 32 * 256 * R.U32
+
+SHAPES = [  # hk, hv, dk, dv
+    (1, 1, 128, 128), (2, 4, 128, 128), (1, 3, 64, 64), (2, 2, 40, 72), (1, 2, 128, 64), (1, 2, 24, 128),
+    (2, 2, 33, 17), (1, 1, 1, 1),
+]
+LENGTHS = [dict(batch=(1, 1)), dict(batch=(2, 64)), dict(batch=(1, 65)), dict(lens=[63, 0, 130, 1]),
+           dict(lens=[0, 0]), dict(batch=(3, 191)), dict(lens=[700, 5])]
+
+
+def dtypes(f):
+    return pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])(f)
+
+
+def run_forward(d, **kw):
+    from linear_attention_sequence_sm_b200 import gdn
+    c = R.cuda(d)
+    out = gdn.decay_forward(c["q"], c["k"], c["v"], c["g"], initial_state=c["s0"], cu_seqlens=c["cu"], **kw)
+    torch.cuda.synchronize()
+    return out
+
+
+def check_forward(d, o, sf):
+    lens = R.lens_of(d["q"], d["cu"])
+    ro, rs = R.forward(d["q"], d["k"], d["v"], d["g"], d["s0"], d["cu"])
+    bar = BF16 if d["q"].dtype == torch.bfloat16 else F32
+    assert R.worst(o, ro, lens, True) <= bar
+    assert R.worst(sf, rs, lens, False) <= F32
+
+
+@dtypes
+@pytest.mark.parametrize("lengths", LENGTHS, ids=str)
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_forward(shape, lengths, dtype):
+    d = R.make(3, *shape, dtype, **lengths)
+    check_forward(d, *run_forward(d))
+
+
+@dtypes
+@pytest.mark.parametrize("shape", [(1, 2, 128, 128), (1, 1, 64, 40)], ids=str)
+def test_forward_per_head_decays_and_no_state(shape, dtype):
+    d = R.make(5, *shape, dtype, lens=[200, 31], per_token=False, s0=False)
+    check_forward(d, *run_forward(d))
+
+
+@dtypes
+@pytest.mark.parametrize("tokens", [257, 512, 1500])
+def test_forward_split_sequences(tokens, dtype):
+    """Few chains: sequences are cut into segments (the first longer than 256)."""
+    d = R.make(7, 1, 2, 128, 128, dtype, lens=[tokens, 100])
+    check_forward(d, *run_forward(d))
+
+
+@dtypes
+def test_forward_simt_and_default_agree_with_strong_decays(dtype):
+    """Decays of e^-1 to e^-20 a token, values below the floor among them, and none at all."""
+    d = R.make(9, 1, 4, 128, 128, dtype, lens=[150, 64])
+    d["g"][:, 0] = 0.0
+    d["g"][:, 1] = -1.0
+    d["g"][:, 2] = -20.0
+    d["g"][::3, 3] = -40.0
+    d["g"][1::7, 3] = float("-inf")
+    for simt in (False, True):
+        check_forward(d, *run_forward(d, force_simt=simt))
+
+
+@dtypes
+def test_decode_continues_prefill(dtype):
+    from linear_attention_sequence_sm_b200 import gdn
+    d = R.make(11, 2, 4, 128, 128, dtype, batch=(3, 70))
+    _, rs = R.forward(d["q"], d["k"], d["v"], d["g"], d["s0"])
+    ro, _ = R.forward(d["q"], d["k"], d["v"], d["g"], d["s0"])
+    c = R.cuda(d)
+    cut = {k: c[k][:, :66].contiguous() for k in ("q", "k", "v", "g")}
+    _, state = gdn.decay_forward(cut["q"], cut["k"], cut["v"], cut["g"], initial_state=c["s0"])
+    outs = []
+    for t in range(66, 70):
+        outs.append(gdn.decay_decode_step(c["q"][:, t].contiguous(), c["k"][:, t].contiguous(),
+                                          c["v"][:, t].contiguous(), c["g"][:, t].contiguous(), state))
+    torch.cuda.synchronize()
+    ref = ro.reshape(3, 70, 4, 128)[:, 66:]
+    got = torch.stack(outs, 1).double().cpu()
+    rel = (got - ref).norm(dim=(1, 3)) / ref.norm(dim=(1, 3))
+    # the decode step keeps everything in fp32 and rounds once
+    assert float(rel.max()) <= (2.0 ** -8 + F32 if dtype == torch.bfloat16 else F32)
+    assert R.worst(state, rs, None, False) <= F32
+
+
+@dtypes
+@pytest.mark.parametrize("per_token", [True, False])
+@pytest.mark.parametrize("shape", [(1, 1, 128, 128), (2, 6, 128, 100), (3, 6, 80, 72), (1, 2, 33, 5), (1, 1, 256, 64),
+                                   (2, 2, 132, 130), (1, 2, 16, 1), (4, 8, 64, 64)], ids=str)
+@pytest.mark.parametrize("n", [1, 5, 200])
+def test_decode(n, shape, per_token, dtype):
+    from linear_attention_sequence_sm_b200 import gdn
+    hk, hv, dk, dv = shape
+    d = R.make(13, hk, hv, dk, dv, dtype, batch=(n, 1), per_token=per_token)
+    ro, rs = R.forward(d["q"], d["k"], d["v"], d["g"], d["s0"])
+    c = R.cuda(d)
+    state = c["s0"].clone()
+    one = lambda t: t[:, 0].contiguous()  # noqa: E731
+    o = gdn.decay_decode_step(one(c["q"]), one(c["k"]), one(c["v"]), one(c["g"]) if per_token else c["g"], state)
+    torch.cuda.synchronize()
+    # An output is one sum of d_k products, and where they cancel its own size bounds nothing: the error
+    # of a sum of d_k products of fp32 values, each s = a s' + v k within 3 u of |a s'| + |v k| (a's own
+    # error, the product's, the sum's), is at most (d_k + 4) u sum_j (|a s'_j| + |v k_j|) |q_j|.
+    absd = {k: (t.abs() if k != "g" else t) for k, t in d.items() if k in ("q", "k", "v", "g", "s0")}
+    size, _ = R.forward(absd["q"], absd["k"], absd["v"], absd["g"], absd["s0"])
+    half = 2.0 ** -8 if dtype == torch.bfloat16 else R.U32
+    err = (o.double().cpu() - ro).abs()
+    assert bool((err <= (dk + 4) * R.U32 * size * (1 + half) + half * ro.abs()).all())
+    assert R.worst(state, rs, None, False) <= 4 * R.U32
+
+
+def grads(d, **kw):
+    from linear_attention_sequence_sm_b200 import gdn
+    c = R.cuda(d)
+    out = gdn.decay_backward(c["q"], c["k"], c["v"], c["g"], c["do"], d_final_state=c["dsf"], initial_state=c["s0"],
+                             cu_seqlens=c["cu"], **kw)
+    torch.cuda.synchronize()
+    return out
+
+
+def check_backward(d, got, dg_bar=DG):
+    lens = R.lens_of(d["q"], d["cu"])
+    ref = R.backward(d["q"], d["k"], d["v"], d["g"], d["do"], d["dsf"], d["s0"], d["cu"])
+    bar = BF16 if d["q"].dtype == torch.bfloat16 else F32
+    for name in ("dq", "dk", "dv"):
+        assert got[name].dtype == d["q"].dtype
+        assert R.worst(got[name], ref[name], lens, True) <= bar, name
+    assert R.worst(got["d_initial_state"], ref["d_initial_state"], lens, False) <= F32
+    if d["g"].dim() == 1:
+        rel = (got["dg"].double().cpu() - ref["dg"]).norm() / ref["dg"].norm().clamp(min=1e-30)
+        assert float(rel) <= dg_bar
+    else:
+        assert R.worst(got["dg"], ref["dg"], lens, True) <= dg_bar
+
+
+@dtypes
+@pytest.mark.parametrize("lengths", LENGTHS, ids=str)
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_backward(shape, lengths, dtype):
+    d = R.make(17, *shape, dtype, **lengths)
+    check_backward(d, grads(d))
+
+
+@dtypes
+@pytest.mark.parametrize("tokens", [300, 1500])
+@pytest.mark.parametrize("per_token", [True, False])
+def test_backward_split_sequences(per_token, tokens, dtype):
+    d = R.make(19, 1, 2, 128, 128, dtype, lens=[64, tokens], per_token=per_token)
+    check_backward(d, grads(d))
+
+
+@dtypes
+def test_backward_without_states(dtype):
+    d = R.make(21, 2, 2, 128, 128, dtype, batch=(2, 130), s0=False)
+    d["dsf"] = None
+    got = grads(d)
+    check_backward(d, got)
+    lean = grads(d, want_dg=False, want_d_initial_state=False)
+    assert lean["dg"] is None and lean["d_initial_state"] is None
+    for n in ("dq", "dk", "dv"):
+        assert torch.equal(lean[n], got[n])
+
+
+@dtypes
+@pytest.mark.parametrize("simt", [False, True])
+def test_backward_strong_decays(simt, dtype):
+    """dg stays accurate where the decays are strong (small beside q . dq) and is zero below the floor."""
+    d = R.make(23, 1, 4, 128, 128, dtype, lens=[150, 64])
+    d["g"][:, 0] = 0.0
+    d["g"][:, 1] = -3.0
+    d["g"][:, 2] = -8.0
+    d["g"][::3, 3] = -40.0
+    got = grads(d, force_simt=simt)
+    check_backward(d, got)
+    assert bool((got["dg"][::3, 3] == 0).all())
+
+
+def test_backward_against_differences():
+    """Directional differences of the 64-bit forward against the kernels' gradients (fp32)."""
+    d = R.make(25, 1, 2, 24, 16, torch.float32, lens=[70, 9])
+    got = grads(d)
+
+    def loss(x):
+        o, S = R.forward(x["q"], x["k"], x["v"], x["g"], x["s0"], d["cu"])
+        return float((o * d["do"].double().reshape(o.shape)).sum() + (S * d["dsf"].double()).sum())
+
+    gen = torch.Generator().manual_seed(1)
+    names = dict(q="dq", k="dk", v="dv", g="dg", s0="d_initial_state")
+    base = {k: d[k].double() for k in names}
+    for k, name in names.items():
+        step = torch.randn(base[k].shape, generator=gen, dtype=torch.float64)
+        h = 1e-5
+        diff = (loss({**base, k: base[k] + h * step}) - loss({**base, k: base[k] - h * step})) / (2 * h)
+        terms = got[name].double().cpu().reshape(step.shape) * step
+        # the difference is off by h^2 times third derivatives and 1e-16 / h of the loss
+        assert abs(float(terms.sum()) - diff) <= 1e-4 * float(terms.norm()), k
+
+
+def test_same_call_same_bits():
+    d = R.make(27, 2, 6, 128, 128, torch.bfloat16, lens=[300, 64, 77])
+    a, b = grads(d), grads(d)
+    assert all(torch.equal(a[k], b[k]) for k in a)
+    x, y = run_forward(d), run_forward(d)
+    assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+
+
+@dtypes
+def test_output_side(dtype):
+    """The output side over o: one more rounding of o (stored, then read again)."""
+    from linear_attention_sequence_sm_b200 import gdn
+    d = R.make(29, 1, 2, 128, 128, dtype, batch=(2, 70))
+    gen = torch.Generator().manual_seed(2)
+    w, z = torch.randn(128, generator=gen), torch.randn(2, 70, 2, 128, generator=gen).to(dtype)
+    y, _ = run_forward(d, output_norm=gdn.OutputNorm(weight=w.cuda(), gate=z.cuda(), eps=1e-6))
+    ro, _ = R.forward(d["q"], d["k"], d["v"], d["g"], d["s0"])
+    zz = z.double().reshape(ro.shape)
+    ref = ro / (ro.square().mean(-1, keepdim=True) + 1e-6).sqrt() * w.double() * zz * torch.sigmoid(zz)
+    # two relative errors of o (its own and its root mean square's) and the result's rounding
+    bar = 2 * BF16 + 2.0 ** -8 if dtype == torch.bfloat16 else 4 * F32
+    assert R.worst(y, ref, [70, 70], True) <= bar
+    one = lambda t: t[:, 0].contiguous()  # noqa: E731
+    c = R.cuda(d)
+    y1 = gdn.decay_decode_step(one(c["q"]), one(c["k"]), one(c["v"]), one(c["g"]), c["s0"].clone(),
+                               output_norm=gdn.OutputNorm(weight=w.cuda(), gate=one(z.cuda()), eps=1e-6))
+    first = ref.reshape(2, 70, 2, 128)[:, 0]
+    assert R.worst(y1, first, [1, 1], True) <= bar
+
+
+def test_bad_cu_seqlens_leaves_outputs_and_says_so():
+    from linear_attention_sequence_sm_b200 import gdn
+    d = R.make(31, 1, 2, 128, 128, torch.bfloat16, lens=[40, 60])
+    c = R.cuda(d)
+    for bad in ([0, 101, 100], [1, 40, 100], [0, 40, 99], [0, 60, 40], [0, -1, 100]):
+        cu = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        shape = gdn.make_shape(c["q"], c["v"], cu, 64)
+        ws = torch.empty(gdn.decay_workspace_size(shape, backward=True), dtype=torch.uint8, device="cuda")
+        o, sf = torch.full_like(c["v"], 7.0), torch.full_like(c["s0"], 7.0)
+        gdn.decay_forward(c["q"], c["k"], c["v"], c["g"], initial_state=c["s0"], cu_seqlens=cu, out=o, final_state=sf,
+                          workspace=ws)
+        assert gdn.read_device_status(ws) == gdn.GDN_ERR_DEVICE_CHECK
+        assert bool((o == 7).all()) and bool((sf == 7).all())
+        gdn.decay_backward(c["q"], c["k"], c["v"], c["g"], c["do"], cu_seqlens=cu, workspace=ws)
+        assert gdn.read_device_status(ws) == gdn.GDN_ERR_DEVICE_CHECK
+    gdn.decay_forward(c["q"], c["k"], c["v"], c["g"], cu_seqlens=c["cu"], workspace=ws)
+    assert gdn.read_device_status(ws) == gdn.GDN_OK
+
+
+def test_final_state_in_place_and_other_stream():
+    from linear_attention_sequence_sm_b200 import gdn
+    d = R.make(33, 1, 2, 128, 128, torch.bfloat16, batch=(1, 400))
+    o, sf = run_forward(d)
+    c = R.cuda(d)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    state = c["s0"].clone()
+    side.wait_stream(torch.cuda.current_stream())
+    o2, s2 = gdn.decay_forward(c["q"], c["k"], c["v"], c["g"], initial_state=state, final_state=state, stream=side)
+    side.synchronize()
+    assert s2 is state and torch.equal(o, o2) and torch.equal(sf, state)
+
+
+def test_captured_and_replayed():
+    """Prefill, decode and backward in one graph, replayed on new inputs."""
+    from linear_attention_sequence_sm_b200 import gdn
+    d, e = (R.make(s, 1, 2, 128, 128, torch.bfloat16, lens=[300, 50]) for s in (35, 36))
+    c = R.cuda(d)
+    state = c["s0"].clone()
+    one = {k: c[k][:2].contiguous() for k in ("q", "k", "v", "g")}
+
+    def step():
+        state.copy_(c["s0"])
+        o, sf = gdn.decay_forward(c["q"], c["k"], c["v"], c["g"], initial_state=state, cu_seqlens=c["cu"],
+                                  final_state=state)
+        t = gdn.decay_decode_step(one["q"], one["k"], one["v"], one["g"], state)
+        gr = gdn.decay_backward(c["q"], c["k"], c["v"], c["g"], c["do"], d_final_state=c["dsf"],
+                                initial_state=c["s0"], cu_seqlens=c["cu"])
+        return [o, t, state, *gr.values()]
+
+    warm = torch.cuda.Stream()
+    warm.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(warm):
+        step()
+    torch.cuda.current_stream().wait_stream(warm)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for src in (e, d):
+        for k, t in R.cuda(src).items():
+            c[k].copy_(t)
+        for k in one:
+            one[k].copy_(c[k][:2])
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in outs]
+        want = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
