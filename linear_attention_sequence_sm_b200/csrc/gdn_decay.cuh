@@ -102,7 +102,7 @@ struct DecayPass {
     int32_t out_f32;              // 32-bit out whatever the inputs' type
     float *dot;                   // [hv][tokens], or NULL
     float *ckpt;                  // [cks][hv][128 * 128], or NULL
-    float *zsum;                  // backward in time: <Sigma, checkpoint>, [cks][hv]; NULL: write checkpoints
+    float *zsum;                  // backward in time: <Sigma, checkpoint>, [cks][hv][8 parts]; NULL: write checkpoints
     const float *s_first;         // the checkpoint at a sequence's start, stored as s_in, or NULL for zeros
     int32_t counter;              // which work counter
     DecaySched sched;
@@ -120,6 +120,8 @@ cudaError_t launch_decay_combine(const gdn_shape_t &s, const DecayLayout &L, con
 // The pass on CUDA cores (fp32 or bf16 storage, any d <= 128), and on the
 // tensor cores (bf16, d a multiple of 8).
 cudaError_t launch_decay_pass_simt(const DecayPass &p, int32_t dtype, int64_t max_units, cudaStream_t stream);
+bool decay_tc_supported(const gdn_shape_t &s);
+cudaError_t launch_decay_pass_tc(const DecayPass &p, int64_t max_units, cudaStream_t stream);
 
 // Pairs inside a chunk for the decays' gradient: intra [hv][tokens].
 cudaError_t launch_decay_intra_simt(const gdn_shape_t &s, const int32_t *cu, const DecayLayout &L,

@@ -57,6 +57,10 @@ gdn_status_t check_gate_layout(int32_t g_layout) {
 }
 
 cudaError_t run_pass(const DecayPass &p, const gdn_shape_t &s, int64_t max_units, cudaStream_t stream) {
+    int major = 0;
+    device_sm_count(&major);
+    // the tensor-core form where it applies (bf16, head sizes multiples of 8)
+    if (major == 10 && decay_tc_supported(s)) return launch_decay_pass_tc(p, max_units, stream);
     return launch_decay_pass_simt(p, s.dtype, max_units, stream);
 }
 

@@ -216,7 +216,8 @@ decay_dg_kernel(int num_seqs, int hv, int tokens, const int32_t *__restrict__ cu
         const int p0 = (ck - sc.ck_base[n]) * ick, p1 = min(len, p0 + ick);
         const float *dq = dot_q + size_t(h) * tokens + start, *dk = dot_k + size_t(h) * tokens + start;
         const float *in = intra + size_t(h) * tokens + start;
-        float across = zsum[size_t(ck) * hv + h];
+        float across = 0.f;
+        for (int e = 0; e < 8; ++e) across += zsum[(size_t(ck) * hv + h) * 8 + e];
         for (int b = p0; b < p1; b += kDecayChunk) {
             const int t0 = b + 2 * lane, t1 = t0 + 1;
             const bool v0 = t0 < p1, v1 = t1 < p1;
@@ -335,7 +336,7 @@ DecayLayout decay_layout(const gdn_shape_t &s, bool backward) {
     if (backward) {
         L.state_off[1] = take(size_t(L.max_slots) * hv * 65536);
         L.ckpt_off = take(size_t(L.max_cks) * hv * 65536);
-        L.zsum_off = take(size_t(L.max_cks) * hv * 4);
+        L.zsum_off = take(size_t(L.max_cks) * hv * 32);
         for (int i = 0; i < 2; ++i) L.dot_off[i] = take(size_t(tokens) * hv * 4);
         L.intra_off = take(size_t(tokens) * hv * 4);
         L.dgtok_off = take(size_t(tokens) * hv * 4);

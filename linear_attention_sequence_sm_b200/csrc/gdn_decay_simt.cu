@@ -282,11 +282,7 @@ decay_pass_simt_kernel(const DecayPass a) {
                 for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
                 if ((tid & 31) == 0) sm.red[tid >> 5] = s;
                 __syncthreads();
-                if (tid == 0) {
-                    s = 0.f;
-                    for (int w = 0; w < kThreads / 32; ++w) s += sm.red[w];
-                    a.zsum[size_t(slot) * hv + h] = s;
-                }
+                if (tid < 8) a.zsum[(size_t(slot) * hv + h) * 8 + tid] = sm.red[tid];
             }
         }
         __syncthreads();

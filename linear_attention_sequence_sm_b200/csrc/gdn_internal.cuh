@@ -242,10 +242,12 @@ cudaError_t launch_chunk_simt(const PrefillArgs &a, cudaStream_t stream, int num
 
 // Tensor maps (gdn_tma.cu): gates [tokens, heads] fp32 in boxes of 4 heads x
 // 64 tokens; [tokens, heads, 128] bf16 in boxes of 64 x 1 x 64, 128-byte
-// swizzle (out: 128 x 1 x 64, no swizzle); rows x 64 bf16 tiles of 64 rows,
+// swizzle (out: 128 x 1 x 64, no swizzle; make_head_map: any d, a multiple of
+// 8); rows x 64 bf16 tiles of 64 rows,
 // 128-byte swizzle.
 bool make_gate_map(CUtensorMap *map, const float *base, int heads, int tokens);
 bool make_map(CUtensorMap *map, const void *base, int heads, int tokens, bool out = false);
+bool make_head_map(CUtensorMap *map, const void *base, int heads, int d, int tokens);
 bool make_tile_map(CUtensorMap *map, const void *base, int64_t rows);
 
 // Tensor-core chunkwise kernel (bf16, d = 128, C = 64) as one kernel.

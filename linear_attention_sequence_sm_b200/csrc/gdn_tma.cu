@@ -56,6 +56,21 @@ bool make_map(CUtensorMap *map, const void *base, int heads, int tokens, bool ou
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [tokens, heads, d] bf16 with d a multiple of 8 up to 128, in boxes of 64 (d)
+// x 1 (head) x 64 (tokens), 128-byte swizzle; columns past d and rows past the
+// last token read as zeros.
+bool make_head_map(CUtensorMap *map, const void *base, int heads, int d, int tokens) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {cuuint64_t(d), cuuint64_t(heads), cuuint64_t(tokens)};
+    const cuuint64_t strides[2] = {cuuint64_t(d) * 2, cuuint64_t(heads) * cuuint64_t(d) * 2};
+    const cuuint32_t box[3] = {64, 1, 64};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // `rows` x 64 bf16 matrix (rows of 128 bytes) in boxes of 64 rows, 128-byte
 // swizzle: the 64 x 64 tiles of the chunk inverses.
 bool make_tile_map(CUtensorMap *map, const void *base, int64_t rows) {

@@ -179,8 +179,9 @@ def test_backward_without_states(dtype):
     check_backward(d, got)
     lean = grads(d, want_dg=False, want_d_initial_state=False)
     assert lean["dg"] is None and lean["d_initial_state"] is None
-    for n in ("dq", "dk", "dv"):
-        assert torch.equal(lean[n], got[n])
+    # without dg the state's copy is rounded once (with it, its products feed a 32-bit sum): the bars
+    # of the formula hold either way, equal bits do not
+    check_backward(d, dict(got, **{n: lean[n] for n in ("dq", "dk", "dv")}))
 
 
 @dtypes
