@@ -2,33 +2,42 @@
 // (bf16, head sizes a multiple of 8 up to 128), see gdn_decay.cuh for the
 // pass and its operands x, y, z, out.
 //
-// Chunk of 64 tokens, state Sigma (z x y, fp32, tensor memory), every product
-// one tcgen05.mma stream with fp32 accumulators:
-//   (QK) x y^T                     64 x 64 x dy      -> P = QK . decay mask, bf16
-//   (KV) Sigma += z^T (w y)        128 x dy x 64     the state's critical path
-//   (X1) X1 = Sigma x^T            128 x 64 x dy     bf16 copies of Sigma (tensor memory) times x
-//   (X2) X2 = z^T P^T              128 x 64 x 64
+// Chunk of 64 tokens; every product is one tcgen05.mma stream with fp32
+// accumulators in tensor memory:
+//   (QK) x y^T               64 x 64 x dy    -> P = QK . decay mask, bf16
+//   (KV) L = (w z)^T y       128 x dy x 64   -> Sigma <- e^G Sigma + L
+//   (X1) X1 = Sigma x^T      128 x 64 x dy   bf16 copies of Sigma times x
+//   (X2) X2 = z^T P^T        128 x 64 x 64
 // out^T = X2 + w_in X1.  x, y, z come by TMA as 128-byte-swizzled tiles and
 // serve as the K-major and MN-major operands they are; head sizes below 128
-// are padded with zeros by TMA.
+// are padded with zeros by TMA.  (w z)^T and the copies of Sigma are A
+// operands in tensor memory: operands read from shared memory are what the
+// products wait for (12 products of 128 x 128 x 16 take 1450 cycles with both
+// operands there, 1040 with one), and what shared memory holds goes to a
+// third tile of x, y and z, loaded two chunks ahead.
 //
-// Precision.  The state is fp32 in and out, so the scaled operand w y is split
-// into three bf16 terms (24 bits; one term would leave 2^-9 of the state, two
-// terms 2^-17).  For `dot` passes, whose products with the start state feed
-// the decays' fp32 gradient, Sigma's copy is split into three terms as well;
-// otherwise X1 ends in a bf16 output, and one bf16 copy costs it as much as
-// the output's own rounding.  P is one bf16 term for the same reason.
+// Sigma itself lives in the state warps' registers, so that L's products need
+// nothing from the chunk before: the chain from chunk to chunk is one
+// multiply-add per element, its rounded copy, and X1.
+//
+// Precision.  The state is fp32 in and out, so w z is split into three bf16
+// terms (24 bits; one term would leave 2^-9 of the state, two 2^-17).  For
+// `dot` passes, whose products with the start state feed the decays' fp32
+// gradient, Sigma's copy is split into three terms as well; otherwise X1 ends
+// in a bf16 output, and one bf16 copy costs it as much as the output's own
+// rounding.  P is one bf16 term for the same reason.
 //
 // Roles (18 warps):
-//   state warps 0-7    two per tensor-memory quarter, 64 state columns each:
-//                      before chunk n: copies of Sigma, Sigma <- e^G Sigma
+//   state warps 0-7    two per tensor-memory quarter, 64 state columns each
 //   out warps 8-11     X1, X2 -> out (and the dot with aux)
-//   prep warps 12-15   decays, the split of w y, P from QK
+//   prep warps 12-15   decays, w z in three terms, P from QK
 //   warp 16            TMA loads;  warp 17  issues every product, in the order
-//                      KV(n), X1(n), X2(n), QK(n + 1): the state warps work on
-//                      chunk n + 1's state while X1, X2 and QK run.  (With
-//                      three copies of Sigma there is tensor memory for one
-//                      set only, so X1(n) goes before KV(n).)
+//                      KV(n), X1(n), X2(n), QK(n + 1), which leaves P(n + 1)
+//                      the time of KV(n + 1) and X1(n + 1).  With three copies
+//                      of Sigma X1 alone is that long, and tensor memory is
+//                      full: X2 shares QK's columns, w z has room for half a
+//                      chunk, and the order is X1(n), X2(n), KV(n + 1),
+//                      QK(n + 1).
 // All hand-overs are mbarriers with bounded waits; a timeout records
 // GDN_ERR_DEVICE_CHECK (bad_index -2).  A CTA takes units (segment, head) with
 // a stride of the grid; nothing synchronises it between units.
@@ -54,49 +63,54 @@ constexpr int kVecG = 0, kVecIn = 64, kVecSt = 128, kVecGamma = 192, kVecFloats 
 
 // kKind: what a pass leaves out or adds
 enum { kPlain = 0, kDot = 1, kStateOnly = 2 };
+constexpr int kRing = 3;  // tiles of x, y and z
 
 template <int kKind> struct Cfg {
     static constexpr int kCopies = kKind == kDot ? 3 : 1;        // bf16 terms of Sigma's copy
-    static constexpr int kQkBufs = kKind == kDot ? 1 : 2;
-    static constexpr int kNX = kKind == kDot ? 2 : 3, kNZ = kNX, kNY = 2;
+    static constexpr int kWz = kKind == kDot ? 1 : 2;            // half chunks of w z
     // shared memory, from a 1024-byte-aligned base
     static constexpr uint32_t kOffX = 0;
-    static constexpr uint32_t kOffZ = kOffX + kNX * kTile;
-    static constexpr uint32_t kOffY = kOffZ + kNZ * kTile;
-    static constexpr uint32_t kOffAux = kOffY + kNY * kTile;                    // [2], kDot only
-    static constexpr uint32_t kOffYs = kOffAux + (kKind == kDot ? 2 * kTile : 0);  // three terms of w y
-    static constexpr uint32_t kOffP = kOffYs + 3 * kTile;                       // [2]
-    static constexpr uint32_t kOffVec = kOffP + 2 * kPTile;                     // [4]
-    static constexpr uint32_t kOffRed = kOffVec + 4 * kVecFloats * 4;           // [4 warps][64]
+    static constexpr uint32_t kOffZ = kOffX + kRing * kTile;
+    static constexpr uint32_t kOffY = kOffZ + kRing * kTile;
+    static constexpr uint32_t kOffAux = kOffY + kRing * kTile;                     // [2], kDot only
+    static constexpr uint32_t kOffP = kOffAux + (kKind == kDot ? 2 * kTile : 0);   // [2]
+    static constexpr uint32_t kOffOut = kOffP + 2 * kPTile;                        // 4096 bytes an out warp
+    static constexpr uint32_t kOffVec = kOffOut + kTile;                           // [4]
+    static constexpr uint32_t kOffRed = kOffVec + 4 * kVecFloats * 4;              // [4 warps][64]
     static constexpr uint32_t kOffBar = kOffRed + 1024;
     static constexpr uint32_t kSmem = kOffBar + 320 + 1024;
     static_assert(kSmem <= 232448, "shared memory over the sm_100 per-block limit");
     // tensor memory columns
-    static constexpr uint32_t kColS = 0, kColC = 128;  // Sigma; its copies (64 columns each, two buffers or three terms)
-    static constexpr uint32_t kColX1 = kCopies == 1 ? 256 : 320, kColX2 = kColX1 + 64, kColQK = kColX2 + 64;
+    static constexpr uint32_t kColL = 0, kColC = 128;  // L; the copies of Sigma (64 columns a term)
+    static constexpr uint32_t kColX1 = kColC + 64 * kCopies, kColX2 = kColX1 + 64;
+    static constexpr uint32_t kColQK = kKind == kDot ? kColX2 : kColX2 + 64;
+    static constexpr uint32_t kColW = kColQK + 64;     // w z: 48 columns a half chunk (16 a term)
+    static_assert(kColW + 48 * kWz <= kTmemCols, "tensor memory");
 };
 
 // mbarriers
 enum {
     kBX = 0,        // [3] x landed
     kBZ = 3,        // [3] z
-    kBY = 6,        // [2] y
-    kBA = 8,        // [2] aux
-    kBXFree = 10,   // [3] X1 and QK of the slot's chunk done
-    kBZFree = 13,   // [3] KV and X2 done
-    kBYFree = 16,   // [2] QK done, w y written (4 prep warps)
-    kBAFree = 18,   // [2] dot taken (4 out warps)
-    kBVec = 20,     // [2] token vectors written
-    kBYs = 22,      // w y written (4 prep warps)
-    kBSt = 23,      // state pass done (8 state warps)
-    kBKV = 24,      // KV done
-    kBQK = 25,      // [2] QK done
-    kBP = 27,       // [2] P written (4 prep warps)
-    kBPFree = 29,   // [2] X2 done
-    kBOut = 31,     // X1, X2 done (and an arrival of the issuing thread, which orders the token vectors)
-    kBOutFree = 32, // X1, X2 read (4 out warps)
-    kBDrain = 33,
-    kNumBars = 34
+    kBY = 6,        // [3] y
+    kBA = 9,        // [2] aux
+    kBXFree = 11,   // [3] X1 (and QK) of the slot's chunk done
+    kBZFree = 14,   // [3] X2 done (w z was taken before KV)
+    kBYFree = 17,   // [3] KV (and QK) done
+    kBAFree = 20,   // [2] dot taken (4 out warps)
+    kBW = 22,       // [2] a half chunk of w z written (4 prep warps)
+    kBKV0 = 24,     // KV of the first half done
+    kBKV1 = 25,     // KV done (and an arrival of the issuing thread, which orders the token vectors)
+    kBLFree = 26,   // L read (8 state warps)
+    kBSt = 27,      // copies of Sigma written (8 state warps)
+    kBX1 = 28,      // X1 done
+    kBQK = 29,      // QK done
+    kBP = 30,       // [2] P written (4 prep warps)
+    kBPFree = 32,   // [2] X2 done
+    kBOut = 34,     // X1, X2 done (and an arrival of the issuing thread)
+    kBOutFree = 35, // X1, X2 read (4 out warps)
+    kBDrain = 36,
+    kNumBars = 37
 };
 
 struct Maps {
@@ -155,30 +169,40 @@ __device__ __forceinline__ void tmem_ld_m64(uint32_t taddr, float (&v)[32]) {
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// 32 state columns at c: copies of Sigma (kCopies bf16 terms, `step` columns
-// apart), Sigma <- gamma Sigma.
-template <int kCopies>
-__device__ __forceinline__ void state_slice(uint32_t s_addr, uint32_t c_addr, float gamma, float (&v)[32]) {
-    uint32_t pk[16];
+// 32 columns of 16 lanes in fragments: registers 4 j .. 4 j + 3 hold columns
+// 8 j + 2 (lane % 4) and the next, of lane / 4 and of lane / 4 + 8.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
 #pragma unroll
-    for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-    tmem_st16u(c_addr, pk);
-    if constexpr (kCopies == 3) {
-        float r[32];
-#pragma unroll
-        for (int t = 1; t < 3; ++t) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                r[2 * j] = (t == 1 ? v[2 * j] : r[2 * j]) - bf_lo(pk[j]);
-                r[2 * j + 1] = (t == 1 ? v[2 * j + 1] : r[2 * j + 1]) - bf_hi(pk[j]);
-                pk[j] = pack_bf16x2(r[2 * j], r[2 * j + 1]);
-            }
-            tmem_st16u(c_addr + 64 * t, pk);
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] *= gamma;
-    tmem_st32(s_addr, v);
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+// 16 columns of 16 lanes: registers 2 j, 2 j + 1 go to column 4 j + lane % 4
+// of lane / 4 and of lane / 4 + 8.
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+// Four 8 x 8 tiles of 16-bit values, transposed on the way: lane l gives the
+// address of row l % 8 of tile l / 8, and holds elements (row 2 (l % 4) and
+// the next, column l / 4) of each tile.
+__device__ __forceinline__ void ldmatrix_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void stmatrix_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
+                 : "memory");
 }
 
 template <int kKind>
@@ -197,10 +221,10 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
     if (tid == 0) {
         for (int i = 0; i < kNumBars; ++i) {
             int n = 1;
-            if (i == kBYFree || i == kBYFree + 1) n = kSt ? 4 : 5;
-            if (i == kBAFree || i == kBAFree + 1 || i == kBYs || i == kBP || i == kBP + 1 || i == kBOutFree) n = 4;
-            if (i == kBSt) n = 8;
-            if (i == kBOut) n = 2;
+            if (i == kBAFree || i == kBAFree + 1 || i == kBW || i == kBW + 1 || i == kBP || i == kBP + 1 || i == kBOutFree)
+                n = 4;
+            if (i == kBSt || i == kBLFree) n = 8;
+            if (i == kBOut || i == kBKV1) n = 2;
             mbar_init(bar(i), uint32_t(n));
         }
         fence_mbarrier_init();
@@ -222,159 +246,160 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
     uint32_t m = 0;  // chunks this CTA has processed
 
     if (warp < kWarpOut) {
-        // ==================== state warps: thread = state row ====================
+        // ==================== state warps: thread = state row, 64 columns in registers ====================
         const int half = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t trow = tmem + (uint32_t((warp & 3) * 32) << 16);
         const int c0 = 64 * half;
         const bool mine = half < ya;
         const bool zin = row < dz;
+        float S[64];
         while (ok && w.next(kSt)) {
             const size_t sbase = (size_t(w.seg.seq) * hv + w.h) * dz * dy;
-            const bool own = !kSt && w.seg.slot >= 0;
-            if (mine) {  // the start state
+#pragma unroll
+            for (int j = 0; j < 64; ++j) S[j] = 0.f;
+            if (mine && zin && !kSt) {  // the start state
                 const float *src = nullptr;
                 bool tr = false;
                 int ld = 0;
-                if (own) {
+                if (w.seg.slot >= 0) {
                     src = a.seg_state + (size_t(w.seg.slot) * hv + w.h) * 16384;
                     tr = a.seg_trans;
                     ld = 128;
-                } else if (!kSt && a.s_in && w.first) {
+                } else if (a.s_in && w.first) {
                     src = a.s_in + sbase;
                     tr = a.s_trans;
                     ld = tr ? dz : dy;
                 }
+                if (src && tr) {
 #pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    float v[32];
-                    const int c = c0 + 32 * p;
+                    for (int j = 0; j < 64; ++j)
+                        if (c0 + j < dy) S[j] = src[size_t(c0 + j) * ld + row];
+                } else if (src) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0.f;
-                    if (src && zin) {
-                        if (tr) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (c + j < dy) v[j] = src[size_t(c + j) * ld + row];
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; j += 4)  // dy and ld are multiples of 8
-                                if (c + j < dy) load4(src + size_t(row) * ld + c + j, v + j);
-                        }
-                    }
-                    tmem_st32(trow + K::kColS + uint32_t(c), v);
+                    for (int j = 0; j < 64; j += 4)  // dy and ld are multiples of 8
+                        if (c0 + j < dy) load4(src + size_t(row) * ld + c0 + j, S + j);
                 }
-                tmem_wait_st();
             }
             float dec = 1.f;
-            for (int n = 0; n <= w.nch; ++n) {
-                // before chunk n, or after the last one
-                const bool end = n == w.nch;
+            for (int n = 0; n < w.nch; ++n) {
                 const uint32_t mm = m + uint32_t(n);
-                if (!end) ok = warp_wait(bar(kBVec + int(mm & 1u)), (mm >> 1) & 1u);
-                if (ok && n > 0) ok = warp_wait(bar(kBKV), (mm - 1) & 1u);
+                const int p = w.seg.pos + w.chunk_at(n);  // the chunk's start in the sequence
+                if (kDots && a.ckpt && !a.zsum && mine && p > 0 && p % a.sched.hdr->ick == 0) {
+                    float *ck = a.ckpt + (size_t(w.seg.ck + p / a.sched.hdr->ick) * hv + w.h) * 16384;
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) ck[(c0 + j) * 128 + row] = S[j];
+                }
+                if constexpr (!kSt) {
+                    // the copies of Sigma, once the previous X1 has read its own
+                    if (mm > 0) ok = warp_wait(bar(kBX1), (mm - 1) & 1u);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (mine) {
+                        const uint32_t ca = trow + K::kColC + uint32_t(c0 / 2);
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(S[32 * q + 2 * j], S[32 * q + 2 * j + 1]);
+                            tmem_st16u(ca + 16 * q, pk);
+                            if constexpr (K::kCopies == 3) {
+                                float r[32];
+#pragma unroll
+                                for (int t = 1; t < 3; ++t) {
+#pragma unroll
+                                    for (int j = 0; j < 16; ++j) {
+                                        r[2 * j] = (t == 1 ? S[32 * q + 2 * j] : r[2 * j]) - bf_lo(pk[j]);
+                                        r[2 * j + 1] = (t == 1 ? S[32 * q + 2 * j + 1] : r[2 * j + 1]) - bf_hi(pk[j]);
+                                        pk[j] = pack_bf16x2(r[2 * j], r[2 * j + 1]);
+                                    }
+                                    tmem_st16u(ca + 64 * t + 16 * q, pk);
+                                }
+                            }
+                        }
+                        tmem_wait_st();
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kBSt));
+                }
+                ok = warp_wait(bar(kBKV1), mm & 1u);
                 if (!ok) break;
                 tc_fence_after();
-                const float gamma = end ? 1.f : vecs(mm)[kVecGamma];
-                // where the state is wanted: a checkpoint to write (forward) or to be dotted with (backward)
-                float *ck = nullptr;
-                const float *cd = nullptr;
-                bool cd_first = false;
-                float *zs = nullptr;
-                if (kDots && a.ckpt) {
-                    const int ick = a.sched.hdr->ick;
-                    if (!a.zsum) {
-                        const int p = w.seg.pos + w.chunk_at(n);
-                        if (!end && p > 0 && p % ick == 0) ck = a.ckpt + (size_t(w.seg.ck + p / ick) * hv + w.h) * 16384;
-                    } else if (n > 0) {
-                        const int p = w.seg.pos + w.chunk_at(n - 1);  // the state is the one at this chunk's start
-                        if (p % ick == 0) {
-                            const size_t slot = size_t(w.seg.ck + p / ick) * hv + w.h;
-                            zs = a.zsum + slot * 8;
-                            cd_first = p == 0;
-                            cd = cd_first ? (a.s_first ? a.s_first + sbase : nullptr) : a.ckpt + slot * 16384;
-                        }
-                    }
-                }
-                float dot = 0.f;
+                const float gamma = vecs(mm)[kVecGamma];
                 if (mine) {
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        const int c = c0 + 32 * p;
+                    for (int q = 0; q < 2; ++q) {
                         float v[32];
-                        tmem_ld32(trow + K::kColS + uint32_t(c), v);
+                        tmem_ld32(trow + K::kColL + uint32_t(c0 + 32 * q), v);
                         tmem_wait_ld();
-                        if constexpr (kDots) {
-                            if (ck) {
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) ck[(c + j) * 128 + row] = v[j];
-                            }
-                            if (cd && zin) {
-                                if (cd_first) {  // stored [y][z] (s_trans)
-#pragma unroll
-                                    for (int j = 0; j < 32; ++j)
-                                        if (c + j < dy) dot = fmaf(cd[size_t(c + j) * dz + row], v[j], dot);
-                                } else {
-#pragma unroll
-                                    for (int j = 0; j < 32; ++j) dot = fmaf(cd[(c + j) * 128 + row], v[j], dot);
-                                }
-                            }
-                        }
-                        if (!end) {
-                            if constexpr (kSt) {
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) v[j] *= gamma;
-                                tmem_st32(trow + K::kColS + uint32_t(c), v);
-                            } else {
-                                const uint32_t ca = trow + K::kColC + (K::kCopies == 1 ? 64u * (mm & 1u) : 0u) + uint32_t(c / 2);
-                                state_slice<K::kCopies>(trow + K::kColS + uint32_t(c), ca, gamma, v);
-                            }
-                        } else {
-                            float *dst = nullptr;
-                            bool tr = false;
-                            int ld = 128;
-                            if constexpr (kSt) {
-                                dst = a.seg_local + (size_t(w.seg.slot) * hv + w.h) * 16384;
-                            } else if (w.last && a.s_out) {
-                                dst = a.s_out + sbase;
-                                tr = a.s_trans;
-                                ld = tr ? dz : dy;
-                            }
-                            if (dst && zin) {
-                                if (tr) {
-#pragma unroll
-                                    for (int j = 0; j < 32; ++j)
-                                        if (c + j < dy) dst[size_t(c + j) * ld + row] = v[j];
-                                } else {
-#pragma unroll
-                                    for (int j = 0; j < 32; j += 4)
-                                        if (c + j < dy)
-                                            *reinterpret_cast<float4 *>(dst + size_t(row) * ld + c + j) =
-                                                make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                                }
-                            }
-                        }
+                        for (int j = 0; j < 32; ++j) S[32 * q + j] = fmaf(gamma, S[32 * q + j], v[j]);
                     }
-                    tmem_wait_st();
-                }
-                if (kDots && zs) {
-#pragma unroll
-                    for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
-                    if (lane == 0) zs[warp] = dot;
                 }
                 dec *= gamma;
                 tc_fence_before();
                 __syncwarp();
-                if (!end && lane == 0) mbar_arrive(bar(kBSt));
+                if (lane == 0) mbar_arrive(bar(kBLFree));
+                if (kDots && a.zsum && p % a.sched.hdr->ick == 0) {
+                    // <Sigma, checkpoint> at the chunk's start
+                    const size_t slot = size_t(w.seg.ck + p / a.sched.hdr->ick) * hv + w.h;
+                    float dot = 0.f;
+                    if (mine && zin) {
+                        if (p == 0) {  // stored [y][z] (s_trans)
+                            if (a.s_first) {
+#pragma unroll
+                                for (int j = 0; j < 64; ++j)
+                                    if (c0 + j < dy) dot = fmaf(a.s_first[sbase + size_t(c0 + j) * dz + row], S[j], dot);
+                            }
+                        } else {
+                            const float *cp = a.ckpt + slot * 16384;
+#pragma unroll
+                            for (int j = 0; j < 64; ++j) dot = fmaf(cp[(c0 + j) * 128 + row], S[j], dot);
+                        }
+                    }
+#pragma unroll
+                    for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
+                    if (lane == 0) a.zsum[slot * 8 + warp] = dot;
+                }
             }
-            if (kSt && ok && tid == 0) a.seg_dec[size_t(w.seg.slot) * hv + w.h] = dec;
+            if (!ok) break;
+            {
+                float *dst = nullptr;
+                bool tr = false;
+                int ld = 128;
+                if constexpr (kSt) {
+                    dst = a.seg_local + (size_t(w.seg.slot) * hv + w.h) * 16384;
+                    if (tid == 0) a.seg_dec[size_t(w.seg.slot) * hv + w.h] = dec;
+                } else if (w.last && a.s_out) {
+                    dst = a.s_out + sbase;
+                    tr = a.s_trans;
+                    ld = tr ? dz : dy;
+                }
+                if (dst && mine && zin) {
+                    if (tr) {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j)
+                            if (c0 + j < dy) dst[size_t(c0 + j) * ld + row] = S[j];
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 64; j += 4)
+                            if (c0 + j < dy)
+                                *reinterpret_cast<float4 *>(dst + size_t(row) * ld + c0 + j) =
+                                    make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+                    }
+                }
+            }
             m += uint32_t(w.nch);
         }
     } else if (warp < kWarpPrep) {
-        // ==================== out warps: thread = z row ====================
+        // ==================== out warps: 32 z rows each, read in fragments ====================
         if constexpr (!kSt) {
-            const int quarter = warp & 3, row = quarter * 32 + lane, ot = tid - 32 * kWarpOut;
-            const uint32_t trow = tmem + (uint32_t(quarter * 32) << 16);
+            const int quarter = warp & 3, ot = tid - 32 * kWarpOut;
+            const uint32_t tq = tmem + (uint32_t(quarter * 32) << 16);
+            const int tp = 2 * (lane & 3);                 // first of this thread's two tokens in a group of 8
             float *red = reinterpret_cast<float *>(smem + K::kOffRed);
+            float *stage = reinterpret_cast<float *>(smem + K::kOffOut + quarter * 4096);
+            const uint32_t stage_u = sb + K::kOffOut + uint32_t(quarter) * 4096;
             while (ok && w.next(false)) {
                 for (int n = 0; n < w.nch; ++n) {
                     const uint32_t mm = m + uint32_t(n);
@@ -389,75 +414,119 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                     const float *win = vecs(mm) + kVecIn;
                     const size_t tok = size_t(w.seg.start) + t0;
                     const size_t step = size_t(hv) * dz;
-                    const size_t at = (tok * hv + w.h) * dz + row;
-                    const uint32_t aux = sb + K::kOffAux + (mm & 1u) * kTile + uint32_t(row >> 6) * kAtom;
-                    float x[64];  // out, all 64 tokens of this row
+                    const size_t at = (tok * hv + w.h) * dz + 32 * quarter;
+                    float d[16];  // dots of this thread's 16 tokens over its 4 rows
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        float x1[32], x2[32];
-                        tmem_ld32(trow + K::kColX1 + 32 * p, x1);
-                        tmem_ld32(trow + K::kColX2 + 32 * p, x2);
+                    for (int p = 0; p < 2; ++p) {  // 32 tokens
+                        float x1[2][16], x2[2][16];
+#pragma unroll
+                        for (int l = 0; l < 2; ++l) {
+                            tmem_ld_frag(tq + (uint32_t(16 * l) << 16) + K::kColX1 + 32 * p, x1[l]);
+                            tmem_ld_frag(tq + (uint32_t(16 * l) << 16) + K::kColX2 + 32 * p, x2[l]);
+                        }
                         tmem_wait_ld();
+                        if (p == 1) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(bar(kBOutFree));
+                        }
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            float wi[4];
-                            load4(win + 32 * p + 4 * q, wi);
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 wi = *reinterpret_cast<const float2 *>(win + 32 * p + 8 * j + tp);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                x1[4 * q + e] *= wi[e];
-                                x[32 * p + 4 * q + e] = x2[4 * q + e] + x1[4 * q + e];
-                            }
+                            for (int l = 0; l < 2; ++l)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    x1[l][4 * j + e] *= (e & 1) ? wi.y : wi.x;
+                                    x2[l][4 * j + e] += x1[l][4 * j + e];
+                                }
                         }
                         if constexpr (kDots) {
                             if (a.aux) {
+                                const uint32_t aux = sb + K::kOffAux + (mm & 1u) * kTile + uint32_t(quarter >> 1) * kAtom;
 #pragma unroll
-                                for (int q = 0; q < 2; ++q) {
-                                    float d[16];
+                                for (int j = 0; j < 4; ++j) {
+                                    // tiles: tokens 8 j .. 8 j + 7, z 8 i .. 8 i + 7 of this quarter, i = lane / 8
+                                    const uint32_t r = uint32_t(32 * p + 8 * j + (lane & 7));
+                                    const uint32_t ch = uint32_t(4 * (quarter & 1) + (lane >> 3));
+                                    uint32_t q[4];
+                                    ldmatrix_t(aux + r * 128 + ((ch ^ (r & 7)) << 4), q);
+                                    float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-                                    for (int e = 0; e < 16; ++e) {
-                                        const int r = 32 * p + 16 * q + e;
-                                        unsigned short b;
-                                        const uint32_t ad = aux + uint32_t(r) * 128 +
-                                                            ((uint32_t((row & 63) >> 3) ^ uint32_t(r & 7)) << 4) + 2 * (row & 7);
-                                        asm volatile("ld.shared.b16 %0, [%1];" : "=h"(b) : "r"(ad) : "memory");
-                                        d[e] = row < dz ? __uint_as_float(uint32_t(b) << 16) * x1[16 * q + e] : 0.f;
+                                    for (int i = 0; i < 4; ++i) {
+                                        s0 = fmaf(bf_lo(q[i]), x1[i >> 1][4 * j + 2 * (i & 1)], s0);
+                                        s1 = fmaf(bf_hi(q[i]), x1[i >> 1][4 * j + 2 * (i & 1) + 1], s1);
                                     }
-                                    const float s = warp_colsum16(d, lane);
-                                    if ((lane & 1) == 0) red[quarter * 64 + 32 * p + 16 * q + (lane >> 1)] = s;
+                                    d[8 * p + 2 * j] = s0;
+                                    d[8 * p + 2 * j + 1] = s1;
+                                }
+                            }
+                        }
+                        if (!a.out_f32) {
+                            // bf16 token pairs, transposed into rows of 64 bytes (four 16-byte pieces, swizzled) per token
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t r = uint32_t(32 * p + 8 * j + (lane & 7));
+                                const uint32_t ch = uint32_t(lane >> 3);
+                                stmatrix_t(stage_u + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4),
+                                           pack_bf16x2(x2[0][4 * j], x2[0][4 * j + 1]),
+                                           pack_bf16x2(x2[0][4 * j + 2], x2[0][4 * j + 3]),
+                                           pack_bf16x2(x2[1][4 * j], x2[1][4 * j + 1]),
+                                           pack_bf16x2(x2[1][4 * j + 2], x2[1][4 * j + 3]));
+                            }
+                        } else {
+                            // fp32, 16 tokens at a time: rows of 36 floats (a token pair's lanes fall into other banks)
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                __syncwarp();
+#pragma unroll
+                                for (int j = 2 * q; j < 2 * q + 2; ++j)
+#pragma unroll
+                                    for (int l = 0; l < 2; ++l)
+#pragma unroll
+                                        for (int e = 0; e < 4; ++e)
+                                            stage[(8 * (j & 1) + tp + (e & 1)) * 36 + 16 * l + 8 * (e >> 1) + (lane >> 2)] =
+                                                x2[l][4 * j + e];
+                                __syncwarp();
+                                float *o = static_cast<float *>(a.out) + at;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const int r = 4 * i + (lane >> 3), c = 4 * (lane & 7), tk = 32 * p + 16 * q + r;
+                                    if (tk < L && 32 * quarter + c < dz)
+                                        *reinterpret_cast<float4 *>(o + tk * step + c) =
+                                            *reinterpret_cast<const float4 *>(stage + r * 36 + c);
                                 }
                             }
                         }
                     }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(bar(kBOutFree));
-                        if (kDots && a.aux) mbar_arrive(bar(kBAFree + int(mm & 1u)));
-                    }
-                    if (row < dz) {
-                        if (a.out_f32) {
-                            float *o = static_cast<float *>(a.out) + at;
-                            if (L == 64) {
+                    if (!a.out_f32) {
+                        __syncwarp();
+                        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.out) + at;
 #pragma unroll
-                                for (int r = 0; r < 64; ++r) __stcs(o + r * step, x[r]);
-                            } else {
-#pragma unroll
-                                for (int r = 0; r < 64; ++r)
-                                    if (r < L) o[r * step] = x[r];
-                            }
-                        } else {
-                            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.out) + at;
-                            if (L == 64) {
-#pragma unroll
-                                for (int r = 0; r < 64; ++r) o[r * step] = __float2bfloat16_rn(x[r]);
-                            } else {
-#pragma unroll
-                                for (int r = 0; r < 64; ++r)
-                                    if (r < L) o[r * step] = __float2bfloat16_rn(x[r]);
-                            }
+                        for (int i = 0; i < 8; ++i) {
+                            const uint32_t r = uint32_t(8 * i + (lane >> 2)), ch = uint32_t(lane & 3);
+                            const uint4 q = ld_shared_v4(stage_u + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
+                            if (int(r) < L && 32 * quarter + 8 * int(ch) < dz)
+                                *reinterpret_cast<uint4 *>(o + r * step + 8 * ch) = q;
                         }
+                        __syncwarp();
                     }
                     if (kDots && a.aux) {
+                        // sums over the 8 lanes of a token pair: halving exchanges leave two of the 16 values
+#pragma unroll
+                        for (int c = 8, bit = 16; c >= 2; c >>= 1, bit >>= 1) {
+                            const bool up = (lane & bit) != 0;
+#pragma unroll
+                            for (int e = 0; e < c; ++e) {
+                                const float send = up ? d[e] : d[e + c], keep = up ? d[e + c] : d[e];
+                                d[e] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
+                            }
+                        }
+                        // lane bits 16, 8, 4 chose p, and two bits of the group of 8 tokens
+                        const int grp = ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
+                        *reinterpret_cast<float2 *>(red + quarter * 64 + 8 * grp + tp) = make_float2(d[0], d[1]);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(kBAFree + int(mm & 1u)));
                         named_sync(kBarOut, 128);
                         if (ot < L)
                             a.dot[size_t(w.h) * a.tokens + tok + ot] =
@@ -468,16 +537,17 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
             }
         }
     } else if (warp < kWarpTma) {
-        // ============ prep warps: decays, w y in three terms, P ============
+        // ============ prep warps: decays, w z in three terms, P ============
         const int pt = tid - 32 * kWarpPrep, quarter = warp & 3;
+        const uint32_t tq = tmem + (uint32_t(quarter * 32) << 16);
         while (w.next(kSt)) {
             const float *g = a.g_const ? a.g + w.h : a.g + size_t(w.seg.start) * hv + w.h;
             const size_t gs = a.g_const ? 0 : hv;
             float g0 = 0.f, g1 = 0.f;
-            auto load_g = [&](int n) {  // this lane's two tokens of the n-th chunk
+            auto load_g = [&](int n) {  // this lane's two tokens of the n-th chunk (floored where they are used)
                 const int t = w.chunk_at(n) + 2 * lane;
-                g0 = t < w.seg.len ? fmaxf(g[size_t(t) * gs], kGFloor) : 0.f;
-                g1 = t + 1 < w.seg.len ? fmaxf(g[size_t(t + 1) * gs], kGFloor) : 0.f;
+                g0 = t < w.seg.len ? g[size_t(t) * gs] : 0.f;
+                g1 = t + 1 < w.seg.len ? g[size_t(t + 1) * gs] : 0.f;
             };
             if (quarter == 0 && w.nch > 0) load_g(0);
             for (int n = 0; n < w.nch; ++n) {
@@ -486,7 +556,9 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                 float *vec = vecs(mm);
                 if (quarter == 0) {
                     // prefix sums and suffix sums (each without a subtraction)
-                    float pre = g0 + g1, suf = g0 + g1;
+                    const float a0 = fmaxf(g0, kGFloor), a1 = fmaxf(g1, kGFloor);
+                    if (n + 1 < w.nch) load_g(n + 1);
+                    float pre = a0 + a1, suf = a0 + a1;
 #pragma unroll
                     for (int d = 1; d < 32; d <<= 1) {
                         const float u = __shfl_up_sync(0xffffffffu, pre, d), v = __shfl_down_sync(0xffffffffu, suf, d);
@@ -496,7 +568,7 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                     float before = __shfl_up_sync(0xffffffffu, pre, 1), after = __shfl_down_sync(0xffffffffu, suf, 1);
                     if (lane == 0) before = 0.f;
                     if (lane == 31) after = 0.f;
-                    const float G0 = before + g0, G1 = pre, R0 = g1 + after, R1 = after;
+                    const float G0 = before + a0, G1 = pre, R0 = a1 + after, R1 = after;
                     const float total = __shfl_sync(0xffffffffu, pre, 31);
                     const float e0 = expf(G0), e1 = expf(G1), f0 = expf(R0), f1 = expf(R1);
                     constexpr float kLog2e = 1.4426950408889634f;
@@ -504,68 +576,89 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                     *reinterpret_cast<float2 *>(vec + kVecIn + 2 * lane) = a.reverse ? make_float2(f0, f1) : make_float2(e0, e1);
                     *reinterpret_cast<float2 *>(vec + kVecSt + 2 * lane) = a.reverse ? make_float2(e0, e1) : make_float2(f0, f1);
                     if (lane == 0) vec[kVecGamma] = expf(total);
-                    if (n + 1 < w.nch) load_g(n + 1);
                 }
                 // the four warps go on, or stop, together
                 if (named_sync_or(kBarPrep, 128, !ok)) {
                     ok = false;
                     goto prep_done;
                 }
-                if (pt == 0) mbar_arrive(bar(kBVec + int(mm & 1u)));
-                // w y in three bf16 terms, over the previous chunk's
-                ok = warp_wait(bar(kBY + int(mm % K::kNY)), (mm / K::kNY) & 1u);
-                if (ok && mm > 0) ok = warp_wait(bar(kBKV), (mm - 1) & 1u);
-                if (!ok) continue;
-                {
-                    const uint32_t ys = sb + K::kOffYs, yt = sb + K::kOffY + (mm % K::kNY) * kTile;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        // 16 bytes of row r: eight rows and their swizzle stay within a warp's reach
-                        const int e = pt + 128 * i, r = (e >> 3) & 63;
-                        const uint32_t off = uint32_t(e) * 16;
-                        if (e >= 512 * ya) break;
-                        const uint4 q = ld_shared_v4(yt + off);
-                        const uint32_t ws[4] = {q.x, q.y, q.z, q.w};
-                        const float wt = vec[kVecSt + r];
-                        uint32_t t0w[4], t1w[4], t2w[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            float lo = r < L ? bf_lo(ws[j]) * wt : 0.f, hi = r < L ? bf_hi(ws[j]) * wt : 0.f;
-                            t0w[j] = pack_bf16x2(lo, hi);
-                            lo -= bf_lo(t0w[j]);
-                            hi -= bf_hi(t0w[j]);
-                            t1w[j] = pack_bf16x2(lo, hi);
-                            lo -= bf_lo(t1w[j]);
-                            hi -= bf_hi(t1w[j]);
-                            t2w[j] = pack_bf16x2(lo, hi);
+                const uint32_t zs = mm % kRing, ring_phase = (mm / kRing) & 1u;
+                const uint32_t zt = sb + K::kOffZ + zs * kTile;
+                ok = warp_wait(bar(kBZ + int(zs)), ring_phase);
+                if (L < kDecayChunk) {
+                    // tokens past the end are another sequence's: their y and z, whatever they hold, must not meet
+                    // a zero weight
+                    if (ok) ok = warp_wait(bar(kBY + int(zs)), ring_phase);
+                    const uint32_t yt = sb + K::kOffY + zs * kTile;
+                    for (int e = pt; e < 1024 && ok; e += 128)
+                        if (((e >> 3) & 63) >= L) {
+                            st_shared_v4(zt + uint32_t(e) * 16, make_uint4(0u, 0u, 0u, 0u));
+                            if (e < 512 * ya) st_shared_v4(yt + uint32_t(e) * 16, make_uint4(0u, 0u, 0u, 0u));
                         }
-                        st_shared_v4(ys + off, make_uint4(t0w[0], t0w[1], t0w[2], t0w[3]));
-                        st_shared_v4(ys + kTile + off, make_uint4(t1w[0], t1w[1], t1w[2], t1w[3]));
-                        st_shared_v4(ys + 2 * kTile + off, make_uint4(t2w[0], t2w[1], t2w[2], t2w[3]));
+                    fence_proxy_async_shared();
+                    if (named_sync_or(kBarPrep, 128, !ok)) {
+                        ok = false;
+                        goto prep_done;
                     }
                 }
-                if (L < kDecayChunk) {
-                    // tokens past the end are another sequence's: their z, whatever it holds, must not meet a zero weight
-                    const uint32_t zs = mm % K::kNZ, zt = sb + K::kOffZ + zs * kTile;
-                    ok = warp_wait(bar(kBZ + int(zs)), (mm / K::kNZ) & 1u);
-                    if (!ok) continue;
-                    for (int e = pt; e < 1024; e += 128)
-                        if (((e >> 3) & 63) >= L) st_shared_v4(zt + uint32_t(e) * 16, make_uint4(0u, 0u, 0u, 0u));
+                if (!ok) continue;
+                // w z, half a chunk at a time: transposed reads give token pairs of a z row, the layout of a
+                // tensor-memory A operand
+                for (int hf = 0; hf < 2; ++hf) {
+                    uint32_t q[4][4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t r = uint32_t(32 * hf + 8 * j + (lane & 7)), ch = uint32_t(4 * (quarter & 1) + (lane >> 3));
+                        ldmatrix_t(zt + uint32_t(quarter >> 1) * kAtom + r * 128 + ((ch ^ (r & 7)) << 4), q[j]);
+                    }
+                    // the half's columns were read by KV: of the chunk before, or (one half's room) of the half before
+                    const uint32_t col = K::kColW + (K::kWz == 2 ? 48u * hf : 0u);
+                    if (K::kWz == 2) {
+                        if (mm > 0) ok = warp_wait(bar(hf ? kBKV1 : kBKV0), (mm - 1) & 1u);
+                    } else if (hf) {
+                        ok = warp_wait(bar(kBKV0), mm & 1u);
+                    } else if (mm > 0) {
+                        ok = warp_wait(bar(kBKV1), (mm - 1) & 1u);
+                    }
+                    if (!ok) break;
+                    tc_fence_after();
+                    // registers of a store: token group j (two registers each: z rows i and i + 1 of the half quarter)
+#pragma unroll
+                    for (int l = 0; l < 2; ++l) {
+                        uint32_t t0w[8], t1w[8], t2w[8];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 wt = *reinterpret_cast<const float2 *>(vec + kVecSt + 32 * hf + 8 * j + 2 * (lane & 3));
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                float lo = bf_lo(q[j][2 * l + i]) * wt.x, hi = bf_hi(q[j][2 * l + i]) * wt.y;
+                                t0w[2 * j + i] = pack_bf16x2(lo, hi);
+                                lo -= bf_lo(t0w[2 * j + i]);
+                                hi -= bf_hi(t0w[2 * j + i]);
+                                t1w[2 * j + i] = pack_bf16x2(lo, hi);
+                                lo -= bf_lo(t1w[2 * j + i]);
+                                hi -= bf_hi(t1w[2 * j + i]);
+                                t2w[2 * j + i] = pack_bf16x2(lo, hi);
+                            }
+                        }
+                        const uint32_t dst = tq + (uint32_t(16 * l) << 16) + col;
+                        tmem_st_frag(dst, t0w);
+                        tmem_st_frag(dst + 16, t1w);
+                        tmem_st_frag(dst + 32, t2w);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kBW + hf));
                 }
-                fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(bar(kBYs));
-                    mbar_arrive(bar(kBYFree + int(mm % K::kNY)));
-                }
+                if (!ok) continue;
                 if constexpr (!kSt) {
-                    const uint32_t qb = K::kQkBufs == 2 ? (mm & 1u) : 0u;
-                    ok = K::kQkBufs == 2 ? warp_wait(bar(kBQK + int(qb)), (mm >> 1) & 1u) : warp_wait(bar(kBQK), mm & 1u);
+                    ok = warp_wait(bar(kBQK), mm & 1u);
                     if (ok && mm >= 2) ok = warp_wait(bar(kBPFree + int(mm & 1u)), ((mm >> 1) - 1) & 1u);
                     if (!ok) continue;
                     tc_fence_after();
                     float v[32];
-                    tmem_ld_m64(tmem + (uint32_t(quarter * 32) << 16) + K::kColQK + 64 * qb, v);
+                    tmem_ld_m64(tq + K::kColQK, v);
                     tmem_wait_ld();
                     const int r = 16 * quarter + (lane & 15), cb = lane < 16 ? 0 : 32;
                     const float Gr = vec[kVecG + r];
@@ -596,126 +689,132 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
         }
     prep_done:;
     } else if (warp == kWarpTma) {
-        if (lane == 0) {
+        if (elect_one()) {
             const uint32_t bytes_y = kAtom * uint32_t(ya);
             while (ok && w.next(kSt)) {
-                const int hx = w.h / (hv / a.hx), hy = w.h / (hv / a.hy), hz = w.h / (hv / a.hz);
+                const int hx = kSt ? 0 : w.h / (hv / a.hx), hy = w.h / (hv / a.hy), hz = w.h / (hv / a.hz);
                 const int ha = kDots && a.aux ? w.h / (hv / a.haux) : 0;
                 for (int n = 0; n < w.nch; ++n) {
                     const uint32_t mm = m + uint32_t(n);
                     const int tok = w.seg.start + w.chunk_at(n);
+                    const uint32_t s = mm % kRing, freed = (mm / kRing - 1) & 1u;
+                    const bool wait = mm >= uint32_t(kRing);
+                    {
+                        const uint32_t dst = sb + K::kOffY + s * kTile, b = bar(kBY + int(s));
+                        if (wait) ok = mbar_wait(bar(kBYFree + int(s)), freed);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(b, bytes_y);
+                        tma_load_3d(dst, &tm.y, 0, hy, tok, b);
+                        if (ya == 2) tma_load_3d(dst + kAtom, &tm.y, 64, hy, tok, b);
+                    }
                     if constexpr (!kSt) {
-                        const uint32_t s = mm % K::kNX, dst = sb + K::kOffX + s * kTile;
-                        if (mm >= uint32_t(K::kNX)) ok = mbar_wait(bar(kBXFree + int(s)), (mm / K::kNX - 1) & 1u);
+                        const uint32_t dst = sb + K::kOffX + s * kTile, b = bar(kBX + int(s));
+                        if (wait) ok = mbar_wait(bar(kBXFree + int(s)), freed);
                         if (!ok) break;
-                        mbar_arrive_expect_tx(bar(kBX + int(s)), bytes_y);
-                        tma_load_3d(dst, &tm.x, 0, hx, tok, bar(kBX + int(s)));
-                        if (ya == 2) tma_load_3d(dst + kAtom, &tm.x, 64, hx, tok, bar(kBX + int(s)));
+                        mbar_arrive_expect_tx(b, bytes_y);
+                        tma_load_3d(dst, &tm.x, 0, hx, tok, b);
+                        if (ya == 2) tma_load_3d(dst + kAtom, &tm.x, 64, hx, tok, b);
                     }
                     {
-                        const uint32_t s = mm % K::kNY, dst = sb + K::kOffY + s * kTile;
-                        if (mm >= uint32_t(K::kNY)) ok = mbar_wait(bar(kBYFree + int(s)), (mm / K::kNY - 1) & 1u);
+                        const uint32_t dst = sb + K::kOffZ + s * kTile, b = bar(kBZ + int(s));
+                        if (wait) ok = mbar_wait(bar(kBZFree + int(s)), freed);
                         if (!ok) break;
-                        mbar_arrive_expect_tx(bar(kBY + int(s)), bytes_y);
-                        tma_load_3d(dst, &tm.y, 0, hy, tok, bar(kBY + int(s)));
-                        if (ya == 2) tma_load_3d(dst + kAtom, &tm.y, 64, hy, tok, bar(kBY + int(s)));
-                    }
-                    {
-                        const uint32_t s = mm % K::kNZ, dst = sb + K::kOffZ + s * kTile;
-                        if (mm >= uint32_t(K::kNZ)) ok = mbar_wait(bar(kBZFree + int(s)), (mm / K::kNZ - 1) & 1u);
-                        if (!ok) break;
-                        mbar_arrive_expect_tx(bar(kBZ + int(s)), kTile);
-                        tma_load_3d(dst, &tm.z, 0, hz, tok, bar(kBZ + int(s)));
-                        tma_load_3d(dst + kAtom, &tm.z, 64, hz, tok, bar(kBZ + int(s)));
+                        mbar_arrive_expect_tx(b, kTile);
+                        tma_load_3d(dst, &tm.z, 0, hz, tok, b);
+                        tma_load_3d(dst + kAtom, &tm.z, 64, hz, tok, b);
                     }
                     if (kDots && a.aux) {
-                        const uint32_t s = mm & 1u, dst = sb + K::kOffAux + s * kTile;
-                        if (mm >= 2) ok = mbar_wait(bar(kBAFree + int(s)), ((mm >> 1) - 1) & 1u);
+                        const uint32_t i = mm & 1u, dst = sb + K::kOffAux + i * kTile, b = bar(kBA + int(i));
+                        if (mm >= 2) ok = mbar_wait(bar(kBAFree + int(i)), ((mm >> 1) - 1) & 1u);
                         if (!ok) break;
-                        mbar_arrive_expect_tx(bar(kBA + int(s)), kTile);
-                        tma_load_3d(dst, &tm.aux, 0, ha, tok, bar(kBA + int(s)));
-                        tma_load_3d(dst + kAtom, &tm.aux, 64, ha, tok, bar(kBA + int(s)));
+                        mbar_arrive_expect_tx(b, kTile);
+                        tma_load_3d(dst, &tm.aux, 0, ha, tok, b);
+                        tma_load_3d(dst + kAtom, &tm.aux, 64, ha, tok, b);
                     }
                 }
                 m += uint32_t(w.nch);
             }
         }
-    } else if (lane == 0) {
+    } else if (elect_one()) {
         // ==================== the issuing thread ====================
         uint32_t total = 0;
         while (w.next(kSt)) total += uint32_t(w.nch);
-        const uint32_t id_qk = idesc_bf16(64, 64, false, false), id_kv = idesc_bf16(128, 64 * ya, true, true);
+        const uint32_t id_qk = idesc_bf16(64, 64, false, false), id_kv = idesc_bf16(128, 64 * ya, false, true);
         const uint32_t id_x1 = idesc_bf16(128, 64, false, false), id_x2 = idesc_bf16(128, 64, true, false);
-        const int ksteps = 4 * ya;
         auto koff = [](int s) { return uint64_t(((s >> 2) * kAtom + (s & 3) * 32) >> 4); };  // K-major steps
         auto issue_qk = [&](uint32_t c) {
-            const uint32_t s = c % K::kNX, t = c % K::kNY;
-            bool good = mbar_wait(bar(kBX + int(s)), (c / K::kNX) & 1u) && mbar_wait(bar(kBY + int(t)), (c / K::kNY) & 1u);
-            if (!good) return false;
+            const uint32_t s = c % kRing, ph = (c / kRing) & 1u;
+            if (!mbar_wait(bar(kBX + int(s)), ph) || !mbar_wait(bar(kBY + int(s)), ph)) return false;
+            // (with shared columns: the out warps have read the previous X2)
+            if (K::kColQK == K::kColX2 && c > 0 && !mbar_wait(bar(kBOutFree), (c - 1) & 1u)) return false;
             tc_fence_after();
-            const uint64_t dx = smem_desc(sb + K::kOffX + s * kTile, 16, 1024), dyd = smem_desc(sb + K::kOffY + t * kTile, 16, 1024);
-            const uint32_t qb = K::kQkBufs == 2 ? (c & 1u) : 0u;
-            for (int i = 0; i < ksteps; ++i) mma_bf16(tmem + K::kColQK + 64 * qb, dx + koff(i), dyd + koff(i), id_qk, i > 0);
-            mma_commit(bar(kBQK + int(qb)));
-            mma_commit(bar(kBYFree + int(t)));
+            const uint64_t dx = smem_desc(sb + K::kOffX + s * kTile, 16, 1024), dyd = smem_desc(sb + K::kOffY + s * kTile, 16, 1024);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < 4 * ya) mma_bf16(tmem + K::kColQK, dx + koff(i), dyd + koff(i), id_qk, i > 0);
+            mma_commit(bar(kBQK));
             return true;
         };
         auto issue_kv = [&](uint32_t c) {
-            const uint32_t s = c % K::kNZ;
-            bool good = mbar_wait(bar(kBSt), c & 1u) && mbar_wait(bar(kBYs), c & 1u) &&
-                        mbar_wait(bar(kBZ + int(s)), (c / K::kNZ) & 1u);
-            if (!good) return false;
-            tc_fence_after();
-            const uint64_t da = smem_desc(sb + K::kOffZ + s * kTile, 8192, 1024);
+            const uint32_t s = c % kRing;
+            if (!mbar_wait(bar(kBY + int(s)), (c / kRing) & 1u)) return false;
+            if (c > 0 && !mbar_wait(bar(kBLFree), (c - 1) & 1u)) return false;
+            const uint64_t db = smem_desc(sb + K::kOffY + s * kTile, 8192, 1024);
 #pragma unroll
-            for (int t = 0; t < 3; ++t) {
-                const uint64_t db = smem_desc(sb + K::kOffYs + uint32_t(t) * kTile, 8192, 1024);
+            for (int hf = 0; hf < 2; ++hf) {
+                if (!mbar_wait(bar(kBW + hf), c & 1u)) return false;
+                tc_fence_after();
+                const uint32_t col = tmem + K::kColW + (K::kWz == 2 ? 48u * hf : 0u);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    mma_bf16(tmem + K::kColS, da + uint64_t((i * 2048) >> 4), db + uint64_t((i * 2048) >> 4), id_kv, 1);
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int t = 0; t < 3; ++t)
+                        mma_bf16_ts(tmem + K::kColL, col + 16 * t + 8 * i, db + uint64_t(((2 * hf + i) * 2048) >> 4), id_kv,
+                                    hf > 0 || i > 0 || t > 0);
+                mma_commit(bar(hf ? kBKV1 : kBKV0));
             }
-            mma_commit(bar(kBKV));
+            mbar_arrive(bar(kBKV1));
+            mma_commit(bar(kBYFree + int(s)));
             if (kSt) mma_commit(bar(kBZFree + int(s)));
             return true;
         };
-        auto issue_x1 = [&](uint32_t c) {
-            const uint32_t s = c % K::kNX;
-            bool good = mbar_wait(bar(kBSt), c & 1u);
-            if (good && c > 0) good = mbar_wait(bar(kBOutFree), (c - 1) & 1u);
-            if (!good) return false;
+        auto issue_x = [&](uint32_t c) {
+            const uint32_t s = c % kRing;
+            if (!mbar_wait(bar(kBSt), c & 1u)) return false;
+            if (c > 0 && !mbar_wait(bar(kBOutFree), (c - 1) & 1u)) return false;
             tc_fence_after();
             const uint64_t dx = smem_desc(sb + K::kOffX + s * kTile, 16, 1024);
-            const uint32_t cb = tmem + K::kColC + (K::kCopies == 1 ? 64u * (c & 1u) : 0u);
 #pragma unroll
             for (int t = 0; t < K::kCopies; ++t)
-                for (int i = 0; i < ksteps; ++i)
-                    mma_bf16_ts(tmem + K::kColX1, cb + 64 * t + 8 * i, dx + koff(i), id_x1, t > 0 || i > 0);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < 4 * ya)
+                        mma_bf16_ts(tmem + K::kColX1, tmem + K::kColC + 64 * t + 8 * i, dx + koff(i), id_x1, t > 0 || i > 0);
+            mma_commit(bar(kBX1));
+            mma_commit(bar(kBXFree + int(s)));
+            if (!mbar_wait(bar(kBP + int(c & 1u)), (c >> 1) & 1u)) return false;
+            tc_fence_after();
+            const uint64_t da = smem_desc(sb + K::kOffZ + s * kTile, 8192, 1024);
+            const uint64_t db = smem_desc(sb + K::kOffP + (c & 1u) * kPTile, 16, 1024);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                mma_bf16(tmem + K::kColX2, da + uint64_t((i * 2048) >> 4), db + uint64_t((i * 32) >> 4), id_x2, i > 0);
+            mma_commit(bar(kBOut));
+            mbar_arrive(bar(kBOut));
+            mma_commit(bar(kBZFree + int(s)));
+            mma_commit(bar(kBPFree + int(c & 1u)));
             return true;
         };
-        if (!kSt && ok && total > 0) ok = issue_qk(0);
-        for (uint32_t c = 0; ok && c < total; ++c) {
-            if constexpr (kSt) {
-                ok = issue_kv(c);
-            } else {
-                if (K::kCopies == 1) ok = issue_kv(c) && issue_x1(c);
-                else ok = issue_x1(c) && issue_kv(c);
-                if (!ok) break;
-                const uint32_t s = c % K::kNZ;
-                ok = mbar_wait(bar(kBP + int(c & 1u)), (c >> 1) & 1u);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t da = smem_desc(sb + K::kOffZ + s * kTile, 8192, 1024);
-                const uint64_t db = smem_desc(sb + K::kOffP + (c & 1u) * kPTile, 16, 1024);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    mma_bf16(tmem + K::kColX2, da + uint64_t((i * 2048) >> 4), db + uint64_t((i * 32) >> 4), id_x2, i > 0);
-                mma_commit(bar(kBOut));
-                mbar_arrive(bar(kBOut));
-                mma_commit(bar(kBXFree + int(c % K::kNX)));
-                mma_commit(bar(kBZFree + int(s)));
-                mma_commit(bar(kBPFree + int(c & 1u)));
-                if (c + 1 < total) ok = issue_qk(c + 1);
-            }
+        if constexpr (kSt) {
+            for (uint32_t c = 0; ok && c < total; ++c) ok = issue_kv(c);
+        } else if constexpr (K::kCopies == 1) {
+            if (total > 0) ok = ok && issue_qk(0);
+            for (uint32_t c = 0; ok && c < total; ++c)
+                ok = issue_kv(c) && issue_x(c) && (c + 1 == total || issue_qk(c + 1));
+        } else {
+            if (total > 0) ok = ok && issue_kv(0) && issue_qk(0);
+            for (uint32_t c = 0; ok && c < total; ++c)
+                ok = issue_x(c) && (c + 1 == total || (issue_kv(c + 1) && issue_qk(c + 1)));
         }
         // every product done before the tensor memory goes
         mma_commit(bar(kBDrain));
