@@ -27,17 +27,18 @@
 // in a bf16 output, and one bf16 copy costs it as much as the output's own
 // rounding.  P is one bf16 term for the same reason.
 //
-// Roles (18 warps):
-//   state warps 0-7    two per tensor-memory quarter, 64 state columns each
-//   out warps 8-11     X1, X2 -> out (and the dot with aux)
-//   prep warps 12-15   decays, w z in three terms, P from QK
-//   warp 16            TMA loads;  warp 17  issues every product, in the order
-//                      KV(n), X1(n), X2(n), QK(n + 1), which leaves P(n + 1)
-//                      the time of KV(n + 1) and X1(n + 1).  With three copies
-//                      of Sigma X1 alone is that long, and tensor memory is
-//                      full: X2 shares QK's columns, w z has room for half a
-//                      chunk, and the order is X1(n), X2(n), KV(n + 1),
-//                      QK(n + 1).
+// Roles (7 warpgroups; a role's warps are latency-bound, so the work is spread
+// until the products set the pace):
+//   0-7     state      two warps per tensor-memory quarter, 64 columns each
+//   8-11    out        X1, X2 -> out (and the dot with aux)
+//   12-19   split      w z in three terms, 32 tokens of the chunk a warpgroup
+//   20-23   mask       P from QK
+//   24 TMA loads, 25 products, 26 decays (27 only fills the warpgroup)
+// The registers go where the state is (setmaxnreg).  Products are issued in
+// the order KV(n), X1(n), X2(n), QK(n + 1), which leaves P(n + 1) the time of
+// KV(n + 1) and X1(n + 1).  With three copies of Sigma X1 alone is that long,
+// and tensor memory is full: X2 shares QK's columns, w z has room for half a
+// chunk, and the order is X1(n), X2(n), KV(n + 1), QK(n + 1).
 // All hand-overs are mbarriers with bounded waits; a timeout records
 // GDN_ERR_DEVICE_CHECK (bad_index -2).  A CTA takes units (segment, head) with
 // a stride of the grid; nothing synchronises it between units.
@@ -51,9 +52,14 @@ using namespace sm100;
 
 namespace {
 
-constexpr int kThreads = 576;
-constexpr int kWarpOut = 8, kWarpPrep = 12, kWarpTma = 16, kWarpMma = 17;
-constexpr int kBarPrep = 1, kBarOut = 2;  // named barriers (128 threads each)
+constexpr int kThreads = 896;
+constexpr int kWarpOut = 8, kWarpSplit = 12, kWarpMask = 20, kWarpTma = 24, kWarpMma = 25, kWarpGate = 26;
+constexpr int kBarOut = 1, kBarSplit = 2;  // named barriers (128 threads each; one for each split warpgroup)
+// Registers a thread: 72 at launch (896 threads: 64,512), then by role; the
+// sum over the seven warpgroups, 128 (2 x 104 + 80 + 3 x 56 + 40) = 63,488,
+// stays below what the block was launched with.
+constexpr int kRegsLaunch = 72, kRegsState = 104, kRegsOut = 80, kRegsWork = 56, kRegsCtl = 40;
+static_assert(128 * (2 * kRegsState + kRegsOut + 3 * kRegsWork + kRegsCtl) <= kThreads * kRegsLaunch, "registers");
 constexpr uint32_t kTile = 16384, kAtom = 8192, kPTile = 8192;
 constexpr uint32_t kTmemCols = 512;
 
@@ -78,7 +84,7 @@ template <int kKind> struct Cfg {
     static constexpr uint32_t kOffVec = kOffOut + kTile;                           // [4]
     static constexpr uint32_t kOffRed = kOffVec + 4 * kVecFloats * 4;              // [4 warps][64]
     static constexpr uint32_t kOffBar = kOffRed + 1024;
-    static constexpr uint32_t kSmem = kOffBar + 320 + 1024;
+    static constexpr uint32_t kSmem = kOffBar + 384 + 1024;
     static_assert(kSmem <= 232448, "shared memory over the sm_100 per-block limit");
     // tensor memory columns
     static constexpr uint32_t kColL = 0, kColC = 128;  // L; the copies of Sigma (64 columns a term)
@@ -98,19 +104,21 @@ enum {
     kBZFree = 14,   // [3] X2 done (w z was taken before KV)
     kBYFree = 17,   // [3] KV (and QK) done
     kBAFree = 20,   // [2] dot taken (4 out warps)
-    kBW = 22,       // [2] a half chunk of w z written (4 prep warps)
+    kBW = 22,       // [2] a half chunk of w z written (4 split warps)
     kBKV0 = 24,     // KV of the first half done
     kBKV1 = 25,     // KV done (and an arrival of the issuing thread, which orders the token vectors)
     kBLFree = 26,   // L read (8 state warps)
     kBSt = 27,      // copies of Sigma written (8 state warps)
     kBX1 = 28,      // X1 done
     kBQK = 29,      // QK done
-    kBP = 30,       // [2] P written (4 prep warps)
+    kBP = 30,       // [2] P written (4 mask warps)
     kBPFree = 32,   // [2] X2 done
     kBOut = 34,     // X1, X2 done (and an arrival of the issuing thread)
     kBOutFree = 35, // X1, X2 read (4 out warps)
-    kBDrain = 36,
-    kNumBars = 37
+    kBVec = 36,     // [4] token vectors written
+    kBVecFree = 40, // [4] token vectors read (8 state warps, 4 out warps)
+    kBDrain = 44,
+    kNumBars = 45
 };
 
 struct Maps {
@@ -143,39 +151,39 @@ struct UnitWalk {
     __device__ int chunk_at(int n) const { return kDecayChunk * (a.reverse ? nch - 1 - n : n); }
 };
 
+// A bounded wait that leaves the issue slots to the others: the thread is
+// suspended until the phase completes or kIdleNs pass.
+constexpr uint32_t kIdleNs = 1000000;
+__device__ __forceinline__ bool idle_wait(uint32_t bar, uint32_t parity) {
+    for (int i = 0; i < 2000; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(kIdleNs)
+            : "memory");
+        if (ok) return true;
+    }
+    return false;
+}
+
 // A bounded wait of a whole warp; every lane gets the same answer.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+    return __all_sync(0xffffffffu, idle_wait(bar, parity));
 }
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// Rows 16 (warp % 4) + lane % 16 of an M = 64 accumulator, columns 0-31 in
-// lanes 0-15 and 32-63 in lanes 16-31.
-__device__ __forceinline__ void tmem_ld_m64(uint32_t taddr, float (&v)[32]) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x32bx2.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32], 32;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr)
-        : "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-// 32 columns of 16 lanes in fragments: registers 4 j .. 4 j + 3 hold columns
-// 8 j + 2 (lane % 4) and the next, of lane / 4 and of lane / 4 + 8.
-__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&v)[16]) {
+// Rows 16 (warp % 4) + lane % 16 of an M = 64 accumulator: 16 columns from
+// `taddr` in lanes 0-15, the 16 columns 32 further on in lanes 16-31.
+__device__ __forceinline__ void tmem_ld_m64(uint32_t taddr, float (&v)[16]) {
     uint32_t r[16];
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16], 32;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr)
@@ -183,12 +191,21 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&v)[16]) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
-// 16 columns of 16 lanes: registers 2 j, 2 j + 1 go to column 4 j + lane % 4
-// of lane / 4 and of lane / 4 + 8.
-__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+
+// 16 columns of 16 lanes in fragments: registers 4 j .. 4 j + 3 hold columns
+// 8 j + 2 (lane % 4) and the next, of lane / 4 and of lane / 4 + 8.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&v)[8]) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
                  : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+// 4 columns of 16 lanes: column lane % 4 of lane / 4 and of lane / 4 + 8.
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)[2]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x1.b32 [%0], {%1, %2};" ::"r"(taddr), "r"(r[0]), "r"(r[1]) : "memory");
 }
 // Four 8 x 8 tiles of 16-bit values, transposed on the way: lane l gives the
 // address of row l % 8 of tile l / 8, and holds elements (row 2 (l % 4) and
@@ -198,6 +215,12 @@ __device__ __forceinline__ void ldmatrix_t(uint32_t addr, uint32_t (&r)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr)
                  : "memory");
+}
+template <int kRegs> __device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs> __device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 __device__ __forceinline__ void stmatrix_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
@@ -225,6 +248,7 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                 n = 4;
             if (i == kBSt || i == kBLFree) n = 8;
             if (i == kBOut || i == kBKV1) n = 2;
+            if (i >= kBVecFree && i < kBVecFree + 4) n = kSt ? 8 : 12;
             mbar_init(bar(i), uint32_t(n));
         }
         fence_mbarrier_init();
@@ -247,6 +271,7 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
 
     if (warp < kWarpOut) {
         // ==================== state warps: thread = state row, 64 columns in registers ====================
+        regs_up<kRegsState>();
         const int half = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t trow = tmem + (uint32_t((warp & 3) * 32) << 16);
         const int c0 = 64 * half;
@@ -339,7 +364,10 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                 dec *= gamma;
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kBLFree));
+                if (lane == 0) {
+                    mbar_arrive(bar(kBLFree));
+                    mbar_arrive(bar(kBVecFree + int(mm & 3u)));
+                }
                 if (kDots && a.zsum && p % a.sched.hdr->ick == 0) {
                     // <Sigma, checkpoint> at the chunk's start
                     const size_t slot = size_t(w.seg.ck + p / a.sched.hdr->ick) * hv + w.h;
@@ -391,8 +419,9 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
             }
             m += uint32_t(w.nch);
         }
-    } else if (warp < kWarpPrep) {
+    } else if (warp < kWarpSplit) {
         // ==================== out warps: 32 z rows each, read in fragments ====================
+        regs_up<kRegsOut>();
         if constexpr (!kSt) {
             const int quarter = warp & 3, ot = tid - 32 * kWarpOut;
             const uint32_t tq = tmem + (uint32_t(quarter * 32) << 16);
@@ -415,24 +444,23 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                     const size_t tok = size_t(w.seg.start) + t0;
                     const size_t step = size_t(hv) * dz;
                     const size_t at = (tok * hv + w.h) * dz + 32 * quarter;
-                    float d[16];  // dots of this thread's 16 tokens over its 4 rows
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {  // 32 tokens
-                        float x1[2][16], x2[2][16];
+#pragma unroll 1
+                    for (int p = 0; p < 4; ++p) {  // 16 tokens (rolled: the roles share the instruction caches)
+                        float x1[2][8], x2[2][8];
 #pragma unroll
                         for (int l = 0; l < 2; ++l) {
-                            tmem_ld_frag(tq + (uint32_t(16 * l) << 16) + K::kColX1 + 32 * p, x1[l]);
-                            tmem_ld_frag(tq + (uint32_t(16 * l) << 16) + K::kColX2 + 32 * p, x2[l]);
+                            tmem_ld_frag(tq + (uint32_t(16 * l) << 16) + K::kColX1 + 16 * p, x1[l]);
+                            tmem_ld_frag(tq + (uint32_t(16 * l) << 16) + K::kColX2 + 16 * p, x2[l]);
                         }
                         tmem_wait_ld();
-                        if (p == 1) {
+                        if (p == 3) {
                             tc_fence_before();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(bar(kBOutFree));
                         }
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 wi = *reinterpret_cast<const float2 *>(win + 32 * p + 8 * j + tp);
+                        for (int j = 0; j < 2; ++j) {
+                            const float2 wi = *reinterpret_cast<const float2 *>(win + 16 * p + 8 * j + tp);
 #pragma unroll
                             for (int l = 0; l < 2; ++l)
 #pragma unroll
@@ -443,11 +471,12 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                         }
                         if constexpr (kDots) {
                             if (a.aux) {
+                                float d[4];  // dots of this thread's 4 tokens over its 4 rows
                                 const uint32_t aux = sb + K::kOffAux + (mm & 1u) * kTile + uint32_t(quarter >> 1) * kAtom;
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) {
+                                for (int j = 0; j < 2; ++j) {
                                     // tiles: tokens 8 j .. 8 j + 7, z 8 i .. 8 i + 7 of this quarter, i = lane / 8
-                                    const uint32_t r = uint32_t(32 * p + 8 * j + (lane & 7));
+                                    const uint32_t r = uint32_t(16 * p + 8 * j + (lane & 7));
                                     const uint32_t ch = uint32_t(4 * (quarter & 1) + (lane >> 3));
                                     uint32_t q[4];
                                     ldmatrix_t(aux + r * 128 + ((ch ^ (r & 7)) << 4), q);
@@ -457,16 +486,30 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                                         s0 = fmaf(bf_lo(q[i]), x1[i >> 1][4 * j + 2 * (i & 1)], s0);
                                         s1 = fmaf(bf_hi(q[i]), x1[i >> 1][4 * j + 2 * (i & 1) + 1], s1);
                                     }
-                                    d[8 * p + 2 * j] = s0;
-                                    d[8 * p + 2 * j + 1] = s1;
+                                    d[2 * j] = s0;
+                                    d[2 * j + 1] = s1;
                                 }
+                                // sums over the 8 lanes of a token pair: two halving exchanges and a plain one
+#pragma unroll
+                                for (int c = 2, bit = 16; c >= 1; c >>= 1, bit >>= 1) {
+                                    const bool up = (lane & bit) != 0;
+#pragma unroll
+                                    for (int e = 0; e < c; ++e) {
+                                        const float send = up ? d[e] : d[e + c], keep = up ? d[e + c] : d[e];
+                                        d[e] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
+                                    }
+                                }
+                                d[0] += __shfl_xor_sync(0xffffffffu, d[0], 4);
+                                // lane bit 16 chose the group of 8 tokens, bit 8 the token of the pair
+                                if ((lane & 4) == 0)
+                                    red[quarter * 64 + 16 * p + 8 * (lane >> 4) + tp + ((lane >> 3) & 1)] = d[0];
                             }
                         }
                         if (!a.out_f32) {
                             // bf16 token pairs, transposed into rows of 64 bytes (four 16-byte pieces, swizzled) per token
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const uint32_t r = uint32_t(32 * p + 8 * j + (lane & 7));
+                            for (int j = 0; j < 2; ++j) {
+                                const uint32_t r = uint32_t(16 * p + 8 * j + (lane & 7));
                                 const uint32_t ch = uint32_t(lane >> 3);
                                 stmatrix_t(stage_u + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4),
                                            pack_bf16x2(x2[0][4 * j], x2[0][4 * j + 1]),
@@ -475,34 +518,32 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                                            pack_bf16x2(x2[1][4 * j + 2], x2[1][4 * j + 3]));
                             }
                         } else {
-                            // fp32, 16 tokens at a time: rows of 36 floats (a token pair's lanes fall into other banks)
+                            // fp32 rows of 36 floats (a token pair's lanes fall into other banks)
+                            __syncwarp();
 #pragma unroll
-                            for (int q = 0; q < 2; ++q) {
-                                __syncwarp();
+                            for (int j = 0; j < 2; ++j)
 #pragma unroll
-                                for (int j = 2 * q; j < 2 * q + 2; ++j)
+                                for (int l = 0; l < 2; ++l)
 #pragma unroll
-                                    for (int l = 0; l < 2; ++l)
+                                    for (int e = 0; e < 4; ++e)
+                                        stage[(8 * j + tp + (e & 1)) * 36 + 16 * l + 8 * (e >> 1) + (lane >> 2)] =
+                                            x2[l][4 * j + e];
+                            __syncwarp();
+                            float *o = static_cast<float *>(a.out) + at;
 #pragma unroll
-                                        for (int e = 0; e < 4; ++e)
-                                            stage[(8 * (j & 1) + tp + (e & 1)) * 36 + 16 * l + 8 * (e >> 1) + (lane >> 2)] =
-                                                x2[l][4 * j + e];
-                                __syncwarp();
-                                float *o = static_cast<float *>(a.out) + at;
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const int r = 4 * i + (lane >> 3), c = 4 * (lane & 7), tk = 32 * p + 16 * q + r;
-                                    if (tk < L && 32 * quarter + c < dz)
-                                        *reinterpret_cast<float4 *>(o + tk * step + c) =
-                                            *reinterpret_cast<const float4 *>(stage + r * 36 + c);
-                                }
+                            for (int i = 0; i < 4; ++i) {
+                                const int r = 4 * i + (lane >> 3), c = 4 * (lane & 7), tk = 16 * p + r;
+                                if (tk < L && 32 * quarter + c < dz)
+                                    *reinterpret_cast<float4 *>(o + tk * step + c) =
+                                        *reinterpret_cast<const float4 *>(stage + r * 36 + c);
                             }
                         }
                     }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kBVecFree + int(mm & 3u)));
                     if (!a.out_f32) {
-                        __syncwarp();
                         __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.out) + at;
-#pragma unroll
+#pragma unroll 4
                         for (int i = 0; i < 8; ++i) {
                             const uint32_t r = uint32_t(8 * i + (lane >> 2)), ch = uint32_t(lane & 3);
                             const uint4 q = ld_shared_v4(stage_u + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
@@ -512,19 +553,6 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                         __syncwarp();
                     }
                     if (kDots && a.aux) {
-                        // sums over the 8 lanes of a token pair: halving exchanges leave two of the 16 values
-#pragma unroll
-                        for (int c = 8, bit = 16; c >= 2; c >>= 1, bit >>= 1) {
-                            const bool up = (lane & bit) != 0;
-#pragma unroll
-                            for (int e = 0; e < c; ++e) {
-                                const float send = up ? d[e] : d[e + c], keep = up ? d[e + c] : d[e];
-                                d[e] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
-                            }
-                        }
-                        // lane bits 16, 8, 4 chose p, and two bits of the group of 8 tokens
-                        const int grp = ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
-                        *reinterpret_cast<float2 *>(red + quarter * 64 + 8 * grp + tp) = make_float2(d[0], d[1]);
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(kBAFree + int(mm & 1u)));
                         named_sync(kBarOut, 128);
@@ -536,26 +564,156 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                 m += uint32_t(w.nch);
             }
         }
-    } else if (warp < kWarpTma) {
-        // ============ prep warps: decays, w z in three terms, P ============
-        const int pt = tid - 32 * kWarpPrep, quarter = warp & 3;
+    } else if (warp < kWarpMask) {
+        // ============ split warps: w z of 32 tokens, in three terms ============
+        regs_down<kRegsWork>();
+        const int quarter = warp & 3, hf = (warp - kWarpSplit) >> 2, st = tid - 32 * kWarpSplit - 128 * hf;
         const uint32_t tq = tmem + (uint32_t(quarter * 32) << 16);
+        const uint32_t col = K::kColW + (K::kWz == 2 ? 48u * hf : 0u);
         while (w.next(kSt)) {
-            const float *g = a.g_const ? a.g + w.h : a.g + size_t(w.seg.start) * hv + w.h;
-            const size_t gs = a.g_const ? 0 : hv;
-            float g0 = 0.f, g1 = 0.f;
-            auto load_g = [&](int n) {  // this lane's two tokens of the n-th chunk (floored where they are used)
-                const int t = w.chunk_at(n) + 2 * lane;
-                g0 = t < w.seg.len ? g[size_t(t) * gs] : 0.f;
-                g1 = t + 1 < w.seg.len ? g[size_t(t + 1) * gs] : 0.f;
-            };
-            if (quarter == 0 && w.nch > 0) load_g(0);
             for (int n = 0; n < w.nch; ++n) {
                 const uint32_t mm = m + uint32_t(n);
-                const int t0 = w.chunk_at(n), L = min(kDecayChunk, w.seg.len - t0);
-                float *vec = vecs(mm);
-                if (quarter == 0) {
-                    // prefix sums and suffix sums (each without a subtraction)
+                const int L = min(kDecayChunk, w.seg.len - w.chunk_at(n));
+                const uint32_t s = mm % kRing, ring_phase = (mm / kRing) & 1u;
+                const uint32_t zt = sb + K::kOffZ + s * kTile;
+                if (ok) ok = warp_wait(bar(kBZ + int(s)), ring_phase) && warp_wait(bar(kBVec + int(mm & 3u)), (mm >> 2) & 1u);
+                if (L < kDecayChunk) {
+                    // tokens past the end are another sequence's: their y and z, whatever they hold, must not meet
+                    // a zero weight
+                    if (ok) ok = warp_wait(bar(kBY + int(s)), ring_phase);
+                    const uint32_t yt = sb + K::kOffY + s * kTile;
+                    for (int e = st; e < 512 && ok; e += 128) {
+                        const int r = 32 * hf + ((e >> 3) & 31);  // pieces of 16 bytes: 8 a row, 32 rows, 2 column halves
+                        const uint32_t off = uint32_t(e >> 8) * kAtom + uint32_t(r) * 128 + uint32_t(e & 7) * 16;
+                        if (r >= L) {
+                            st_shared_v4(zt + off, make_uint4(0u, 0u, 0u, 0u));
+                            if ((e >> 8) < ya) st_shared_v4(yt + off, make_uint4(0u, 0u, 0u, 0u));
+                        }
+                    }
+                    fence_proxy_async_shared();
+                    // the four warps go on, or stop, together
+                    if (named_sync_or(kBarSplit + hf, 128, !ok)) {
+                        ok = false;
+                        goto split_done;
+                    }
+                }
+                if (!ok) continue;  // (on to the next meeting of the four, or out)
+                {
+                    // KV has read these columns: the chunk before's, or (room for one half) the half before's
+                    if (K::kWz == 2) {
+                        if (mm > 0) ok = warp_wait(bar(hf ? kBKV1 : kBKV0), (mm - 1) & 1u);
+                    } else if (hf) {
+                        ok = warp_wait(bar(kBKV0), mm & 1u);
+                    } else if (mm > 0) {
+                        ok = warp_wait(bar(kBKV1), (mm - 1) & 1u);
+                    }
+                    if (!ok) continue;
+                    tc_fence_after();
+                    // transposed reads give token pairs of a z row, the layout of a tensor-memory A operand
+                    const float *wst = vecs(mm) + kVecSt + 32 * hf + 2 * (lane & 3);
+                    const uint32_t ch = uint32_t(4 * (quarter & 1) + (lane >> 3)), r7 = uint32_t(lane & 7);
+                    const uint32_t src = zt + uint32_t(quarter >> 1) * kAtom + uint32_t(32 * hf + r7) * 128 + ((ch ^ r7) << 4);
+#pragma unroll 2
+                    for (int j = 0; j < 4; ++j) {  // groups of 8 tokens
+                        uint32_t q[4];
+                        ldmatrix_t(src + 1024 * j, q);
+                        const float2 wt = *reinterpret_cast<const float2 *>(wst + 8 * j);
+#pragma unroll
+                        for (int l = 0; l < 2; ++l) {  // 16 z rows
+                            uint32_t w0[2], w1[2], w2[2];
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                float lo = bf_lo(q[2 * l + i]) * wt.x, hi = bf_hi(q[2 * l + i]) * wt.y;
+                                w0[i] = pack_bf16x2(lo, hi);
+                                lo -= bf_lo(w0[i]);
+                                hi -= bf_hi(w0[i]);
+                                w1[i] = pack_bf16x2(lo, hi);
+                                lo -= bf_lo(w1[i]);
+                                hi -= bf_hi(w1[i]);
+                                w2[i] = pack_bf16x2(lo, hi);
+                            }
+                            const uint32_t dst = tq + (uint32_t(16 * l) << 16) + col + 4 * j;
+                            tmem_st_frag(dst, w0);
+                            tmem_st_frag(dst + 16, w1);
+                            tmem_st_frag(dst + 32, w2);
+                        }
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kBW + hf));
+                }
+            }
+            m += uint32_t(w.nch);
+        }
+    split_done:;
+    } else if (warp < kWarpTma) {
+        // ============ mask warps: P = QK . decay mask ============
+        regs_down<kRegsWork>();
+        if constexpr (!kSt) {
+            const int quarter = warp & 3;
+            const uint32_t tq = tmem + (uint32_t(quarter * 32) << 16);
+            const int r = 16 * quarter + (lane & 15), cb = lane < 16 ? 0 : 32;
+            while (ok && w.next(false)) {
+                for (int n = 0; n < w.nch; ++n) {
+                    const uint32_t mm = m + uint32_t(n);
+                    const int L = min(kDecayChunk, w.seg.len - w.chunk_at(n));
+                    const float *G = vecs(mm) + kVecG;
+                    ok = warp_wait(bar(kBVec + int(mm & 3u)), (mm >> 2) & 1u);
+                    if (ok && mm >= 2) ok = warp_wait(bar(kBPFree + int(mm & 1u)), ((mm >> 1) - 1) & 1u);
+                    if (ok) ok = warp_wait(bar(kBQK), mm & 1u);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const float Gr = G[r];
+                    const uint32_t base = sb + K::kOffP + (mm & 1u) * kPTile + uint32_t(r) * 128;
+#pragma unroll 1
+                    for (int p = 0; p < 2; ++p) {
+                        float v[16];
+                        tmem_ld_m64(tq + K::kColQK + 16 * p, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            float gc[8], x[8];
+                            const int c0 = cb + 16 * p + 8 * q;
+                            load4(G + c0, gc);
+                            load4(G + c0 + 4, gc + 4);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const int c = c0 + j;
+                                const bool in = a.reverse ? (c >= r && c < L) : c <= r;
+                                const float d = a.reverse ? gc[j] - Gr : Gr - gc[j];
+                                float e;
+                                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(d));
+                                x[j] = in ? v[8 * q + j] * e : 0.f;
+                            }
+                            st_shared_v4(base + ((uint32_t(c0 / 8) ^ uint32_t(r & 7)) << 4), pack_bf16x8(x));
+                        }
+                    }
+                    fence_proxy_async_shared();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kBP + int(mm & 1u)));
+                }
+                m += uint32_t(w.nch);
+            }
+        }
+    } else {
+        regs_down<kRegsCtl>();
+        if (warp == kWarpGate) {
+            // ============ decays: prefix and suffix sums (each without a subtraction), their exponentials ============
+            while (ok && w.next(kSt)) {
+                const float *g = a.g_const ? a.g + w.h : a.g + size_t(w.seg.start) * hv + w.h;
+                const size_t gs = a.g_const ? 0 : hv;
+                float g0 = 0.f, g1 = 0.f;
+                auto load_g = [&](int n) {  // this lane's two tokens of the n-th chunk (floored where they are used)
+                    const int t = w.chunk_at(n) + 2 * lane;
+                    g0 = t < w.seg.len ? g[size_t(t) * gs] : 0.f;
+                    g1 = t + 1 < w.seg.len ? g[size_t(t + 1) * gs] : 0.f;
+                };
+                if (w.nch > 0) load_g(0);
+                for (int n = 0; n < w.nch; ++n) {
+                    const uint32_t mm = m + uint32_t(n);
+                    float *vec = vecs(mm);
                     const float a0 = fmaxf(g0, kGFloor), a1 = fmaxf(g1, kGFloor);
                     if (n + 1 < w.nch) load_g(n + 1);
                     float pre = a0 + a1, suf = a0 + a1;
@@ -570,126 +728,20 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                     if (lane == 31) after = 0.f;
                     const float G0 = before + a0, G1 = pre, R0 = a1 + after, R1 = after;
                     const float total = __shfl_sync(0xffffffffu, pre, 31);
-                    const float e0 = expf(G0), e1 = expf(G1), f0 = expf(R0), f1 = expf(R1);
+                    const float e0 = expf(G0), e1 = expf(G1), f0 = expf(R0), f1 = expf(R1), et = expf(total);
                     constexpr float kLog2e = 1.4426950408889634f;
+                    if (mm >= 4) ok = warp_wait(bar(kBVecFree + int(mm & 3u)), ((mm >> 2) - 1) & 1u);
+                    if (!ok) break;
                     *reinterpret_cast<float2 *>(vec + kVecG + 2 * lane) = make_float2(G0 * kLog2e, G1 * kLog2e);
                     *reinterpret_cast<float2 *>(vec + kVecIn + 2 * lane) = a.reverse ? make_float2(f0, f1) : make_float2(e0, e1);
                     *reinterpret_cast<float2 *>(vec + kVecSt + 2 * lane) = a.reverse ? make_float2(e0, e1) : make_float2(f0, f1);
-                    if (lane == 0) vec[kVecGamma] = expf(total);
-                }
-                // the four warps go on, or stop, together
-                if (named_sync_or(kBarPrep, 128, !ok)) {
-                    ok = false;
-                    goto prep_done;
-                }
-                const uint32_t zs = mm % kRing, ring_phase = (mm / kRing) & 1u;
-                const uint32_t zt = sb + K::kOffZ + zs * kTile;
-                ok = warp_wait(bar(kBZ + int(zs)), ring_phase);
-                if (L < kDecayChunk) {
-                    // tokens past the end are another sequence's: their y and z, whatever they hold, must not meet
-                    // a zero weight
-                    if (ok) ok = warp_wait(bar(kBY + int(zs)), ring_phase);
-                    const uint32_t yt = sb + K::kOffY + zs * kTile;
-                    for (int e = pt; e < 1024 && ok; e += 128)
-                        if (((e >> 3) & 63) >= L) {
-                            st_shared_v4(zt + uint32_t(e) * 16, make_uint4(0u, 0u, 0u, 0u));
-                            if (e < 512 * ya) st_shared_v4(yt + uint32_t(e) * 16, make_uint4(0u, 0u, 0u, 0u));
-                        }
-                    fence_proxy_async_shared();
-                    if (named_sync_or(kBarPrep, 128, !ok)) {
-                        ok = false;
-                        goto prep_done;
-                    }
-                }
-                if (!ok) continue;
-                // w z, half a chunk at a time: transposed reads give token pairs of a z row, the layout of a
-                // tensor-memory A operand
-                for (int hf = 0; hf < 2; ++hf) {
-                    uint32_t q[4][4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t r = uint32_t(32 * hf + 8 * j + (lane & 7)), ch = uint32_t(4 * (quarter & 1) + (lane >> 3));
-                        ldmatrix_t(zt + uint32_t(quarter >> 1) * kAtom + r * 128 + ((ch ^ (r & 7)) << 4), q[j]);
-                    }
-                    // the half's columns were read by KV: of the chunk before, or (one half's room) of the half before
-                    const uint32_t col = K::kColW + (K::kWz == 2 ? 48u * hf : 0u);
-                    if (K::kWz == 2) {
-                        if (mm > 0) ok = warp_wait(bar(hf ? kBKV1 : kBKV0), (mm - 1) & 1u);
-                    } else if (hf) {
-                        ok = warp_wait(bar(kBKV0), mm & 1u);
-                    } else if (mm > 0) {
-                        ok = warp_wait(bar(kBKV1), (mm - 1) & 1u);
-                    }
-                    if (!ok) break;
-                    tc_fence_after();
-                    // registers of a store: token group j (two registers each: z rows i and i + 1 of the half quarter)
-#pragma unroll
-                    for (int l = 0; l < 2; ++l) {
-                        uint32_t t0w[8], t1w[8], t2w[8];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 wt = *reinterpret_cast<const float2 *>(vec + kVecSt + 32 * hf + 8 * j + 2 * (lane & 3));
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                float lo = bf_lo(q[j][2 * l + i]) * wt.x, hi = bf_hi(q[j][2 * l + i]) * wt.y;
-                                t0w[2 * j + i] = pack_bf16x2(lo, hi);
-                                lo -= bf_lo(t0w[2 * j + i]);
-                                hi -= bf_hi(t0w[2 * j + i]);
-                                t1w[2 * j + i] = pack_bf16x2(lo, hi);
-                                lo -= bf_lo(t1w[2 * j + i]);
-                                hi -= bf_hi(t1w[2 * j + i]);
-                                t2w[2 * j + i] = pack_bf16x2(lo, hi);
-                            }
-                        }
-                        const uint32_t dst = tq + (uint32_t(16 * l) << 16) + col;
-                        tmem_st_frag(dst, t0w);
-                        tmem_st_frag(dst + 16, t1w);
-                        tmem_st_frag(dst + 32, t2w);
-                    }
-                    tmem_wait_st();
-                    tc_fence_before();
+                    if (lane == 0) vec[kVecGamma] = et;
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(kBW + hf));
+                    if (lane == 0) mbar_arrive(bar(kBVec + int(mm & 3u)));
                 }
-                if (!ok) continue;
-                if constexpr (!kSt) {
-                    ok = warp_wait(bar(kBQK), mm & 1u);
-                    if (ok && mm >= 2) ok = warp_wait(bar(kBPFree + int(mm & 1u)), ((mm >> 1) - 1) & 1u);
-                    if (!ok) continue;
-                    tc_fence_after();
-                    float v[32];
-                    tmem_ld_m64(tq + K::kColQK, v);
-                    tmem_wait_ld();
-                    const int r = 16 * quarter + (lane & 15), cb = lane < 16 ? 0 : 32;
-                    const float Gr = vec[kVecG + r];
-                    const uint32_t base = sb + K::kOffP + (mm & 1u) * kPTile + uint32_t(r) * 128;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float gc[8], x[8];
-                        load4(vec + kVecG + cb + 8 * q, gc);
-                        load4(vec + kVecG + cb + 8 * q + 4, gc + 4);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const int c = cb + 8 * q + j;
-                            const bool in = a.reverse ? (c >= r && c < L) : c <= r;
-                            const float d = a.reverse ? gc[j] - Gr : Gr - gc[j];
-                            float e;
-                            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(d));
-                            x[j] = in ? v[8 * q + j] * e : 0.f;
-                        }
-                        st_shared_v4(base + ((uint32_t(cb / 8 + q) ^ uint32_t(r & 7)) << 4), pack_bf16x8(x));
-                    }
-                    fence_proxy_async_shared();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(kBP + int(mm & 1u)));
-                }
+                m += uint32_t(w.nch);
             }
-            m += uint32_t(w.nch);
-        }
-    prep_done:;
-    } else if (warp == kWarpTma) {
-        if (elect_one()) {
+        } else if (warp == kWarpTma && elect_one()) {
             const uint32_t bytes_y = kAtom * uint32_t(ya);
             while (ok && w.next(kSt)) {
                 const int hx = kSt ? 0 : w.h / (hv / a.hx), hy = w.h / (hv / a.hy), hz = w.h / (hv / a.hz);
@@ -734,8 +786,7 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                 }
                 m += uint32_t(w.nch);
             }
-        }
-    } else if (elect_one()) {
+        } else if (warp == kWarpMma && elect_one()) {
         // ==================== the issuing thread ====================
         uint32_t total = 0;
         while (w.next(kSt)) total += uint32_t(w.nch);
@@ -819,6 +870,7 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
         // every product done before the tensor memory goes
         mma_commit(bar(kBDrain));
         if (!mbar_wait(bar(kBDrain), 0u)) ok = false;
+        }
     }
     if (!ok && !dead) {
         a.sched.hdr->bad_index = -2;
@@ -834,6 +886,9 @@ cudaError_t launch_as(const Maps &tm, const DecayPass &p, int64_t max_units, cud
     cudaError_t e = cudaFuncSetAttribute(decay_pass_tc_kernel<kKind>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          int(Cfg<kKind>::kSmem));
     if (e != cudaSuccess) return e;
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, decay_pass_tc_kernel<kKind>)) != cudaSuccess) return e;
+    if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidKernelImage;  // the roles' registers are dealt out of these
     int dev = 0, sms = kDecayPlanSms;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess ||
         (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
