@@ -27,18 +27,20 @@
 // in a bf16 output, and one bf16 copy costs it as much as the output's own
 // rounding.  P is one bf16 term for the same reason.
 //
-// Roles (7 warpgroups; a role's warps are latency-bound, so the work is spread
+// Roles (8 warpgroups; a role's warps are latency-bound, so the work is spread
 // until the products set the pace):
 //   0-7     state      two warps per tensor-memory quarter, 64 columns each
-//   8-11    out        X1, X2 -> out (and the dot with aux)
-//   12-19   split      w z in three terms, 32 tokens of the chunk a warpgroup
-//   20-23   mask       P from QK
-//   24 TMA loads, 25 products, 26 decays (27 only fills the warpgroup)
-// The registers go where the state is (setmaxnreg).  Products are issued in
-// the order KV(n), X1(n), X2(n), QK(n + 1), which leaves P(n + 1) the time of
-// KV(n + 1) and X1(n + 1).  With three copies of Sigma X1 alone is that long,
-// and tensor memory is full: X2 shares QK's columns, w z has room for half a
-// chunk, and the order is X1(n), X2(n), KV(n + 1), QK(n + 1).
+//   8-15    out        X1, X2 -> out (and the dot with aux), 32 tokens a warpgroup
+//   16-23   split      w z in three terms, 32 tokens a warpgroup
+//   24-27   mask       P from QK
+//   28 TMA loads, 29 products, 30 decays (31 only fills the warpgroup)
+// The registers go where the state is (setmaxnreg).
+//
+// Order of the products.  Plain passes: KV(n), X1(n), X2(n), QK(n + 1), which
+// leaves the masking of P(n + 1) the time of KV(n + 1) and X1(n + 1).  With
+// three copies of Sigma tensor memory is full: X2 shares QK's columns, w z has
+// room for half a chunk, and KV runs a chunk ahead: KV(n + 1) first half,
+// X1(n), KV(n + 1) second half, X2(n), QK(n + 1).
 // All hand-overs are mbarriers with bounded waits; a timeout records
 // GDN_ERR_DEVICE_CHECK (bad_index -2).  A CTA takes units (segment, head) with
 // a stride of the grid; nothing synchronises it between units.
@@ -52,14 +54,13 @@ using namespace sm100;
 
 namespace {
 
-constexpr int kThreads = 896;
-constexpr int kWarpOut = 8, kWarpSplit = 12, kWarpMask = 20, kWarpTma = 24, kWarpMma = 25, kWarpGate = 26;
-constexpr int kBarOut = 1, kBarSplit = 2;  // named barriers (128 threads each; one for each split warpgroup)
-// Registers a thread: 72 at launch (896 threads: 64,512), then by role; the
-// sum over the seven warpgroups, 128 (2 x 104 + 80 + 3 x 56 + 40) = 63,488,
-// stays below what the block was launched with.
-constexpr int kRegsLaunch = 72, kRegsState = 104, kRegsOut = 80, kRegsWork = 56, kRegsCtl = 40;
-static_assert(128 * (2 * kRegsState + kRegsOut + 3 * kRegsWork + kRegsCtl) <= kThreads * kRegsLaunch, "registers");
+constexpr int kThreads = 1024;
+constexpr int kWarpOut = 8, kWarpSplit = 16, kWarpMask = 24, kWarpTma = 28, kWarpMma = 29, kWarpGate = 30;
+constexpr int kBarOut = 1, kBarSplit = 3;  // named barriers (128 threads each; one for each out and split warpgroup)
+// Registers a thread: 64 at launch, then by role; the sum over the eight
+// warpgroups is what the block was launched with.
+constexpr int kRegsLaunch = 64, kRegsState = 96, kRegsOut = 72, kRegsWork = 48, kRegsCtl = 32;
+static_assert(128 * (2 * kRegsState + 2 * kRegsOut + 3 * kRegsWork + kRegsCtl) <= kThreads * kRegsLaunch, "registers");
 constexpr uint32_t kTile = 16384, kAtom = 8192, kPTile = 8192;
 constexpr uint32_t kTmemCols = 512;
 
@@ -70,6 +71,7 @@ constexpr int kVecG = 0, kVecIn = 64, kVecSt = 128, kVecGamma = 192, kVecFloats 
 // kKind: what a pass leaves out or adds
 enum { kPlain = 0, kDot = 1, kStateOnly = 2 };
 constexpr int kRing = 3;  // tiles of x, y and z
+constexpr uint32_t kStage = 2304;  // an out warp's staging: 32 rows of 64 bytes, or 16 rows of 36 floats
 
 template <int kKind> struct Cfg {
     static constexpr int kCopies = kKind == kDot ? 3 : 1;        // bf16 terms of Sigma's copy
@@ -80,17 +82,16 @@ template <int kKind> struct Cfg {
     static constexpr uint32_t kOffY = kOffZ + kRing * kTile;
     static constexpr uint32_t kOffAux = kOffY + kRing * kTile;                     // [2], kDot only
     static constexpr uint32_t kOffP = kOffAux + (kKind == kDot ? 2 * kTile : 0);   // [2]
-    static constexpr uint32_t kOffOut = kOffP + 2 * kPTile;                        // 4096 bytes an out warp
-    static constexpr uint32_t kOffVec = kOffOut + kTile;                           // [4]
+    static constexpr uint32_t kOffOut = kOffP + 2 * kPTile;                        // kStage bytes an out warp
+    static constexpr uint32_t kOffVec = kOffOut + 8 * kStage;                           // [4]
     static constexpr uint32_t kOffRed = kOffVec + 4 * kVecFloats * 4;              // [4 warps][64]
     static constexpr uint32_t kOffBar = kOffRed + 1024;
     static constexpr uint32_t kSmem = kOffBar + 384 + 1024;
     static_assert(kSmem <= 232448, "shared memory over the sm_100 per-block limit");
     // tensor memory columns
-    static constexpr uint32_t kColL = 0, kColC = 128;  // L; the copies of Sigma (64 columns a term)
-    static constexpr uint32_t kColX1 = kColC + 64 * kCopies, kColX2 = kColX1 + 64;
-    static constexpr uint32_t kColQK = kKind == kDot ? kColX2 : kColX2 + 64;
-    static constexpr uint32_t kColW = kColQK + 64;     // w z: 48 columns a half chunk (16 a term)
+    // L; the copies of Sigma (64 columns a term); X1; X2; QK; w z (48 a half chunk, 16 a term)
+    static constexpr uint32_t kColL = 0, kColC = 128, kColX1 = kColC + 64 * kCopies, kColX2 = kColX1 + 64;
+    static constexpr uint32_t kColQK = kKind == kDot ? kColX2 : kColX2 + 64, kColW = kColQK + 64;
     static_assert(kColW + 48 * kWz <= kTmemCols, "tensor memory");
 };
 
@@ -103,8 +104,8 @@ enum {
     kBXFree = 11,   // [3] X1 (and QK) of the slot's chunk done
     kBZFree = 14,   // [3] X2 done (w z was taken before KV)
     kBYFree = 17,   // [3] KV (and QK) done
-    kBAFree = 20,   // [2] dot taken (4 out warps)
-    kBW = 22,       // [2] a half chunk of w z written (4 split warps)
+    kBAFree = 20,   // [2] dot taken (8 out warps)
+    kBW = 22,       // [2] first, second half of w z written (4 split warps each)
     kBKV0 = 24,     // KV of the first half done
     kBKV1 = 25,     // KV done (and an arrival of the issuing thread, which orders the token vectors)
     kBLFree = 26,   // L read (8 state warps)
@@ -114,9 +115,9 @@ enum {
     kBP = 30,       // [2] P written (4 mask warps)
     kBPFree = 32,   // [2] X2 done
     kBOut = 34,     // X1, X2 done (and an arrival of the issuing thread)
-    kBOutFree = 35, // X1, X2 read (4 out warps)
+    kBOutFree = 35, // X1, X2 read (8 out warps)
     kBVec = 36,     // [4] token vectors written
-    kBVecFree = 40, // [4] token vectors read (8 state warps, 4 out warps)
+    kBVecFree = 40, // [4] token vectors read (8 state warps, 8 out warps)
     kBDrain = 44,
     kNumBars = 45
 };
@@ -244,11 +245,10 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
     if (tid == 0) {
         for (int i = 0; i < kNumBars; ++i) {
             int n = 1;
-            if (i == kBAFree || i == kBAFree + 1 || i == kBW || i == kBW + 1 || i == kBP || i == kBP + 1 || i == kBOutFree)
-                n = 4;
-            if (i == kBSt || i == kBLFree) n = 8;
+            if (i == kBW || i == kBW + 1 || i == kBP || i == kBP + 1) n = 4;
+            if (i == kBSt || i == kBLFree || i == kBOutFree || i == kBAFree || i == kBAFree + 1) n = 8;
             if (i == kBOut || i == kBKV1) n = 2;
-            if (i >= kBVecFree && i < kBVecFree + 4) n = kSt ? 8 : 12;
+            if (i >= kBVecFree && i < kBVecFree + 4) n = kSt ? 8 : 16;
             mbar_init(bar(i), uint32_t(n));
         }
         fence_mbarrier_init();
@@ -353,12 +353,12 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                 const float gamma = vecs(mm)[kVecGamma];
                 if (mine) {
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        float v[32];
-                        tmem_ld32(trow + K::kColL + uint32_t(c0 + 32 * q), v);
+                    for (int q = 0; q < 4; ++q) {
+                        float v[16];
+                        tmem_ld16(trow + K::kColL + uint32_t(c0 + 16 * q), v);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) S[32 * q + j] = fmaf(gamma, S[32 * q + j], v[j]);
+                        for (int j = 0; j < 16; ++j) S[16 * q + j] = fmaf(gamma, S[16 * q + j], v[j]);
                     }
                 }
                 dec *= gamma;
@@ -423,12 +423,12 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
         // ==================== out warps: 32 z rows each, read in fragments ====================
         regs_up<kRegsOut>();
         if constexpr (!kSt) {
-            const int quarter = warp & 3, ot = tid - 32 * kWarpOut;
+            const int quarter = warp & 3, part = (warp - kWarpOut) >> 2, ot = tid - 32 * kWarpOut - 128 * part;
             const uint32_t tq = tmem + (uint32_t(quarter * 32) << 16);
             const int tp = 2 * (lane & 3);                 // first of this thread's two tokens in a group of 8
             float *red = reinterpret_cast<float *>(smem + K::kOffRed);
-            float *stage = reinterpret_cast<float *>(smem + K::kOffOut + quarter * 4096);
-            const uint32_t stage_u = sb + K::kOffOut + uint32_t(quarter) * 4096;
+            float *stage = reinterpret_cast<float *>(smem + K::kOffOut + (warp - kWarpOut) * kStage);
+            const uint32_t stage_u = sb + K::kOffOut + uint32_t(warp - kWarpOut) * kStage;
             while (ok && w.next(false)) {
                 for (int n = 0; n < w.nch; ++n) {
                     const uint32_t mm = m + uint32_t(n);
@@ -436,7 +436,7 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                     ok = warp_wait(bar(kBOut), mm & 1u);
                     if (kDots && a.aux) {
                         if (ok) ok = warp_wait(bar(kBA + int(mm & 1u)), (mm >> 1) & 1u);
-                        ok = !named_sync_or(kBarOut, 128, !ok);  // the four warps stay together (and `red` was read)
+                        ok = !named_sync_or(kBarOut + part, 128, !ok);  // the four warps stay together (and `red` was read)
                     }
                     if (!ok) break;
                     tc_fence_after();
@@ -445,7 +445,8 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                     const size_t step = size_t(hv) * dz;
                     const size_t at = (tok * hv + w.h) * dz + 32 * quarter;
 #pragma unroll 1
-                    for (int p = 0; p < 4; ++p) {  // 16 tokens (rolled: the roles share the instruction caches)
+                    for (int pp = 0; pp < 2; ++pp) {  // 16 tokens (rolled: the roles share the instruction caches)
+                        const int p = 2 * part + pp;
                         float x1[2][8], x2[2][8];
 #pragma unroll
                         for (int l = 0; l < 2; ++l) {
@@ -453,7 +454,7 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                             tmem_ld_frag(tq + (uint32_t(16 * l) << 16) + K::kColX2 + 16 * p, x2[l]);
                         }
                         tmem_wait_ld();
-                        if (p == 3) {
+                        if (pp == 1) {
                             tc_fence_before();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(bar(kBOutFree));
@@ -509,7 +510,7 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                             // bf16 token pairs, transposed into rows of 64 bytes (four 16-byte pieces, swizzled) per token
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
-                                const uint32_t r = uint32_t(16 * p + 8 * j + (lane & 7));
+                                const uint32_t r = uint32_t(16 * pp + 8 * j + (lane & 7));
                                 const uint32_t ch = uint32_t(lane >> 3);
                                 stmatrix_t(stage_u + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4),
                                            pack_bf16x2(x2[0][4 * j], x2[0][4 * j + 1]),
@@ -543,22 +544,24 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                     if (lane == 0) mbar_arrive(bar(kBVecFree + int(mm & 3u)));
                     if (!a.out_f32) {
                         __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.out) + at;
-#pragma unroll 4
-                        for (int i = 0; i < 8; ++i) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
                             const uint32_t r = uint32_t(8 * i + (lane >> 2)), ch = uint32_t(lane & 3);
                             const uint4 q = ld_shared_v4(stage_u + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
-                            if (int(r) < L && 32 * quarter + 8 * int(ch) < dz)
-                                *reinterpret_cast<uint4 *>(o + r * step + 8 * ch) = q;
+                            const int tk = 32 * part + int(r);
+                            if (tk < L && 32 * quarter + 8 * int(ch) < dz)
+                                *reinterpret_cast<uint4 *>(o + tk * step + 8 * ch) = q;
                         }
                         __syncwarp();
                     }
                     if (kDots && a.aux) {
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(kBAFree + int(mm & 1u)));
-                        named_sync(kBarOut, 128);
-                        if (ot < L)
-                            a.dot[size_t(w.h) * a.tokens + tok + ot] =
-                                (red[ot] + red[64 + ot]) + (red[128 + ot] + red[192 + ot]);
+                        named_sync(kBarOut + part, 128);
+                        const int tk = 32 * part + ot;
+                        if (ot < 32 && tk < L)
+                            a.dot[size_t(w.h) * a.tokens + tok + tk] =
+                                (red[tk] + red[64 + tk]) + (red[128 + tk] + red[192 + tk]);
                     }
                 }
                 m += uint32_t(w.nch);
@@ -568,8 +571,7 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
         // ============ split warps: w z of 32 tokens, in three terms ============
         regs_down<kRegsWork>();
         const int quarter = warp & 3, hf = (warp - kWarpSplit) >> 2, st = tid - 32 * kWarpSplit - 128 * hf;
-        const uint32_t tq = tmem + (uint32_t(quarter * 32) << 16);
-        const uint32_t col = K::kColW + (K::kWz == 2 ? 48u * hf : 0u);
+        const uint32_t tq = tmem + (uint32_t(quarter * 32) << 16) + K::kColW + (K::kWz == 2 ? 48u * hf : 0u);
         while (w.next(kSt)) {
             for (int n = 0; n < w.nch; ++n) {
                 const uint32_t mm = m + uint32_t(n);
@@ -601,7 +603,7 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                 {
                     // KV has read these columns: the chunk before's, or (room for one half) the half before's
                     if (K::kWz == 2) {
-                        if (mm > 0) ok = warp_wait(bar(hf ? kBKV1 : kBKV0), (mm - 1) & 1u);
+                        if (mm > 0) ok = warp_wait(bar(kBKV0 + hf), (mm - 1) & 1u);
                     } else if (hf) {
                         ok = warp_wait(bar(kBKV0), mm & 1u);
                     } else if (mm > 0) {
@@ -632,7 +634,7 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                                 hi -= bf_hi(w1[i]);
                                 w2[i] = pack_bf16x2(lo, hi);
                             }
-                            const uint32_t dst = tq + (uint32_t(16 * l) << 16) + col + 4 * j;
+                            const uint32_t dst = tq + (uint32_t(16 * l) << 16) + 4 * j;
                             tmem_st_frag(dst, w0);
                             tmem_st_frag(dst + 16, w1);
                             tmem_st_frag(dst + 32, w2);
@@ -793,56 +795,64 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
         const uint32_t id_qk = idesc_bf16(64, 64, false, false), id_kv = idesc_bf16(128, 64 * ya, false, true);
         const uint32_t id_x1 = idesc_bf16(128, 64, false, false), id_x2 = idesc_bf16(128, 64, true, false);
         auto koff = [](int s) { return uint64_t(((s >> 2) * kAtom + (s & 3) * 32) >> 4); };  // K-major steps
+        auto out_read = [&](uint32_t c) { return c == 0 || mbar_wait(bar(kBOutFree), (c - 1) & 1u); };
         auto issue_qk = [&](uint32_t c) {
             const uint32_t s = c % kRing, ph = (c / kRing) & 1u;
             if (!mbar_wait(bar(kBX + int(s)), ph) || !mbar_wait(bar(kBY + int(s)), ph)) return false;
-            // (with shared columns: the out warps have read the previous X2)
-            if (K::kColQK == K::kColX2 && c > 0 && !mbar_wait(bar(kBOutFree), (c - 1) & 1u)) return false;
+            if (K::kColQK == K::kColX2 && !out_read(c)) return false;
             tc_fence_after();
             const uint64_t dx = smem_desc(sb + K::kOffX + s * kTile, 16, 1024), dyd = smem_desc(sb + K::kOffY + s * kTile, 16, 1024);
+#pragma unroll 1
+            for (int j = 0; j < ya; ++j)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < 4 * ya) mma_bf16(tmem + K::kColQK, dx + koff(i), dyd + koff(i), id_qk, i > 0);
+                for (int i = 0; i < 4; ++i)
+                    mma_bf16(tmem + K::kColQK, dx + koff(4 * j) + koff(i), dyd + koff(4 * j) + koff(i), id_qk, i > 0 || j > 0);
             mma_commit(bar(kBQK));
+            if (kDots) mma_commit(bar(kBYFree + int(s)));  // the last reader of y
             return true;
         };
-        auto issue_kv = [&](uint32_t c) {
+        auto issue_kv = [&](uint32_t c, int hf) {
             const uint32_t s = c % kRing;
-            if (!mbar_wait(bar(kBY + int(s)), (c / kRing) & 1u)) return false;
-            if (c > 0 && !mbar_wait(bar(kBLFree), (c - 1) & 1u)) return false;
-            const uint64_t db = smem_desc(sb + K::kOffY + s * kTile, 8192, 1024);
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                if (!mbar_wait(bar(kBW + hf), c & 1u)) return false;
-                tc_fence_after();
-                const uint32_t col = tmem + K::kColW + (K::kWz == 2 ? 48u * hf : 0u);
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int t = 0; t < 3; ++t)
-                        mma_bf16_ts(tmem + K::kColL, col + 16 * t + 8 * i, db + uint64_t(((2 * hf + i) * 2048) >> 4), id_kv,
-                                    hf > 0 || i > 0 || t > 0);
-                mma_commit(bar(hf ? kBKV1 : kBKV0));
+            if (hf == 0) {
+                if (!mbar_wait(bar(kBY + int(s)), (c / kRing) & 1u)) return false;
+                if (c > 0 && !mbar_wait(bar(kBLFree), (c - 1) & 1u)) return false;
             }
-            mbar_arrive(bar(kBKV1));
-            mma_commit(bar(kBYFree + int(s)));
-            if (kSt) mma_commit(bar(kBZFree + int(s)));
+            if (!mbar_wait(bar(kBW + hf), c & 1u)) return false;
+            tc_fence_after();
+            const uint64_t db = smem_desc(sb + K::kOffY + s * kTile + 4096u * uint32_t(hf), 8192, 1024);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int t = 0; t < 3; ++t)
+                    mma_bf16_ts(tmem + K::kColL, tmem + K::kColW + (K::kWz == 2 ? 48u * hf : 0u) + 16 * t + 8 * i, db + uint64_t((i * 2048) >> 4), id_kv,
+                                hf > 0 || i > 0 || t > 0);
+            mma_commit(bar(kBKV0 + hf));
+            if (hf) {
+                mbar_arrive(bar(kBKV1));
+                if (!kDots) mma_commit(bar(kBYFree + int(s)));
+                if (kSt) mma_commit(bar(kBZFree + int(s)));
+            }
             return true;
         };
-        auto issue_x = [&](uint32_t c) {
+        auto issue_x1 = [&](uint32_t c) {
             const uint32_t s = c % kRing;
-            if (!mbar_wait(bar(kBSt), c & 1u)) return false;
-            if (c > 0 && !mbar_wait(bar(kBOutFree), (c - 1) & 1u)) return false;
+            if (!mbar_wait(bar(kBSt), c & 1u) || !out_read(c)) return false;
             tc_fence_after();
             const uint64_t dx = smem_desc(sb + K::kOffX + s * kTile, 16, 1024);
+#pragma unroll 1
+            for (int j = 0; j < 2 * K::kCopies; ++j) {
+                if ((j & 1) >= ya) continue;  // (j & 1: 64 columns of y; j / 2: term)
 #pragma unroll
-            for (int t = 0; t < K::kCopies; ++t)
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i < 4 * ya)
-                        mma_bf16_ts(tmem + K::kColX1, tmem + K::kColC + 64 * t + 8 * i, dx + koff(i), id_x1, t > 0 || i > 0);
+                for (int i = 0; i < 4; ++i)
+                    mma_bf16_ts(tmem + K::kColX1, tmem + K::kColC + 32 * j + 8 * i, dx + koff(4 * (j & 1)) + koff(i), id_x1,
+                                j > 0 || i > 0);
+            }
             mma_commit(bar(kBX1));
             mma_commit(bar(kBXFree + int(s)));
+            return true;
+        };
+        auto issue_x2 = [&](uint32_t c) {
+            const uint32_t s = c % kRing;
             if (!mbar_wait(bar(kBP + int(c & 1u)), (c >> 1) & 1u)) return false;
             tc_fence_after();
             const uint64_t da = smem_desc(sb + K::kOffZ + s * kTile, 8192, 1024);
@@ -857,15 +867,18 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
             return true;
         };
         if constexpr (kSt) {
-            for (uint32_t c = 0; ok && c < total; ++c) ok = issue_kv(c);
-        } else if constexpr (K::kCopies == 1) {
+            for (uint32_t c = 0; ok && c < total; ++c) ok = issue_kv(c, 0) && issue_kv(c, 1);
+        } else if constexpr (!kDots) {
             if (total > 0) ok = ok && issue_qk(0);
             for (uint32_t c = 0; ok && c < total; ++c)
-                ok = issue_kv(c) && issue_x(c) && (c + 1 == total || issue_qk(c + 1));
+                ok = issue_kv(c, 0) && issue_kv(c, 1) && issue_x1(c) && issue_x2(c) && (c + 1 == total || issue_qk(c + 1));
         } else {
-            if (total > 0) ok = ok && issue_kv(0) && issue_qk(0);
-            for (uint32_t c = 0; ok && c < total; ++c)
-                ok = issue_x(c) && (c + 1 == total || (issue_kv(c + 1) && issue_qk(c + 1)));
+            if (total > 0) ok = ok && issue_kv(0, 0) && issue_kv(0, 1) && issue_qk(0);
+            for (uint32_t c = 0; ok && c < total; ++c) {
+                const bool more = c + 1 < total;
+                ok = (!more || issue_kv(c + 1, 0)) && issue_x1(c) && (!more || issue_kv(c + 1, 1)) && issue_x2(c) &&
+                     (!more || issue_qk(c + 1));
+            }
         }
         // every product done before the tensor memory goes
         mma_commit(bar(kBDrain));
