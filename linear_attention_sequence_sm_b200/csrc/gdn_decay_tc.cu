@@ -33,14 +33,15 @@
 //   8-15    out        X1, X2 -> out (and the dot with aux), 32 tokens a warpgroup
 //   16-23   split      w z in three terms, 32 tokens a warpgroup
 //   24-27   mask       P from QK
-//   28 TMA loads, 29 products, 30 decays (31 only fills the warpgroup)
-// The registers go where the state is (setmaxnreg).
+//   28 TMA loads, 29 issues X1, X2 and QK, 30 decays, 31 issues KV
+// The registers go where the state is (setmaxnreg).  A chunk's products are 32
+// instructions with a dozen waits and commits between them; issued by one
+// thread these took 3300 cycles a chunk, more than the products themselves.
 //
-// Order of the products.  Plain passes: KV(n), X1(n), X2(n), QK(n + 1), which
-// leaves the masking of P(n + 1) the time of KV(n + 1) and X1(n + 1).  With
-// three copies of Sigma tensor memory is full: X2 shares QK's columns, w z has
-// room for half a chunk, and KV runs a chunk ahead: KV(n + 1) first half,
-// X1(n), KV(n + 1) second half, X2(n), QK(n + 1).
+// Two chains run side by side, each bound by its own hand-overs: KV(n) -> L
+// read by the state warps -> KV(n + 1), and QK(n + 1) -> P(n + 1) -> X2(n + 1).
+// With three copies of Sigma tensor memory is full: X2 shares QK's columns,
+// and w z has room for half a chunk.
 // All hand-overs are mbarriers with bounded waits; a timeout records
 // GDN_ERR_DEVICE_CHECK (bad_index -2).  A CTA takes units (segment, head) with
 // a stride of the grid; nothing synchronises it between units.
@@ -55,7 +56,7 @@ using namespace sm100;
 namespace {
 
 constexpr int kThreads = 1024;
-constexpr int kWarpOut = 8, kWarpSplit = 16, kWarpMask = 24, kWarpTma = 28, kWarpMma = 29, kWarpGate = 30;
+constexpr int kWarpOut = 8, kWarpSplit = 16, kWarpMask = 24, kWarpTma = 28, kWarpMma = 29, kWarpGate = 30, kWarpKv = 31;
 constexpr int kBarOut = 1, kBarSplit = 3;  // named barriers (128 threads each; one for each out and split warpgroup)
 // Registers a thread: 64 at launch, then by role; the sum over the eight
 // warpgroups is what the block was launched with.
@@ -102,8 +103,8 @@ enum {
     kBY = 6,        // [3] y
     kBA = 9,        // [2] aux
     kBXFree = 11,   // [3] X1 (and QK) of the slot's chunk done
-    kBZFree = 14,   // [3] X2 done (w z was taken before KV)
-    kBYFree = 17,   // [3] KV (and QK) done
+    kBZFree = 14,   // [3] X2 done, w z taken (8 split warps)
+    kBYFree = 17,   // [3] KV done, QK done
     kBAFree = 20,   // [2] dot taken (8 out warps)
     kBW = 22,       // [2] first, second half of w z written (4 split warps each)
     kBKV0 = 24,     // KV of the first half done
@@ -248,6 +249,9 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
             if (i == kBW || i == kBW + 1 || i == kBP || i == kBP + 1) n = 4;
             if (i == kBSt || i == kBLFree || i == kBOutFree || i == kBAFree || i == kBAFree + 1) n = 8;
             if (i == kBOut || i == kBKV1) n = 2;
+            if (i >= kBZFree && i < kBZFree + kRing) n = kSt ? 8 : 9;
+            if (i >= kBYFree && i < kBYFree + kRing) n = kSt ? 1 : 2;
+            if (i == kBDrain) n = 2;
             if (i >= kBVecFree && i < kBVecFree + 4) n = kSt ? 8 : 16;
             mbar_init(bar(i), uint32_t(n));
         }
@@ -580,20 +584,18 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                 const uint32_t zt = sb + K::kOffZ + s * kTile;
                 if (ok) ok = warp_wait(bar(kBZ + int(s)), ring_phase) && warp_wait(bar(kBVec + int(mm & 3u)), (mm >> 2) & 1u);
                 if (L < kDecayChunk) {
-                    // tokens past the end are another sequence's: their y and z, whatever they hold, must not meet
-                    // a zero weight
+                    // tokens past the end are another sequence's: their y, whatever it holds, must not meet a zero
+                    // weight (their z is left out below)
                     if (ok) ok = warp_wait(bar(kBY + int(s)), ring_phase);
                     const uint32_t yt = sb + K::kOffY + s * kTile;
-                    for (int e = st; e < 512 && ok; e += 128) {
-                        const int r = 32 * hf + ((e >> 3) & 31);  // pieces of 16 bytes: 8 a row, 32 rows, 2 column halves
-                        const uint32_t off = uint32_t(e >> 8) * kAtom + uint32_t(r) * 128 + uint32_t(e & 7) * 16;
-                        if (r >= L) {
-                            st_shared_v4(zt + off, make_uint4(0u, 0u, 0u, 0u));
-                            if ((e >> 8) < ya) st_shared_v4(yt + off, make_uint4(0u, 0u, 0u, 0u));
-                        }
+                    for (int e = st; e < 256 * ya && ok; e += 128) {
+                        const int r = 32 * hf + ((e >> 3) & 31);  // pieces of 16 bytes: 8 a row, 32 rows, column halves
+                        if (r >= L)
+                            st_shared_v4(yt + uint32_t(e >> 8) * kAtom + uint32_t(r) * 128 + uint32_t(e & 7) * 16,
+                                         make_uint4(0u, 0u, 0u, 0u));
                     }
                     fence_proxy_async_shared();
-                    // the four warps go on, or stop, together
+                    // all four warps' rows are written before any of them arrives; they go on, or stop, together
                     if (named_sync_or(kBarSplit + hf, 128, !ok)) {
                         ok = false;
                         goto split_done;
@@ -619,6 +621,12 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                     for (int j = 0; j < 4; ++j) {  // groups of 8 tokens
                         uint32_t q[4];
                         ldmatrix_t(src + 1024 * j, q);
+                        if (L < kDecayChunk) {
+                            const int tk = 32 * hf + 8 * j + 2 * (lane & 3);
+                            const uint32_t keep = (tk < L ? 0xffffu : 0u) | (tk + 1 < L ? 0xffff0000u : 0u);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) q[i] &= keep;
+                        }
                         const float2 wt = *reinterpret_cast<const float2 *>(wst + 8 * j);
 #pragma unroll
                         for (int l = 0; l < 2; ++l) {  // 16 z rows
@@ -643,7 +651,10 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(kBW + hf));
+                    if (lane == 0) {
+                        mbar_arrive(bar(kBW + hf));
+                        mbar_arrive(bar(kBZFree + int(s)));
+                    }
                 }
             }
             m += uint32_t(w.nch);
@@ -664,8 +675,16 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                     ok = warp_wait(bar(kBVec + int(mm & 3u)), (mm >> 2) & 1u);
                     if (ok && mm >= 2) ok = warp_wait(bar(kBPFree + int(mm & 1u)), ((mm >> 1) - 1) & 1u);
                     if (ok) ok = warp_wait(bar(kBQK), mm & 1u);
+                    const uint32_t s = mm % kRing;
+                    if (ok && L < kDecayChunk) ok = warp_wait(bar(kBZ + int(s)), (mm / kRing) & 1u);
                     if (!ok) break;
                     tc_fence_after();
+                    if (L < kDecayChunk) {
+                        // tokens past the end are another sequence's: their z must not meet P's zeros
+                        const uint32_t zt = sb + K::kOffZ + s * kTile;
+                        for (int e = 32 * quarter + lane; e < 1024; e += 128)
+                            if (((e >> 3) & 63) >= L) st_shared_v4(zt + uint32_t(e) * 16, make_uint4(0u, 0u, 0u, 0u));
+                    }
                     const float Gr = G[r];
                     const uint32_t base = sb + K::kOffP + (mm & 1u) * kPTile + uint32_t(r) * 128;
 #pragma unroll 1
@@ -788,8 +807,8 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                 }
                 m += uint32_t(w.nch);
             }
-        } else if (warp == kWarpMma && elect_one()) {
-        // ==================== the issuing thread ====================
+        } else if ((warp == kWarpMma || warp == kWarpKv) && elect_one()) {
+        // ==================== the issuing threads ====================
         uint32_t total = 0;
         while (w.next(kSt)) total += uint32_t(w.nch);
         const uint32_t id_qk = idesc_bf16(64, 64, false, false), id_kv = idesc_bf16(128, 64 * ya, false, true);
@@ -808,7 +827,7 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                 for (int i = 0; i < 4; ++i)
                     mma_bf16(tmem + K::kColQK, dx + koff(4 * j) + koff(i), dyd + koff(4 * j) + koff(i), id_qk, i > 0 || j > 0);
             mma_commit(bar(kBQK));
-            if (kDots) mma_commit(bar(kBYFree + int(s)));  // the last reader of y
+            mma_commit(bar(kBYFree + int(s)));
             return true;
         };
         auto issue_kv = [&](uint32_t c, int hf) {
@@ -829,8 +848,7 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
             mma_commit(bar(kBKV0 + hf));
             if (hf) {
                 mbar_arrive(bar(kBKV1));
-                if (!kDots) mma_commit(bar(kBYFree + int(s)));
-                if (kSt) mma_commit(bar(kBZFree + int(s)));
+                mma_commit(bar(kBYFree + int(s)));
             }
             return true;
         };
@@ -851,9 +869,10 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
             mma_commit(bar(kBXFree + int(s)));
             return true;
         };
-        auto issue_x2 = [&](uint32_t c) {
+        auto issue_x2 = [&](uint32_t c, bool first) {  // (first: P(c) has not been waited for)
             const uint32_t s = c % kRing;
-            if (!mbar_wait(bar(kBP + int(c & 1u)), (c >> 1) & 1u)) return false;
+            if (first && !mbar_wait(bar(kBP + int(c & 1u)), (c >> 1) & 1u)) return false;
+            if (!mbar_wait(bar(kBZ + int(s)), (c / kRing) & 1u)) return false;
             tc_fence_after();
             const uint64_t da = smem_desc(sb + K::kOffZ + s * kTile, 8192, 1024);
             const uint64_t db = smem_desc(sb + K::kOffP + (c & 1u) * kPTile, 16, 1024);
@@ -866,19 +885,19 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
             mma_commit(bar(kBPFree + int(c & 1u)));
             return true;
         };
-        if constexpr (kSt) {
+        if (warp == kWarpKv) {
             for (uint32_t c = 0; ok && c < total; ++c) ok = issue_kv(c, 0) && issue_kv(c, 1);
-        } else if constexpr (!kDots) {
+        } else if constexpr (kKind == kPlain) {
+            // QK(c + 1) as soon as the mask warps have read QK(c)
+            if (total > 0) ok = ok && issue_qk(0);
+            for (uint32_t c = 0; ok && c < total; ++c) {
+                ok = issue_x1(c) && mbar_wait(bar(kBP + int(c & 1u)), (c >> 1) & 1u) &&
+                     (c + 1 == total || issue_qk(c + 1)) && issue_x2(c, false);
+            }
+        } else if constexpr (kDots) {
             if (total > 0) ok = ok && issue_qk(0);
             for (uint32_t c = 0; ok && c < total; ++c)
-                ok = issue_kv(c, 0) && issue_kv(c, 1) && issue_x1(c) && issue_x2(c) && (c + 1 == total || issue_qk(c + 1));
-        } else {
-            if (total > 0) ok = ok && issue_kv(0, 0) && issue_kv(0, 1) && issue_qk(0);
-            for (uint32_t c = 0; ok && c < total; ++c) {
-                const bool more = c + 1 < total;
-                ok = (!more || issue_kv(c + 1, 0)) && issue_x1(c) && (!more || issue_kv(c + 1, 1)) && issue_x2(c) &&
-                     (!more || issue_qk(c + 1));
-            }
+                ok = issue_x1(c) && issue_x2(c, true) && (c + 1 == total || issue_qk(c + 1));
         }
         // every product done before the tensor memory goes
         mma_commit(bar(kBDrain));
