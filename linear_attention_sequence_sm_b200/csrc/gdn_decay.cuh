@@ -123,11 +123,14 @@ cudaError_t launch_decay_pass_simt(const DecayPass &p, int32_t dtype, int64_t ma
 bool decay_tc_supported(const gdn_shape_t &s);
 cudaError_t launch_decay_pass_tc(const DecayPass &p, int64_t max_units, cudaStream_t stream);
 
-// Pairs inside a chunk for the decays' gradient: intra [hv][tokens].
+// Pairs inside a chunk for the decays' gradient: intra [hv][tokens]; the first
+// for every shape, the second for bf16 with head sizes a multiple of 8.
 cudaError_t launch_decay_intra_simt(const gdn_shape_t &s, const int32_t *cu, const DecayLayout &L,
-                                    const DecaySched &sc, const void *q,
-                                    const void *k, const void *v, const void *d_o, const float *g, bool g_const,
-                                    float *intra, cudaStream_t stream);
+                                    const DecaySched &sc, const void *q, const void *k, const void *v,
+                                    const void *d_o, const float *g, bool g_const, float *intra, cudaStream_t stream);
+cudaError_t launch_decay_intra(const gdn_shape_t &s, const int32_t *cu, const DecayLayout &L, const DecaySched &sc,
+                               const void *q, const void *k, const void *v, const void *d_o, const float *g,
+                               bool g_const, float *intra, cudaStream_t stream);
 
 // dg from its parts, and the sums over grouped value heads.
 cudaError_t launch_decay_dg(const gdn_shape_t &s, const int32_t *cu, const DecayLayout &L, const DecaySched &sc, const float *dot_q,

@@ -289,7 +289,9 @@ gdn_status_t gdn_decay_backward(const gdn_shape_t *s, const void *q, const void 
         return cuda_fail(e, "backward launch");
     if (tokens == 0) return GDN_OK;
     if (dg) {
-        e = launch_decay_intra_simt(*s, cu_seqlens, L, sc, q, k, v, d_o, g, base.g_const, at(L.intra_off), stream);
+        e = decay_tc_supported(*s)
+                ? launch_decay_intra(*s, cu_seqlens, L, sc, q, k, v, d_o, g, base.g_const, at(L.intra_off), stream)
+                : launch_decay_intra_simt(*s, cu_seqlens, L, sc, q, k, v, d_o, g, base.g_const, at(L.intra_off), stream);
         if (e == cudaSuccess)
             e = launch_decay_dg(*s, cu_seqlens, L, sc, pq.dot, pk.dot, at(L.intra_off), pk.zsum, g, base.g_const,
                                 at(L.dgtok_off), dg, stream);
