@@ -17,27 +17,15 @@
 #include <algorithm>
 
 #include "gdn_block_norm.cuh"
+#include "gdn_sm100.cuh"
 
 namespace gdn {
+using namespace sm100;
 
 namespace {
 
-constexpr int kMaxThreads = 1024;
+constexpr int kMaxThreads = 512;  // per block
 
-template <typename T> __device__ __forceinline__ void load8(const T *p, float (&v)[8]);
-template <> __device__ __forceinline__ void load8<float>(const float *p, float (&v)[8]) {
-    const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-template <> __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16 *p, float (&v)[8]) {
-    const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p));
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
 __device__ __forceinline__ void load8w(const float *p, float (&v)[8]) {  // weights: cached
     const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
@@ -57,25 +45,15 @@ template <> __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16 
     __stcs(reinterpret_cast<uint4 *>(p), make_uint4(w[0], w[1], w[2], w[3]));
 }
 
-// A thread's values of a row: group i holds columns 8 (i n + t) .. + 7 (n
-// threads a row) where rows are 16-byte multiples (kVec), else columns
-// (8 i + e) n + t.
-template <bool kVec, typename T>
+// A thread's values of a row.  Aligned rows (16-byte multiples) are staged in
+// shared memory, and group i holds columns 8 (i n + t) .. + 7 (n threads a
+// row); other rows are read directly, columns (8 i + e) n + t.
+template <typename T>
 __device__ __forceinline__ void row_load(const T *row, int i, int t, int n, int width, float (&v)[8]) {
-    if constexpr (kVec) {
-        const int c = 8 * (i * n + t);
-        if (c < width) {
-            load8(row + c, v);
-        } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = 0.f;
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int c = (8 * i + e) * n + t;
-            v[e] = c < width ? to_f32(row[c]) : 0.f;
-        }
+    for (int e = 0; e < 8; ++e) {
+        const int c = (8 * i + e) * n + t;
+        v[e] = c < width ? to_f32(row[c]) : 0.f;
     }
 }
 // Weights of the same columns; `none` where the pointer is NULL.
@@ -85,9 +63,7 @@ __device__ __forceinline__ void weight_load(const float *w, float none, float ad
     if (!w) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = none;
-        return;
-    }
-    if constexpr (kVec) {
+    } else if constexpr (kVec) {
         const int c = 8 * (i * n + t);
         if (c < width) {
             load8w(w + c, v);
@@ -102,8 +78,10 @@ __device__ __forceinline__ void weight_load(const float *w, float none, float ad
             v[e] = c < width ? __ldg(w + c) : 0.f;
         }
     }
+    if (add != 0.f) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += add;
+        for (int e = 0; e < 8; ++e) v[e] += add;
+    }
 }
 template <bool kVec, typename T>
 __device__ __forceinline__ void row_store(T *row, int i, int t, int n, int width, const float (&v)[8]) {
@@ -118,6 +96,69 @@ __device__ __forceinline__ void row_store(T *row, int i, int t, int n, int width
         }
     }
 }
+
+// Eight values of a staged row, zeros past its end.
+template <typename T>
+__device__ __forceinline__ void staged(const unsigned char *row, int c, int width, float (&v)[8]) {
+    if (c >= width) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    } else if constexpr (sizeof(T) == 4) {
+        const float4 a = *reinterpret_cast<const float4 *>(row + 4 * c), b = *reinterpret_cast<const float4 *>(row + 4 * c + 16);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+        const uint4 a = *reinterpret_cast<const uint4 *>(row + 2 * c);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+}
+
+// The staged rows: a block takes blockDim.y consecutive rows at a time, which
+// are one run of bytes of each tensor; kStages groups are in flight as bulk
+// copies counted on an mbarrier each.
+constexpr int kMaxTensors = 5;
+struct Stages {
+    const unsigned char *src[kMaxTensors];  // NULL: not wanted
+    uint32_t row_bytes[kMaxTensors], off[kMaxTensors];  // a row's bytes; where its group starts in a stage
+    uint32_t stage_bytes;
+};
+template <int kStages> struct Pipe {
+    uint32_t bars, buf;
+    int64_t rows;
+    int per;
+    __device__ void init(unsigned char *smem, int64_t rows_, int per_) {
+        bars = smem_u32(smem);
+        buf = bars + 64;
+        rows = rows_;
+        per = per_;
+        if (threadIdx.x == 0 && threadIdx.y == 0) {
+            for (int i = 0; i < kStages; ++i) mbar_init(bars + 8 * i, 1);
+            fence_mbarrier_init();
+        }
+        __syncthreads();
+    }
+    // one thread: the copies of the `it`-th group of this block
+    __device__ void fetch(const Stages &s, int64_t it) {
+        const int64_t first = (it * gridDim.x + blockIdx.x) * per;
+        if (first >= rows) return;
+        const uint32_t live = uint32_t(rows - first < per ? rows - first : per);
+        const uint32_t st = uint32_t(it % kStages), bar = bars + 8 * st, dst = buf + st * s.stage_bytes;
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int i = 0; i < kMaxTensors; ++i)
+            if (s.src[i]) bytes += live * s.row_bytes[i];
+        mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+        for (int i = 0; i < kMaxTensors; ++i)
+            if (s.src[i]) bulk_load(dst + s.off[i], s.src[i] + first * int64_t(s.row_bytes[i]), live * s.row_bytes[i], bar);
+    }
+    // every thread; false: the copy did not arrive in time
+    __device__ bool wait(int64_t it) const { return mbar_wait(bars + 8 * uint32_t(it % kStages), uint32_t(it / kStages) & 1u); }
+};
 
 // Sums of kN values over the n threads of a row (n a multiple of 32; the
 // block's rows reduce together).  `red` has kN * 32 floats per row.
@@ -150,9 +191,90 @@ template <typename T> __device__ __forceinline__ float gate_sigmoid(float z) {
     return sigmoid_fast(z);
 }
 
-template <typename T, typename R, bool kVec, int kGroups>
+// Aligned rows.  Per row 20 bytes of inputs and outputs a column and some 20
+// instructions: memory-bound once enough rows are in flight, so each block
+// keeps kFwdStages groups of rows coming while it works on one (two blocks an
+// SM at 4096 columns).
+constexpr int kFwdStages = 3;
+template <typename T, typename R, int kGroups>
+__global__ void __launch_bounds__(512, 2)
+block_norm_forward_kernel(const BlockNormArgs a, const Stages sg) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ float red_all[32 * 16];
+    const int n = blockDim.x, t = threadIdx.x, width = a.width;
+    const bool leader = threadIdx.x == 0 && threadIdx.y == 0;
+    float *red = red_all + 32 * threadIdx.y;
+    Pipe<kFwdStages> pipe;
+    pipe.init(smem, a.rows, blockDim.y);
+    const bool post = a.flags & GDN_BLOCK_POST_NORM, pre = a.flags & GDN_BLOCK_PRE_NORM;
+    const bool silu = a.flags & GDN_BLOCK_GATE_SILU, gated = sg.src[1] != nullptr, res = sg.src[2] != nullptr;
+    const float zc = (a.flags & GDN_BLOCK_ZERO_CENTRED) ? 1.f : 0.f, none = 1.f - zc;
+    const int64_t groups = (a.rows + blockDim.y - 1) / blockDim.y;
+    if (leader)
+        for (int i = 0; i < kFwdStages; ++i) pipe.fetch(sg, i);
+    for (int64_t it = 0; it * gridDim.x + blockIdx.x < groups; ++it) {
+        const int64_t row = (it * gridDim.x + blockIdx.x) * blockDim.y + threadIdx.y;
+        const bool live = row < a.rows && pipe.wait(it);
+        const unsigned char *st = smem + 64 + (it % kFwdStages) * sg.stage_bytes;
+        auto at = [&](int i) { return st + sg.off[i] + threadIdx.y * sg.row_bytes[i]; };
+        const int64_t base = row * width;
+        float xv[kGroups][8], scale1 = 1.f;
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) staged<T>(at(0), 8 * (i * n + t), live ? width : 0, xv[i]);
+        if (post) {
+            float ss[1] = {0.f};
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ss[0] = fmaf(xv[i][e], xv[i][e], ss[0]);
+            row_sum(ss, red, t, n);
+            scale1 = 1.f / sqrtf(ss[0] / float(width) + a.eps);
+        }
+        float ss[1] = {0.f};
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            const int c = 8 * (i * n + t);
+            float w1[8], s[8], zv[8], rv[8];
+            weight_load<true>(post ? a.post_weight : nullptr, post ? none : 1.f, post ? zc : 0.f, i, t, n, width, w1);
+            weight_load<true>(a.scale, 1.f, 0.f, i, t, n, width, s);
+            if (gated) staged<T>(at(1), c, live ? width : 0, zv);
+            if (res) staged<R>(at(2), c, live ? width : 0, rv);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float b = xv[i][e] * scale1 * w1[e];
+                if (gated) {
+                    const float g = gate_sigmoid<T>(zv[e]);
+                    b *= silu ? zv[e] * g : g;
+                }
+                b *= a.branch_scale * s[e];
+                xv[i][e] = res ? fmaf(a.residual_scale, rv[e], b) : b;  // h
+                ss[0] = fmaf(xv[i][e], xv[i][e], ss[0]);
+            }
+        }
+        __syncthreads();  // the stage has been read
+        if (leader) pipe.fetch(sg, it + kFwdStages);
+        if (live && a.h)
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) row_store<true>(static_cast<R *>(a.h) + base, i, t, n, width, xv[i]);
+        if (!pre) continue;
+        row_sum(ss, red, t, n);
+        const float scale2 = 1.f / sqrtf(ss[0] / float(width) + a.eps);
+        if (!live) continue;
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            float w2[8];
+            weight_load<true>(a.pre_weight, none, zc, i, t, n, width, w2);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w2[e] *= xv[i][e] * scale2;
+            row_store<true>(static_cast<T *>(a.y) + base, i, t, n, width, w2);
+        }
+    }
+}
+
+// Rows of any alignment, read directly.
+template <typename T, typename R, int kGroups>
 __global__ void __launch_bounds__(kMaxThreads)
-block_norm_forward_kernel(const BlockNormArgs a) {
+block_norm_forward_any_kernel(const BlockNormArgs a) {
     __shared__ float red_all[32 * 8];
     const int n = blockDim.x, t = threadIdx.x, width = a.width;
     const int64_t row = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
@@ -165,7 +287,7 @@ block_norm_forward_kernel(const BlockNormArgs a) {
     const float none = zc != 0.f ? 0.f : 1.f;
     float xv[kGroups][8], hv[kGroups][8];
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i) row_load<kVec>(x, i, t, n, width, xv[i]);
+    for (int i = 0; i < kGroups; ++i) row_load(x, i, t, n, width, xv[i]);
     float scale1 = 1.f;
     const bool post = a.flags & GDN_BLOCK_POST_NORM;
     if (post) {
@@ -181,10 +303,10 @@ block_norm_forward_kernel(const BlockNormArgs a) {
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
         float w1[8], s[8], zv[8], rv[8];
-        weight_load<kVec>(post ? a.post_weight : nullptr, post ? none : 1.f, post ? zc : 0.f, i, t, n, width, w1);
-        weight_load<kVec>(a.scale, 1.f, 0.f, i, t, n, width, s);
-        if (z) row_load<kVec>(z, i, t, n, width, zv);
-        if (r) row_load<kVec>(r, i, t, n, width, rv);
+        weight_load<false>(post ? a.post_weight : nullptr, post ? none : 1.f, post ? zc : 0.f, i, t, n, width, w1);
+        weight_load<false>(a.scale, 1.f, 0.f, i, t, n, width, s);
+        if (z) row_load(z, i, t, n, width, zv);
+        if (r) row_load(r, i, t, n, width, rv);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             float b = xv[i][e] * scale1 * w1[e];
@@ -199,7 +321,7 @@ block_norm_forward_kernel(const BlockNormArgs a) {
     }
     if (live && a.h)
 #pragma unroll
-        for (int i = 0; i < kGroups; ++i) row_store<kVec>(static_cast<R *>(a.h) + at, i, t, n, width, hv[i]);
+        for (int i = 0; i < kGroups; ++i) row_store<false>(static_cast<R *>(a.h) + at, i, t, n, width, hv[i]);
     if (!(a.flags & GDN_BLOCK_PRE_NORM)) return;
     row_sum(ss, red, t, n);
     const float scale2 = 1.f / sqrtf(ss[0] / float(width) + a.eps);
@@ -207,18 +329,169 @@ block_norm_forward_kernel(const BlockNormArgs a) {
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
         float w2[8];
-        weight_load<kVec>(a.pre_weight, none, zc, i, t, n, width, w2);
+        weight_load<false>(a.pre_weight, none, zc, i, t, n, width, w2);
 #pragma unroll
         for (int e = 0; e < 8; ++e) w2[e] *= hv[i][e] * scale2;
-        row_store<kVec>(static_cast<T *>(a.y) + at, i, t, n, width, w2);
+        row_store<false>(static_cast<T *>(a.y) + at, i, t, n, width, w2);
+    }
+}
+
+// Aligned rows: a block's row groups walk the rows with a stride, kBwdStages
+// groups in flight; a thread's columns keep their weights and their sums over
+// rows in registers (the sums go to the row group's own line of the workspace
+// at the end).  Three sums a row: x^2; h^2 and dy w2 h together; dn1 . n1.
+// About 45 instructions a column against 40 bytes of memory traffic: at 4096
+// bf16 columns the issue slots are busy about as long as the memory.
+constexpr int kBwdStages = 2;
+template <typename T, typename R, int kGroups>
+__global__ void __launch_bounds__(512, 1)
+block_norm_backward_kernel(const BlockNormArgs a, const Stages sg) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ float red_all[64 * 16];
+    const int n = blockDim.x, t = threadIdx.x, width = a.width;
+    const bool leader = threadIdx.x == 0 && threadIdx.y == 0;
+    float *red = red_all + 64 * threadIdx.y;
+    Pipe<kBwdStages> pipe;
+    pipe.init(smem, a.rows, blockDim.y);
+    const bool post = a.flags & GDN_BLOCK_POST_NORM, pre = sg.src[3] != nullptr;
+    const bool silu = a.flags & GDN_BLOCK_GATE_SILU, gated = sg.src[1] != nullptr, res = sg.src[2] != nullptr;
+    const bool has_dh = sg.src[4] != nullptr;
+    const float zc = (a.flags & GDN_BLOCK_ZERO_CENTRED) ? 1.f : 0.f, none = 1.f - zc;
+    const int64_t groups = (a.rows + blockDim.y - 1) / blockDim.y;
+    if (leader)
+        for (int i = 0; i < kBwdStages; ++i) pipe.fetch(sg, i);
+    float sw1[kGroups][8], sw2[kGroups][8], ssc[kGroups][8];
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sw1[i][e] = sw2[i][e] = ssc[i][e] = 0.f;
+    for (int64_t it = 0; it * gridDim.x + blockIdx.x < groups; ++it) {
+        const int64_t row = (it * gridDim.x + blockIdx.x) * blockDim.y + threadIdx.y;
+        const bool live = row < a.rows && pipe.wait(it);
+        const unsigned char *st = smem + 64 + (it % kBwdStages) * sg.stage_bytes;
+        auto at = [&](int i) { return st + sg.off[i] + threadIdx.y * sg.row_bytes[i]; };
+        const int64_t base = row * width;
+        const int lw = live ? width : 0;  // rows past the end read as zeros and add zeros
+        float nv[kGroups][8], scale1 = 1.f;
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) staged<T>(at(0), 8 * (i * n + t), lw, nv[i]);
+        if (post) {
+            float ss[1] = {0.f};
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ss[0] = fmaf(nv[i][e], nv[i][e], ss[0]);
+            row_sum(ss, red, t, n);
+            scale1 = 1.f / sqrtf(ss[0] / float(width) + a.eps);
+        }
+        float hv[kGroups][8], s2[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            const int c = 8 * (i * n + t);
+            float w1[8], s[8], w2[8], zv[8], yv[8];
+            weight_load<true>(post ? a.post_weight : nullptr, post ? none : 1.f, post ? zc : 0.f, i, t, n, width, w1);
+            weight_load<true>(a.scale, 1.f, 0.f, i, t, n, width, s);
+            if (pre) weight_load<true>(a.pre_weight, none, zc, i, t, n, width, w2);
+            if (gated) staged<T>(at(1), c, lw, zv);
+            if (res) staged<R>(at(2), c, lw, hv[i]);
+            if (pre) staged<T>(at(3), c, lw, yv);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                nv[i][e] *= scale1;
+                float b = nv[i][e] * w1[e];
+                if (gated) {
+                    const float g = gate_sigmoid<T>(zv[e]);
+                    b *= silu ? zv[e] * g : g;
+                }
+                b *= a.branch_scale * s[e];
+                hv[i][e] = res ? fmaf(a.residual_scale, hv[i][e], b) : b;
+                if (pre) {
+                    s2[0] = fmaf(hv[i][e], hv[i][e], s2[0]);
+                    s2[1] = fmaf(yv[e] * w2[e], hv[i][e], s2[1]);
+                }
+            }
+        }
+        float scale2 = 0.f, mean2 = 0.f;
+        if (pre) {
+            row_sum(s2, red, t, n);
+            scale2 = 1.f / sqrtf(s2[0] / float(width) + a.eps);
+            mean2 = scale2 * s2[1] / float(width);  // mean(dn2 . n2)
+        }
+        float s3[1] = {0.f};
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            const int c = 8 * (i * n + t);
+            float w1[8], s[8], w2[8], zv[8], yv[8], ev[8];
+            weight_load<true>(post ? a.post_weight : nullptr, post ? none : 1.f, post ? zc : 0.f, i, t, n, width, w1);
+            weight_load<true>(a.scale, 1.f, 0.f, i, t, n, width, s);
+            if (has_dh) {
+                staged<R>(at(4), c, lw, ev);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ev[e] = 0.f;
+            }
+            if (pre) {
+                weight_load<true>(a.pre_weight, none, zc, i, t, n, width, w2);
+                staged<T>(at(3), c, lw, yv);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float n2 = hv[i][e] * scale2;
+                    sw2[i][e] = fmaf(yv[e], n2, sw2[i][e]);
+                    ev[e] = fmaf(scale2, fmaf(-n2, mean2, yv[e] * w2[e]), ev[e]);  // h's whole gradient
+                }
+            }
+            if (gated) staged<T>(at(1), c, lw, zv);
+            if (live && a.d_residual) {
+                float dr[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) dr[e] = a.residual_scale * ev[e];
+                row_store<true>(static_cast<R *>(a.d_residual) + base, i, t, n, width, dr);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float n1 = nv[i][e], u = n1 * w1[e], cg = a.branch_scale * ev[e], db = cg * s[e];
+                float act = 1.f;
+                if (gated) {
+                    const float zz = zv[e], g = gate_sigmoid<T>(zz);
+                    act = silu ? zz * g : g;
+                    zv[e] = db * u * (silu ? fmaf(act, 1.f - g, g) : g * (1.f - g));
+                }
+                const float du = gated ? db * act : db;
+                ssc[i][e] = fmaf(cg, u * act, ssc[i][e]);
+                sw1[i][e] = fmaf(du, n1, sw1[i][e]);
+                hv[i][e] = du * w1[e];  // dn1 (dx without the norm)
+                s3[0] = fmaf(hv[i][e], n1, s3[0]);
+            }
+            if (live && a.d_gate) row_store<true>(static_cast<T *>(a.d_gate) + base, i, t, n, width, zv);
+        }
+        __syncthreads();  // the stage has been read
+        if (leader) pipe.fetch(sg, it + kBwdStages);
+        if (post) {
+            row_sum(s3, red, t, n);
+            const float mean1 = s3[0] / float(width);
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) hv[i][e] = scale1 * fmaf(-nv[i][e], mean1, hv[i][e]);
+        }
+        if (live && a.dx)
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) row_store<true>(static_cast<T *>(a.dx) + base, i, t, n, width, hv[i]);
+    }
+    float *out = a.partial + (int64_t(blockIdx.x) * blockDim.y + threadIdx.y) * 3 * width;
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+        if (a.d_post_weight) row_store<true>(out, i, t, n, width, sw1[i]);
+        if (a.d_scale) row_store<true>(out + width, i, t, n, width, ssc[i]);
+        if (a.d_pre_weight) row_store<true>(out + 2 * width, i, t, n, width, sw2[i]);
     }
 }
 
 // A block row-group (threadIdx.y) walks rows with a stride; its columns' sums
 // stay in registers and go to its own line of the workspace.
-template <typename T, typename R, bool kVec, int kGroups>
+template <typename T, typename R, int kGroups>
 __global__ void __launch_bounds__(512)
-block_norm_backward_kernel(const BlockNormArgs a) {
+block_norm_backward_any_kernel(const BlockNormArgs a) {
     __shared__ float red_all[64 * 8];
     const int n = blockDim.x, t = threadIdx.x, width = a.width;
     float *red = red_all + 64 * threadIdx.y;
@@ -242,17 +515,17 @@ block_norm_backward_kernel(const BlockNormArgs a) {
         float xv[kGroups][8], zv[kGroups][8], hv[kGroups][8], yv[kGroups][8], ev[kGroups][8];
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
-            row_load<kVec>(x, i, t, n, width, xv[i]);
-            if (z) row_load<kVec>(z, i, t, n, width, zv[i]);
+            row_load(x, i, t, n, width, xv[i]);
+            if (z) row_load(z, i, t, n, width, zv[i]);
             if (r) {
-                row_load<kVec>(r, i, t, n, width, hv[i]);
+                row_load(r, i, t, n, width, hv[i]);
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) hv[i][e] = 0.f;
             }
-            if (pre) row_load<kVec>(static_cast<const T *>(a.d_y) + at, i, t, n, width, yv[i]);
+            if (pre) row_load(static_cast<const T *>(a.d_y) + at, i, t, n, width, yv[i]);
             if (a.d_h) {
-                row_load<kVec>(static_cast<const R *>(a.d_h) + at, i, t, n, width, ev[i]);
+                row_load(static_cast<const R *>(a.d_h) + at, i, t, n, width, ev[i]);
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) ev[i][e] = 0.f;
@@ -273,9 +546,9 @@ block_norm_backward_kernel(const BlockNormArgs a) {
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
             float w1[8], s[8], w2[8];
-            weight_load<kVec>(post ? a.post_weight : nullptr, post ? none : 1.f, post ? zc : 0.f, i, t, n, width, w1);
-            weight_load<kVec>(a.scale, 1.f, 0.f, i, t, n, width, s);
-            if (pre) weight_load<kVec>(a.pre_weight, none, zc, i, t, n, width, w2);
+            weight_load<false>(post ? a.post_weight : nullptr, post ? none : 1.f, post ? zc : 0.f, i, t, n, width, w1);
+            weight_load<false>(a.scale, 1.f, 0.f, i, t, n, width, s);
+            if (pre) weight_load<false>(a.pre_weight, none, zc, i, t, n, width, w2);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 xv[i][e] *= scale1;  // n1
@@ -301,9 +574,9 @@ block_norm_backward_kernel(const BlockNormArgs a) {
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
             float w1[8], s[8], w2[8], dr[8], dzv[8];
-            weight_load<kVec>(post ? a.post_weight : nullptr, post ? none : 1.f, post ? zc : 0.f, i, t, n, width, w1);
-            weight_load<kVec>(a.scale, 1.f, 0.f, i, t, n, width, s);
-            if (pre) weight_load<kVec>(a.pre_weight, none, zc, i, t, n, width, w2);
+            weight_load<false>(post ? a.post_weight : nullptr, post ? none : 1.f, post ? zc : 0.f, i, t, n, width, w1);
+            weight_load<false>(a.scale, 1.f, 0.f, i, t, n, width, s);
+            if (pre) weight_load<false>(a.pre_weight, none, zc, i, t, n, width, w2);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 float g = ev[i][e];
@@ -330,8 +603,8 @@ block_norm_backward_kernel(const BlockNormArgs a) {
                 ev[i][e] = du * w1[e];  // dn1 (dx without the norm)
                 s3[0] = fmaf(ev[i][e], n1, s3[0]);
             }
-            if (live && a.d_residual) row_store<kVec>(static_cast<R *>(a.d_residual) + at, i, t, n, width, dr);
-            if (live && a.d_gate) row_store<kVec>(static_cast<T *>(a.d_gate) + at, i, t, n, width, dzv);
+            if (live && a.d_residual) row_store<false>(static_cast<R *>(a.d_residual) + at, i, t, n, width, dr);
+            if (live && a.d_gate) row_store<false>(static_cast<T *>(a.d_gate) + at, i, t, n, width, dzv);
         }
         if (post) {
             row_sum(s3, red, t, n);
@@ -343,14 +616,14 @@ block_norm_backward_kernel(const BlockNormArgs a) {
         }
         if (live && a.dx)
 #pragma unroll
-            for (int i = 0; i < kGroups; ++i) row_store<kVec>(static_cast<T *>(a.dx) + at, i, t, n, width, ev[i]);
+            for (int i = 0; i < kGroups; ++i) row_store<false>(static_cast<T *>(a.dx) + at, i, t, n, width, ev[i]);
     }
     float *out = a.partial + line * 3 * width;
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
-        if (a.d_post_weight) row_store<kVec>(out, i, t, n, width, sw1[i]);
-        if (a.d_scale) row_store<kVec>(out + width, i, t, n, width, ssc[i]);
-        if (a.d_pre_weight) row_store<kVec>(out + 2 * width, i, t, n, width, sw2[i]);
+        if (a.d_post_weight) row_store<false>(out, i, t, n, width, sw1[i]);
+        if (a.d_scale) row_store<false>(out + width, i, t, n, width, ssc[i]);
+        if (a.d_pre_weight) row_store<false>(out + 2 * width, i, t, n, width, sw2[i]);
     }
 }
 
@@ -380,52 +653,94 @@ block_norm_columns_kernel(const float *__restrict__ part, int lines, int width, 
 // Threads a row takes (a multiple of 32) with `groups` 8-value groups each.
 int row_threads(int width, int groups) { return ((width + 8 * groups - 1) / (8 * groups) + 31) / 32 * 32; }
 
-template <typename T, typename R>
-bool rows_vectorised(const BlockNormArgs &a) {
-    return a.width % (16 / int(sizeof(T))) == 0 && a.width % 8 == 0;
+// Launch shape: threads per row and rows per block (256 threads at least, so
+// that short rows fill an SM), 8 columns a thread up to 4096 columns.
+struct Shape {
+    int groups, n, per;
+};
+Shape shape_of(int width) {
+    Shape s;
+    s.groups = width <= 4096 ? 1 : width <= 8192 ? 2 : 4;
+    s.n = row_threads(width, s.groups);
+    s.per = std::max(1, std::min(8, 256 / s.n));
+    return s;
 }
+
+Stages stages_of(const void *const *src, const int *size, int count, int width, int per) {
+    Stages s = {};
+    for (int i = 0; i < count; ++i) {
+        s.src[i] = static_cast<const unsigned char *>(src[i]);
+        s.row_bytes[i] = uint32_t(width) * uint32_t(size[i]);
+        s.off[i] = s.stage_bytes;
+        if (src[i]) s.stage_bytes += s.row_bytes[i] * uint32_t(per);
+    }
+    return s;
+}
+
+template <typename K>
+cudaError_t staged_launch(K kern, int stages, const BlockNormArgs &a, const Stages &sg, int grid, dim3 block,
+                          cudaStream_t stream) {
+    const size_t bytes = 64 + size_t(stages) * sg.stage_bytes;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    if (e != cudaSuccess) return e;
+    kern<<<unsigned(grid), block, bytes, stream>>>(a, sg);
+    count_launch();
+    return cudaGetLastError();
+}
+
+// Rows whose bytes are multiples of 16 (8 columns), and two stages of which
+// fit in shared memory, are staged.
+constexpr size_t kStageRoom = 220 * 1024;
+bool aligned_rows(const BlockNormArgs &a) { return a.width % 8 == 0; }
 
 template <typename T, typename R>
 cudaError_t forward_as(const BlockNormArgs &a, cudaStream_t stream) {
-    const bool vec = rows_vectorised<T, R>(a);
-    const int groups = a.width <= 2048 ? 1 : a.width <= 16384 ? 2 : 4;
-    const int n = row_threads(a.width, groups);
-    const int per = std::max(1, std::min(8, 128 / n));
-    const int64_t grid = (a.rows + per - 1) / per;
-    if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    const dim3 block(n, per);
-#define GDN_NORM_FWD(V, G) block_norm_forward_kernel<T, R, V, G><<<unsigned(grid), block, 0, stream>>>(a)
-    if (vec) {
-        if (groups == 1) GDN_NORM_FWD(true, 1); else if (groups == 2) GDN_NORM_FWD(true, 2); else GDN_NORM_FWD(true, 4);
-    } else {
-        if (groups == 1) GDN_NORM_FWD(false, 1); else if (groups == 2) GDN_NORM_FWD(false, 2); else GDN_NORM_FWD(false, 4);
+    const Shape s = shape_of(a.width);
+    const dim3 block(s.n, s.per);
+    const int64_t groups = (a.rows + s.per - 1) / s.per;
+    const void *src[] = {a.x, a.gate, a.residual};
+    const int size[] = {sizeof(T), sizeof(T), sizeof(R)};
+    const Stages sg = stages_of(src, size, 3, a.width, s.per);
+    if (aligned_rows(a) && kFwdStages * size_t(sg.stage_bytes) <= kStageRoom) {
+        const int fit = int(std::max<size_t>(1, kStageRoom / (kFwdStages * size_t(sg.stage_bytes) + 1024)));
+        const int per_sm = std::min(fit, std::max(1, 1024 / (s.n * s.per)));
+        const int grid = int(std::min<int64_t>(groups, int64_t(148) * per_sm));
+        if (s.groups == 1) return staged_launch(block_norm_forward_kernel<T, R, 1>, kFwdStages, a, sg, grid, block, stream);
+        if (s.groups == 2) return staged_launch(block_norm_forward_kernel<T, R, 2>, kFwdStages, a, sg, grid, block, stream);
+        return staged_launch(block_norm_forward_kernel<T, R, 4>, kFwdStages, a, sg, grid, block, stream);
     }
-#undef GDN_NORM_FWD
+    if (groups > INT32_MAX) return cudaErrorInvalidValue;
+    if (s.groups == 1) block_norm_forward_any_kernel<T, R, 1><<<unsigned(groups), block, 0, stream>>>(a);
+    else if (s.groups == 2) block_norm_forward_any_kernel<T, R, 2><<<unsigned(groups), block, 0, stream>>>(a);
+    else block_norm_forward_any_kernel<T, R, 4><<<unsigned(groups), block, 0, stream>>>(a);
     count_launch();
     return cudaGetLastError();
 }
 
 template <typename T, typename R>
 cudaError_t backward_as(const BlockNormArgs &a, cudaStream_t stream) {
-    const bool vec = rows_vectorised<T, R>(a);
-    const int groups = a.width <= 2048 ? 1 : a.width <= 8192 ? 2 : 4;
-    const int n = row_threads(a.width, groups);
-    const int per = std::max(1, std::min(8, 128 / n));
-    const int grid = block_norm_lines(a.rows, a.width) / per;
-    const dim3 block(n, per);
-#define GDN_NORM_BWD(V, G) block_norm_backward_kernel<T, R, V, G><<<unsigned(grid), block, 0, stream>>>(a)
-    if (vec) {
-        if (groups == 1) GDN_NORM_BWD(true, 1); else if (groups == 2) GDN_NORM_BWD(true, 2); else GDN_NORM_BWD(true, 4);
+    const Shape s = shape_of(a.width);
+    const dim3 block(s.n, s.per);
+    const int lines = block_norm_lines(a.rows, a.width), grid = lines / s.per;
+    const void *src[] = {a.x, a.gate, a.residual, a.d_y, a.d_h};
+    const int size[] = {sizeof(T), sizeof(T), sizeof(R), sizeof(T), sizeof(R)};
+    const Stages sg = stages_of(src, size, 5, a.width, s.per);
+    cudaError_t e;
+    if (aligned_rows(a) && kBwdStages * size_t(sg.stage_bytes) <= kStageRoom) {
+        e = s.groups == 1   ? staged_launch(block_norm_backward_kernel<T, R, 1>, kBwdStages, a, sg, grid, block, stream)
+            : s.groups == 2 ? staged_launch(block_norm_backward_kernel<T, R, 2>, kBwdStages, a, sg, grid, block, stream)
+                            : staged_launch(block_norm_backward_kernel<T, R, 4>, kBwdStages, a, sg, grid, block, stream);
     } else {
-        if (groups == 1) GDN_NORM_BWD(false, 1); else if (groups == 2) GDN_NORM_BWD(false, 2); else GDN_NORM_BWD(false, 4);
+        if (s.groups == 1) block_norm_backward_any_kernel<T, R, 1><<<unsigned(grid), block, 0, stream>>>(a);
+        else if (s.groups == 2) block_norm_backward_any_kernel<T, R, 2><<<unsigned(grid), block, 0, stream>>>(a);
+        else block_norm_backward_any_kernel<T, R, 4><<<unsigned(grid), block, 0, stream>>>(a);
+        count_launch();
+        e = cudaGetLastError();
     }
-#undef GDN_NORM_BWD
-    count_launch();
-    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     if (a.d_post_weight || a.d_scale || a.d_pre_weight) {
         block_norm_columns_kernel<<<dim3(unsigned((a.width + 31) / 32), 3), dim3(32, 16), 0, stream>>>(
-            a.partial, grid * per, a.width, a.d_post_weight, a.d_scale, a.d_pre_weight);
+            a.partial, lines, a.width, a.d_post_weight, a.d_scale, a.d_pre_weight);
         count_launch();
         e = cudaGetLastError();
     }
@@ -436,11 +751,10 @@ cudaError_t backward_as(const BlockNormArgs &a, cudaStream_t stream) {
 
 // Row groups of the backward, each with a line of column sums in the workspace.
 int block_norm_lines(int64_t rows, int32_t width) {
-    const int groups = width <= 2048 ? 1 : width <= 8192 ? 2 : 4;
-    const int n = row_threads(width, groups), per = std::max(1, std::min(8, 128 / n));
-    const int resident = std::max(1, 512 / (n * per));  // blocks an SM holds at the kernel's registers
-    const int64_t blocks = std::min<int64_t>((rows + per - 1) / per, int64_t(148) * resident);
-    return int(std::max<int64_t>(blocks, 1)) * per;
+    const Shape s = shape_of(width);
+    const int resident = std::max(1, 512 / (s.n * s.per));  // blocks an SM holds at the kernel's registers
+    const int64_t blocks = std::min<int64_t>((rows + s.per - 1) / s.per, int64_t(148) * resident);
+    return int(std::max<int64_t>(blocks, 1)) * s.per;
 }
 
 cudaError_t launch_block_norm_forward(const BlockNormArgs &a, int32_t dtype, int32_t rdtype, cudaStream_t stream) {
