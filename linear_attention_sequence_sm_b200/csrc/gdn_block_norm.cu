@@ -188,19 +188,38 @@ __device__ __forceinline__ void row_sum(float (&v)[kN], float *red, int t, int n
 // about 1e-6 off relative to the result, far below their rounding.
 template <typename T> __device__ __forceinline__ float gate_sigmoid(float z) {
     if constexpr (sizeof(T) == 4) return sigmoid(z);
-    return sigmoid_fast(z);
+    float r;  // (e^-z overflows to infinity below -88: the reciprocal is then 0, as it should be)
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-z)));
+    return r;
 }
 
-// Aligned rows.  Per row 20 bytes of inputs and outputs a column and some 20
-// instructions: memory-bound once enough rows are in flight, so each block
-// keeps kFwdStages groups of rows coming while it works on one (two blocks an
-// SM at 4096 columns).
+// A thread's weights of eight columns of an aligned row: w1 and w2 as the norms
+// use them, and branch_scale s (zeros past the row's end).
+struct Weights {
+    float w1[8], s[8], w2[8];
+    __device__ __forceinline__ void load(const BlockNormArgs &a, int i, int t, int n, int width) {
+        const bool post = a.flags & GDN_BLOCK_POST_NORM;
+        const float zc = (a.flags & GDN_BLOCK_ZERO_CENTRED) ? 1.f : 0.f, none = 1.f - zc;
+        weight_load<true>(post ? a.post_weight : nullptr, post ? none : 1.f, post ? zc : 0.f, i, t, n, width, w1);
+        weight_load<true>(a.scale, 1.f, 0.f, i, t, n, width, s);
+        weight_load<true>(a.pre_weight, none, zc, i, t, n, width, w2);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] *= a.branch_scale;
+    }
+};
+
+// Aligned rows.  A block walks the rows with a stride and keeps kFwdStages
+// groups of them coming; a thread's weights stay in registers (up to 8192
+// columns).  About 20 instructions a column against 10 bytes of memory
+// traffic at bf16: both take about as long, so the fixed work of a row (two
+// sums over the block) is spread over 16 columns a thread.
 constexpr int kFwdStages = 3;
-template <typename T, typename R, int kGroups>
-__global__ void __launch_bounds__(512, 2)
+template <typename T, typename R, int kGroups, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1)
 block_norm_forward_kernel(const BlockNormArgs a, const Stages sg) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float red_all[32 * 16];
+    constexpr bool kKeep = kGroups <= 2;
     const int n = blockDim.x, t = threadIdx.x, width = a.width;
     const bool leader = threadIdx.x == 0 && threadIdx.y == 0;
     float *red = red_all + 32 * threadIdx.y;
@@ -208,19 +227,33 @@ block_norm_forward_kernel(const BlockNormArgs a, const Stages sg) {
     pipe.init(smem, a.rows, blockDim.y);
     const bool post = a.flags & GDN_BLOCK_POST_NORM, pre = a.flags & GDN_BLOCK_PRE_NORM;
     const bool silu = a.flags & GDN_BLOCK_GATE_SILU, gated = sg.src[1] != nullptr, res = sg.src[2] != nullptr;
-    const float zc = (a.flags & GDN_BLOCK_ZERO_CENTRED) ? 1.f : 0.f, none = 1.f - zc;
+    const float inv_width = 1.f / float(width);
     const int64_t groups = (a.rows + blockDim.y - 1) / blockDim.y;
     if (leader)
         for (int i = 0; i < kFwdStages; ++i) pipe.fetch(sg, i);
+    float w1s[kKeep ? kGroups : 1][8], w2[kKeep ? kGroups : 1][8];  // w1 branch_scale s, w2
+    auto weights = [&](int i, float (&u)[8], float (&v)[8]) {
+        Weights w;
+        w.load(a, i, t, n, width);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            u[e] = w.w1[e] * w.s[e];
+            v[e] = w.w2[e];
+        }
+    };
+    if constexpr (kKeep)
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) weights(i, w1s[i], w2[i]);
     for (int64_t it = 0; it * gridDim.x + blockIdx.x < groups; ++it) {
         const int64_t row = (it * gridDim.x + blockIdx.x) * blockDim.y + threadIdx.y;
         const bool live = row < a.rows && pipe.wait(it);
         const unsigned char *st = smem + 64 + (it % kFwdStages) * sg.stage_bytes;
         auto at = [&](int i) { return st + sg.off[i] + threadIdx.y * sg.row_bytes[i]; };
         const int64_t base = row * width;
+        const int lw = live ? width : 0;
         float xv[kGroups][8], scale1 = 1.f;
 #pragma unroll
-        for (int i = 0; i < kGroups; ++i) staged<T>(at(0), 8 * (i * n + t), live ? width : 0, xv[i]);
+        for (int i = 0; i < kGroups; ++i) staged<T>(at(0), 8 * (i * n + t), lw, xv[i]);
         if (post) {
             float ss[1] = {0.f};
 #pragma unroll
@@ -228,28 +261,29 @@ block_norm_forward_kernel(const BlockNormArgs a, const Stages sg) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) ss[0] = fmaf(xv[i][e], xv[i][e], ss[0]);
             row_sum(ss, red, t, n);
-            scale1 = 1.f / sqrtf(ss[0] / float(width) + a.eps);
+            scale1 = rsqrtf(fmaf(ss[0], inv_width, a.eps));
         }
         float ss[1] = {0.f};
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
             const int c = 8 * (i * n + t);
-            float w1[8], s[8], zv[8], rv[8];
-            weight_load<true>(post ? a.post_weight : nullptr, post ? none : 1.f, post ? zc : 0.f, i, t, n, width, w1);
-            weight_load<true>(a.scale, 1.f, 0.f, i, t, n, width, s);
-            if (gated) staged<T>(at(1), c, live ? width : 0, zv);
-            if (res) staged<R>(at(2), c, live ? width : 0, rv);
+            if constexpr (!kKeep) weights(i, w1s[0], w2[0]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float b = xv[i][e] * scale1 * w1[e];
-                if (gated) {
-                    const float g = gate_sigmoid<T>(zv[e]);
-                    b *= silu ? zv[e] * g : g;
-                }
-                b *= a.branch_scale * s[e];
-                xv[i][e] = res ? fmaf(a.residual_scale, rv[e], b) : b;  // h
-                ss[0] = fmaf(xv[i][e], xv[i][e], ss[0]);
+            for (int e = 0; e < 8; ++e) xv[i][e] *= scale1 * w1s[kKeep ? i : 0][e];
+            if (gated) {
+                float zv[8];
+                staged<T>(at(1), c, lw, zv);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) xv[i][e] *= gate_sigmoid<T>(zv[e]) * (silu ? zv[e] : 1.f);
             }
+            if (res) {
+                float rv[8];
+                staged<R>(at(2), c, lw, rv);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) xv[i][e] = fmaf(a.residual_scale, rv[e], xv[i][e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss[0] = fmaf(xv[i][e], xv[i][e], ss[0]);  // h
         }
         __syncthreads();  // the stage has been read
         if (leader) pipe.fetch(sg, it + kFwdStages);
@@ -258,15 +292,15 @@ block_norm_forward_kernel(const BlockNormArgs a, const Stages sg) {
             for (int i = 0; i < kGroups; ++i) row_store<true>(static_cast<R *>(a.h) + base, i, t, n, width, xv[i]);
         if (!pre) continue;
         row_sum(ss, red, t, n);
-        const float scale2 = 1.f / sqrtf(ss[0] / float(width) + a.eps);
+        const float scale2 = rsqrtf(fmaf(ss[0], inv_width, a.eps));
         if (!live) continue;
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
-            float w2[8];
-            weight_load<true>(a.pre_weight, none, zc, i, t, n, width, w2);
+            if constexpr (!kKeep) weights(i, w1s[0], w2[0]);
+            float yv[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w2[e] *= xv[i][e] * scale2;
-            row_store<true>(static_cast<T *>(a.y) + base, i, t, n, width, w2);
+            for (int e = 0; e < 8; ++e) yv[e] = xv[i][e] * (scale2 * w2[kKeep ? i : 0][e]);
+            row_store<true>(static_cast<T *>(a.y) + base, i, t, n, width, yv);
         }
     }
 }
@@ -336,18 +370,17 @@ block_norm_forward_any_kernel(const BlockNormArgs a) {
     }
 }
 
-// Aligned rows: a block's row groups walk the rows with a stride, kBwdStages
-// groups in flight; a thread's columns keep their weights and their sums over
-// rows in registers (the sums go to the row group's own line of the workspace
+// Aligned rows: as the forward, with a thread's sums over rows in registers
+// beside its weights (the sums go to the row group's own line of the workspace
 // at the end).  Three sums a row: x^2; h^2 and dy w2 h together; dn1 . n1.
-// About 45 instructions a column against 40 bytes of memory traffic: at 4096
-// bf16 columns the issue slots are busy about as long as the memory.
+// 512 threads of 128 registers fill an SM at 4096 columns.
 constexpr int kBwdStages = 2;
 template <typename T, typename R, int kGroups>
 __global__ void __launch_bounds__(512, 1)
 block_norm_backward_kernel(const BlockNormArgs a, const Stages sg) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float red_all[64 * 16];
+    constexpr bool kKeep = kGroups == 1;
     const int n = blockDim.x, t = threadIdx.x, width = a.width;
     const bool leader = threadIdx.x == 0 && threadIdx.y == 0;
     float *red = red_all + 64 * threadIdx.y;
@@ -356,10 +389,12 @@ block_norm_backward_kernel(const BlockNormArgs a, const Stages sg) {
     const bool post = a.flags & GDN_BLOCK_POST_NORM, pre = sg.src[3] != nullptr;
     const bool silu = a.flags & GDN_BLOCK_GATE_SILU, gated = sg.src[1] != nullptr, res = sg.src[2] != nullptr;
     const bool has_dh = sg.src[4] != nullptr;
-    const float zc = (a.flags & GDN_BLOCK_ZERO_CENTRED) ? 1.f : 0.f, none = 1.f - zc;
+    const float inv_width = 1.f / float(width);
     const int64_t groups = (a.rows + blockDim.y - 1) / blockDim.y;
     if (leader)
         for (int i = 0; i < kBwdStages; ++i) pipe.fetch(sg, i);
+    Weights w;
+    if constexpr (kKeep) w.load(a, 0, t, n, width);
     float sw1[kGroups][8], sw2[kGroups][8], ssc[kGroups][8];
 #pragma unroll
     for (int i = 0; i < kGroups; ++i)
@@ -382,48 +417,63 @@ block_norm_backward_kernel(const BlockNormArgs a, const Stages sg) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) ss[0] = fmaf(nv[i][e], nv[i][e], ss[0]);
             row_sum(ss, red, t, n);
-            scale1 = 1.f / sqrtf(ss[0] / float(width) + a.eps);
+            scale1 = rsqrtf(fmaf(ss[0], inv_width, a.eps));
         }
-        float hv[kGroups][8], s2[2] = {0.f, 0.f};
+        // n1, the gate and its derivative, h, and the sums of h^2 and dy w2 h
+        float hv[kGroups][8], gv[kGroups][8], dv[kGroups][8], s2[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
             const int c = 8 * (i * n + t);
-            float w1[8], s[8], w2[8], zv[8], yv[8];
-            weight_load<true>(post ? a.post_weight : nullptr, post ? none : 1.f, post ? zc : 0.f, i, t, n, width, w1);
-            weight_load<true>(a.scale, 1.f, 0.f, i, t, n, width, s);
-            if (pre) weight_load<true>(a.pre_weight, none, zc, i, t, n, width, w2);
-            if (gated) staged<T>(at(1), c, lw, zv);
-            if (res) staged<R>(at(2), c, lw, hv[i]);
-            if (pre) staged<T>(at(3), c, lw, yv);
+            if constexpr (!kKeep) w.load(a, i, t, n, width);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                nv[i][e] *= scale1;
-                float b = nv[i][e] * w1[e];
-                if (gated) {
-                    const float g = gate_sigmoid<T>(zv[e]);
-                    b *= silu ? zv[e] * g : g;
+            for (int e = 0; e < 8; ++e) nv[i][e] *= scale1;
+            if (gated) {
+                staged<T>(at(1), c, lw, gv[i]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float g = gate_sigmoid<T>(gv[i][e]), act = silu ? gv[i][e] * g : g;
+                    dv[i][e] = fmaf(act, 1.f - g, silu ? g : 0.f);  // act' = g + act (1 - g), or g (1 - g)
+                    gv[i][e] = act;
                 }
-                b *= a.branch_scale * s[e];
-                hv[i][e] = res ? fmaf(a.residual_scale, hv[i][e], b) : b;
-                if (pre) {
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    gv[i][e] = 1.f;
+                    dv[i][e] = 0.f;
+                }
+            }
+            if (res) {
+                staged<R>(at(2), c, lw, hv[i]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) hv[i][e] *= a.residual_scale;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) hv[i][e] = 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) hv[i][e] = fmaf(nv[i][e] * w.w1[e] * gv[i][e], w.s[e], hv[i][e]);
+            if (pre) {
+                float yv[8];
+                staged<T>(at(3), c, lw, yv);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
                     s2[0] = fmaf(hv[i][e], hv[i][e], s2[0]);
-                    s2[1] = fmaf(yv[e] * w2[e], hv[i][e], s2[1]);
+                    s2[1] = fmaf(yv[e] * w.w2[e], hv[i][e], s2[1]);
                 }
             }
         }
         float scale2 = 0.f, mean2 = 0.f;
         if (pre) {
             row_sum(s2, red, t, n);
-            scale2 = 1.f / sqrtf(s2[0] / float(width) + a.eps);
-            mean2 = scale2 * s2[1] / float(width);  // mean(dn2 . n2)
+            scale2 = rsqrtf(fmaf(s2[0], inv_width, a.eps));
+            mean2 = scale2 * s2[1] * inv_width;  // mean(dn2 . n2)
         }
         float s3[1] = {0.f};
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
             const int c = 8 * (i * n + t);
-            float w1[8], s[8], w2[8], zv[8], yv[8], ev[8];
-            weight_load<true>(post ? a.post_weight : nullptr, post ? none : 1.f, post ? zc : 0.f, i, t, n, width, w1);
-            weight_load<true>(a.scale, 1.f, 0.f, i, t, n, width, s);
+            if constexpr (!kKeep) w.load(a, i, t, n, width);
+            float ev[8];  // h's whole gradient
             if (has_dh) {
                 staged<R>(at(4), c, lw, ev);
             } else {
@@ -431,16 +481,15 @@ block_norm_backward_kernel(const BlockNormArgs a, const Stages sg) {
                 for (int e = 0; e < 8; ++e) ev[e] = 0.f;
             }
             if (pre) {
-                weight_load<true>(a.pre_weight, none, zc, i, t, n, width, w2);
+                float yv[8];
                 staged<T>(at(3), c, lw, yv);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float n2 = hv[i][e] * scale2;
                     sw2[i][e] = fmaf(yv[e], n2, sw2[i][e]);
-                    ev[e] = fmaf(scale2, fmaf(-n2, mean2, yv[e] * w2[e]), ev[e]);  // h's whole gradient
+                    ev[e] = fmaf(scale2, fmaf(-n2, mean2, yv[e] * w.w2[e]), ev[e]);
                 }
             }
-            if (gated) staged<T>(at(1), c, lw, zv);
             if (live && a.d_residual) {
                 float dr[8];
 #pragma unroll
@@ -449,26 +498,20 @@ block_norm_backward_kernel(const BlockNormArgs a, const Stages sg) {
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float n1 = nv[i][e], u = n1 * w1[e], cg = a.branch_scale * ev[e], db = cg * s[e];
-                float act = 1.f;
-                if (gated) {
-                    const float zz = zv[e], g = gate_sigmoid<T>(zz);
-                    act = silu ? zz * g : g;
-                    zv[e] = db * u * (silu ? fmaf(act, 1.f - g, g) : g * (1.f - g));
-                }
-                const float du = gated ? db * act : db;
-                ssc[i][e] = fmaf(cg, u * act, ssc[i][e]);
+                const float n1 = nv[i][e], u = n1 * w.w1[e], db = ev[e] * w.s[e], du = db * gv[i][e];
+                ssc[i][e] = fmaf(ev[e], u * gv[i][e], ssc[i][e]);  // (branch_scale at the end)
+                dv[i][e] *= db * u;                                 // dz
                 sw1[i][e] = fmaf(du, n1, sw1[i][e]);
-                hv[i][e] = du * w1[e];  // dn1 (dx without the norm)
+                hv[i][e] = du * w.w1[e];                            // dn1 (dx without the norm)
                 s3[0] = fmaf(hv[i][e], n1, s3[0]);
             }
-            if (live && a.d_gate) row_store<true>(static_cast<T *>(a.d_gate) + base, i, t, n, width, zv);
+            if (live && a.d_gate) row_store<true>(static_cast<T *>(a.d_gate) + base, i, t, n, width, dv[i]);
         }
         __syncthreads();  // the stage has been read
         if (leader) pipe.fetch(sg, it + kBwdStages);
         if (post) {
             row_sum(s3, red, t, n);
-            const float mean1 = s3[0] / float(width);
+            const float mean1 = s3[0] * inv_width;
 #pragma unroll
             for (int i = 0; i < kGroups; ++i)
 #pragma unroll
@@ -481,6 +524,8 @@ block_norm_backward_kernel(const BlockNormArgs a, const Stages sg) {
     float *out = a.partial + (int64_t(blockIdx.x) * blockDim.y + threadIdx.y) * 3 * width;
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ssc[i][e] *= a.branch_scale;
         if (a.d_post_weight) row_store<true>(out, i, t, n, width, sw1[i]);
         if (a.d_scale) row_store<true>(out + width, i, t, n, width, ssc[i]);
         if (a.d_pre_weight) row_store<true>(out + 2 * width, i, t, n, width, sw2[i]);
@@ -666,6 +711,14 @@ Shape shape_of(int width) {
     return s;
 }
 
+Shape forward_shape_of(int width) {  // 16 columns a thread above 2048
+    Shape s;
+    s.groups = width <= 2048 ? 1 : width <= 8192 ? 2 : 4;
+    s.n = row_threads(width, s.groups);
+    s.per = std::max(1, std::min(8, 256 / s.n));
+    return s;
+}
+
 Stages stages_of(const void *const *src, const int *size, int count, int width, int per) {
     Stages s = {};
     for (int i = 0; i < count; ++i) {
@@ -695,7 +748,7 @@ bool aligned_rows(const BlockNormArgs &a) { return a.width % 8 == 0; }
 
 template <typename T, typename R>
 cudaError_t forward_as(const BlockNormArgs &a, cudaStream_t stream) {
-    const Shape s = shape_of(a.width);
+    const Shape s = forward_shape_of(a.width);
     const dim3 block(s.n, s.per);
     const int64_t groups = (a.rows + s.per - 1) / s.per;
     const void *src[] = {a.x, a.gate, a.residual};
@@ -703,11 +756,13 @@ cudaError_t forward_as(const BlockNormArgs &a, cudaStream_t stream) {
     const Stages sg = stages_of(src, size, 3, a.width, s.per);
     if (aligned_rows(a) && kFwdStages * size_t(sg.stage_bytes) <= kStageRoom) {
         const int fit = int(std::max<size_t>(1, kStageRoom / (kFwdStages * size_t(sg.stage_bytes) + 1024)));
-        const int per_sm = std::min(fit, std::max(1, 1024 / (s.n * s.per)));
-        const int grid = int(std::min<int64_t>(groups, int64_t(148) * per_sm));
-        if (s.groups == 1) return staged_launch(block_norm_forward_kernel<T, R, 1>, kFwdStages, a, sg, grid, block, stream);
-        if (s.groups == 2) return staged_launch(block_norm_forward_kernel<T, R, 2>, kFwdStages, a, sg, grid, block, stream);
-        return staged_launch(block_norm_forward_kernel<T, R, 4>, kFwdStages, a, sg, grid, block, stream);
+        const bool small = s.n * s.per <= 256;
+        const int grid = int(std::min<int64_t>(groups, int64_t(148) * (small ? std::min(fit, 3) : 1)));
+        if (s.groups == 1) return staged_launch(block_norm_forward_kernel<T, R, 1, 256>, kFwdStages, a, sg, grid, block, stream);
+        if (s.groups == 2 && small)
+            return staged_launch(block_norm_forward_kernel<T, R, 2, 256>, kFwdStages, a, sg, grid, block, stream);
+        if (s.groups == 2) return staged_launch(block_norm_forward_kernel<T, R, 2, 512>, kFwdStages, a, sg, grid, block, stream);
+        return staged_launch(block_norm_forward_kernel<T, R, 4, 512>, kFwdStages, a, sg, grid, block, stream);
     }
     if (groups > INT32_MAX) return cudaErrorInvalidValue;
     if (s.groups == 1) block_norm_forward_any_kernel<T, R, 1><<<unsigned(groups), block, 0, stream>>>(a);
