@@ -17,6 +17,7 @@
 #include <algorithm>
 
 #include "gdn_block_norm.cuh"
+#include "gdn_f32x2.cuh"
 #include "gdn_sm100.cuh"
 
 namespace gdn {
@@ -30,21 +31,6 @@ __device__ __forceinline__ void load8w(const float *p, float (&v)[8]) {  // weig
     const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
-template <typename T> __device__ __forceinline__ void store8(T *p, const float (&v)[8]);
-template <> __device__ __forceinline__ void store8<float>(float *p, const float (&v)[8]) {
-    __stcs(reinterpret_cast<float4 *>(p), make_float4(v[0], v[1], v[2], v[3]));
-    __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
-}
-template <> __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16 *p, const float (&v)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&t);
-    }
-    __stcs(reinterpret_cast<uint4 *>(p), make_uint4(w[0], w[1], w[2], w[3]));
-}
-
 // A thread's values of a row.  Aligned rows (16-byte multiples) are staged in
 // shared memory, and group i holds columns 8 (i n + t) .. + 7 (n threads a
 // row); other rows are read directly, columns (8 i + e) n + t.
@@ -83,37 +69,36 @@ __device__ __forceinline__ void weight_load(const float *w, float none, float ad
         for (int e = 0; e < 8; ++e) v[e] += add;
     }
 }
-template <bool kVec, typename T>
+template <typename T>
 __device__ __forceinline__ void row_store(T *row, int i, int t, int n, int width, const float (&v)[8]) {
-    if constexpr (kVec) {
-        const int c = 8 * (i * n + t);
-        if (c < width) store8(row + c, v);
-    } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int c = (8 * i + e) * n + t;
-            if (c < width) row[c] = from_f32<T>(v[e]);
-        }
+    for (int e = 0; e < 8; ++e) {
+        const int c = (8 * i + e) * n + t;
+        if (c < width) row[c] = from_f32<T>(v[e]);
     }
 }
 
-// Eight values of a staged row, zeros past its end.
+// Eight values of a staged row as four pairs, zeros past its end.
 template <typename T>
-__device__ __forceinline__ void staged(const unsigned char *row, int c, int width, float (&v)[8]) {
+__device__ __forceinline__ void staged(const unsigned char *row, int c, int width, f32x2 (&v)[4]) {
     if (c >= width) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0.f;
+        for (int i = 0; i < 4; ++i) v[i] = both(0.f);
     } else if constexpr (sizeof(T) == 4) {
-        const float4 a = *reinterpret_cast<const float4 *>(row + 4 * c), b = *reinterpret_cast<const float4 *>(row + 4 * c + 16);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(row + 4 * c);
+        const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(row + 4 * c + 16);
+        v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
     } else {
         const uint4 a = *reinterpret_cast<const uint4 *>(row + 2 * c);
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+        v[0] = from_bf16x2(a.x); v[1] = from_bf16x2(a.y); v[2] = from_bf16x2(a.z); v[3] = from_bf16x2(a.w);
+    }
+}
+template <typename T> __device__ __forceinline__ void store_pairs(T *p, const f32x2 (&v)[4]) {
+    if constexpr (sizeof(T) == 4) {
+        __stcs(reinterpret_cast<float4 *>(p), make_float4(lo_of(v[0]), hi_of(v[0]), lo_of(v[1]), hi_of(v[1])));
+        __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(lo_of(v[2]), hi_of(v[2]), lo_of(v[3]), hi_of(v[3])));
+    } else {
+        __stcs(reinterpret_cast<uint4 *>(p), make_uint4(to_bf16x2(v[0]), to_bf16x2(v[1]), to_bf16x2(v[2]), to_bf16x2(v[3])));
     }
 }
 
@@ -127,26 +112,25 @@ struct Stages {
     uint32_t stage_bytes;
 };
 template <int kStages> struct Pipe {
-    uint32_t bars, buf;
-    int64_t rows;
-    int per;
-    __device__ void init(unsigned char *smem, int64_t rows_, int per_) {
+    uint32_t bars, buf, stage, phase;  // the stage being read and its barrier's phase
+    int rows, per, next;               // the first row of the next group to fetch
+    __device__ void init(unsigned char *smem, int rows_, int per_) {
         bars = smem_u32(smem);
         buf = bars + 64;
         rows = rows_;
         per = per_;
+        stage = phase = 0;
+        next = int(blockIdx.x) * per;
         if (threadIdx.x == 0 && threadIdx.y == 0) {
             for (int i = 0; i < kStages; ++i) mbar_init(bars + 8 * i, 1);
             fence_mbarrier_init();
         }
         __syncthreads();
     }
-    // one thread: the copies of the `it`-th group of this block
-    __device__ void fetch(const Stages &s, int64_t it) {
-        const int64_t first = (it * gridDim.x + blockIdx.x) * per;
-        if (first >= rows) return;
-        const uint32_t live = uint32_t(rows - first < per ? rows - first : per);
-        const uint32_t st = uint32_t(it % kStages), bar = bars + 8 * st, dst = buf + st * s.stage_bytes;
+    // one thread: the copies of this block's next group, into stage `st`
+    __device__ void fetch(const Stages &s, uint32_t st) {
+        if (next >= rows) return;
+        const uint32_t live = uint32_t(min(rows - next, per)), bar = bars + 8 * st, dst = buf + st * s.stage_bytes;
         uint32_t bytes = 0;
 #pragma unroll
         for (int i = 0; i < kMaxTensors; ++i)
@@ -154,59 +138,126 @@ template <int kStages> struct Pipe {
         mbar_arrive_expect_tx(bar, bytes);
 #pragma unroll
         for (int i = 0; i < kMaxTensors; ++i)
-            if (s.src[i]) bulk_load(dst + s.off[i], s.src[i] + first * int64_t(s.row_bytes[i]), live * s.row_bytes[i], bar);
+            if (s.src[i]) bulk_load(dst + s.off[i], s.src[i] + int64_t(next) * s.row_bytes[i], live * s.row_bytes[i], bar);
+        next = next > rows - int(gridDim.x) * per ? rows : next + int(gridDim.x) * per;
     }
     // every thread; false: the copy did not arrive in time
-    __device__ bool wait(int64_t it) const { return mbar_wait(bars + 8 * uint32_t(it % kStages), uint32_t(it / kStages) & 1u); }
+    __device__ bool wait() const { return mbar_wait(bars + 8 * stage, phase); }
+    __device__ void advance() {
+        if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
 };
 
-// Sums of kN values over the n threads of a row (n a multiple of 32; the
-// block's rows reduce together).  `red` has kN * 32 floats per row.
-template <int kN>
+// Sums of kN values over the n threads of a row (n a multiple of 32, at most
+// 32 kWarps; the block's rows reduce together).  `red` has kN * kWarps floats
+// per row, aligned to 16 bytes and zero where a row has no warp (clear_red).
+// Every thread adds the warps' sums itself: the reads are broadcasts, and the
+// chain is shorter than a second tree of shuffles.
+template <int kN, int kWarps>
 __device__ __forceinline__ void row_sum(float (&v)[kN], float *red, int t, int n) {
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1)
 #pragma unroll
         for (int j = 0; j < kN; ++j) v[j] += __shfl_xor_sync(0xffffffffu, v[j], m);
     if (n == 32) return;
-    const int warps = n >> 5, w = t >> 5, lane = t & 31;
     __syncthreads();  // the previous use of `red` has been read
-    if (lane == 0)
+    if ((t & 31) == 0)
 #pragma unroll
-        for (int j = 0; j < kN; ++j) red[32 * j + w] = v[j];
+        for (int j = 0; j < kN; ++j) red[kWarps * j + (t >> 5)] = v[j];
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
-        float s = lane < warps ? red[32 * j + lane] : 0.f;
+        f32x2 s = both(0.f);
 #pragma unroll
-        for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-        v[j] = s;
+        for (int i = 0; i < kWarps; i += 4) {
+            const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(red + kWarps * j + i);
+            s = i == 0 ? add2(x.x, x.y) : add2(s, add2(x.x, x.y));
+        }
+        v[j] = lo_of(s) + hi_of(s);
     }
+}
+template <int kFloats>
+__device__ __forceinline__ void clear_red(float (&red)[kFloats]) {
+    for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < kFloats; i += blockDim.x * blockDim.y) red[i] = 0.f;
+    __syncthreads();
 }
 
 // Sigmoid: the exact exponential for fp32 rows; for bf16 rows the fast one,
 // about 1e-6 off relative to the result, far below their rounding.
 template <typename T> __device__ __forceinline__ float gate_sigmoid(float z) {
     if constexpr (sizeof(T) == 4) return sigmoid(z);
-    float r;  // (e^-z overflows to infinity below -88: the reciprocal is then 0, as it should be)
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-z)));
-    return r;
+    return sigmoid_fast(z);
 }
 
 // A thread's weights of eight columns of an aligned row: w1 and w2 as the norms
 // use them, and branch_scale s (zeros past the row's end).
 struct Weights {
-    float w1[8], s[8], w2[8];
+    f32x2 w1[4], s[4], w2[4];
     __device__ __forceinline__ void load(const BlockNormArgs &a, int i, int t, int n, int width) {
         const bool post = a.flags & GDN_BLOCK_POST_NORM;
         const float zc = (a.flags & GDN_BLOCK_ZERO_CENTRED) ? 1.f : 0.f, none = 1.f - zc;
-        weight_load<true>(post ? a.post_weight : nullptr, post ? none : 1.f, post ? zc : 0.f, i, t, n, width, w1);
-        weight_load<true>(a.scale, 1.f, 0.f, i, t, n, width, s);
-        weight_load<true>(a.pre_weight, none, zc, i, t, n, width, w2);
+        float u[8], v[8], x[8];
+        weight_load(post ? a.post_weight : nullptr, post ? none : 1.f, post ? zc : 0.f, i, t, n, width, u);
+        weight_load(a.scale, 1.f, 0.f, i, t, n, width, v);
+        weight_load(a.pre_weight, none, zc, i, t, n, width, x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[e] *= a.branch_scale;
+        for (int e = 0; e < 4; ++e) {
+            w1[e] = pair(u[2 * e], u[2 * e + 1]);
+            s[e] = mul2(pair(v[2 * e], v[2 * e + 1]), both(a.branch_scale));
+            w2[e] = pair(x[2 * e], x[2 * e + 1]);
+        }
+    }
+    // the same for aligned columns 8 (i n + t) .. + 7
+    static __device__ __forceinline__ void weight_load(const float *w, float none, float add, int i, int t, int n,
+                                                       int width, float (&v)[8]) {
+        gdn::weight_load<true>(w, none, add, i, t, n, width, v);
     }
 };
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp(float x) {  // (of infinity: 0)
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// The gate of four pairs of pre-activations, and its derivative:
+// act' = g + act (1 - g) for SiLU, g (1 - g) for the sigmoid (g the sigmoid).
+template <typename T, bool kGrad>
+__device__ __forceinline__ void gate(bool silu, f32x2 (&z)[4], f32x2 (&slope)[4]) {
+    f32x2 g[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(T) == 4) {
+            g[e] = pair(sigmoid(lo_of(z[e])), sigmoid(hi_of(z[e])));
+        } else {
+            // 1 / (1 + 2^(-z log2 e)) by the hardware's exponential and reciprocal
+            const f32x2 x = mul2(z[e], both(-1.4426950408889634f));
+            f32x2 d = add2(pair(ex2(lo_of(x)), ex2(hi_of(x))), both(1.f));
+            g[e] = pair(rcp(lo_of(d)), rcp(hi_of(d)));
+        }
+    }
+    if (silu) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            z[e] = mul2(z[e], g[e]);
+            if (kGrad) slope[e] = fma2(z[e], fma2(g[e], both(-1.f), both(1.f)), g[e]);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            z[e] = g[e];
+            if (kGrad) slope[e] = mul2(g[e], fma2(g[e], both(-1.f), both(1.f)));
+        }
+    }
+}
 
 // Aligned rows.  A block walks the rows with a stride and keeps kFwdStages
 // groups of them coming; a thread's weights stay in registers (up to 8192
@@ -218,89 +269,98 @@ template <typename T, typename R, int kGroups, int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1)
 block_norm_forward_kernel(const BlockNormArgs a, const Stages sg) {
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ float red_all[32 * 16];
+    constexpr int kWarps = kThreads / 32;
+    __shared__ __align__(16) float red_all[kWarps * 8];
+    clear_red(red_all);
     constexpr bool kKeep = kGroups <= 2;
     const int n = blockDim.x, t = threadIdx.x, width = a.width;
     const bool leader = threadIdx.x == 0 && threadIdx.y == 0;
-    float *red = red_all + 32 * threadIdx.y;
+    float *red = red_all + kWarps * threadIdx.y;
     Pipe<kFwdStages> pipe;
-    pipe.init(smem, a.rows, blockDim.y);
+    pipe.init(smem, int(a.rows), blockDim.y);
     const bool post = a.flags & GDN_BLOCK_POST_NORM, pre = a.flags & GDN_BLOCK_PRE_NORM;
     const bool silu = a.flags & GDN_BLOCK_GATE_SILU, gated = sg.src[1] != nullptr, res = sg.src[2] != nullptr;
     const float inv_width = 1.f / float(width);
-    const int64_t groups = (a.rows + blockDim.y - 1) / blockDim.y;
+    const int rows = int(a.rows), stride = int(gridDim.x * blockDim.y);
     if (leader)
-        for (int i = 0; i < kFwdStages; ++i) pipe.fetch(sg, i);
-    float w1s[kKeep ? kGroups : 1][8], w2[kKeep ? kGroups : 1][8];  // w1 branch_scale s, w2
-    auto weights = [&](int i, float (&u)[8], float (&v)[8]) {
+        for (uint32_t i = 0; i < kFwdStages; ++i) pipe.fetch(sg, i);
+    f32x2 w1s[kKeep ? kGroups : 1][4], w2[kKeep ? kGroups : 1][4];  // w1 branch_scale s, w2
+    auto weights = [&](int i, f32x2 (&u)[4], f32x2 (&v)[4]) {
         Weights w;
         w.load(a, i, t, n, width);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            u[e] = w.w1[e] * w.s[e];
+        for (int e = 0; e < 4; ++e) {
+            u[e] = mul2(w.w1[e], w.s[e]);
             v[e] = w.w2[e];
         }
     };
     if constexpr (kKeep)
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) weights(i, w1s[i], w2[i]);
-    for (int64_t it = 0; it * gridDim.x + blockIdx.x < groups; ++it) {
-        const int64_t row = (it * gridDim.x + blockIdx.x) * blockDim.y + threadIdx.y;
-        const bool live = row < a.rows && pipe.wait(it);
-        const unsigned char *st = smem + 64 + (it % kFwdStages) * sg.stage_bytes;
+    for (int first = int(blockIdx.x * blockDim.y), left = 1; left > 0; first += stride) {
+        left = rows - first - stride;  // (rows < 2^31, and so is first: `left` > 0 while another group follows)
+        const int row = first + int(threadIdx.y);
+        const bool live = row < rows && pipe.wait();
+        const unsigned char *st = smem + 64 + pipe.stage * sg.stage_bytes;
         auto at = [&](int i) { return st + sg.off[i] + threadIdx.y * sg.row_bytes[i]; };
-        const int64_t base = row * width;
+        const int64_t base = int64_t(row) * width + 8 * t;
         const int lw = live ? width : 0;
-        float xv[kGroups][8], scale1 = 1.f;
+        f32x2 xv[kGroups][4];
+        float scale1 = 1.f;
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) staged<T>(at(0), 8 * (i * n + t), lw, xv[i]);
         if (post) {
-            float ss[1] = {0.f};
+            f32x2 ss = both(0.f);
 #pragma unroll
             for (int i = 0; i < kGroups; ++i)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ss[0] = fmaf(xv[i][e], xv[i][e], ss[0]);
-            row_sum(ss, red, t, n);
-            scale1 = rsqrtf(fmaf(ss[0], inv_width, a.eps));
+                for (int e = 0; e < 4; ++e) ss = fma2(xv[i][e], xv[i][e], ss);
+            float s1[1] = {lo_of(ss) + hi_of(ss)};
+            row_sum<1, kWarps>(s1, red, t, n);
+            scale1 = rsqrtf(fmaf(s1[0], inv_width, a.eps));
         }
-        float ss[1] = {0.f};
+        f32x2 ss = both(0.f);
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
             const int c = 8 * (i * n + t);
             if constexpr (!kKeep) weights(i, w1s[0], w2[0]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) xv[i][e] *= scale1 * w1s[kKeep ? i : 0][e];
+            for (int e = 0; e < 4; ++e) xv[i][e] = mul2(mul2(xv[i][e], both(scale1)), w1s[kKeep ? i : 0][e]);
             if (gated) {
-                float zv[8];
+                f32x2 zv[4], none[4];
                 staged<T>(at(1), c, lw, zv);
+                gate<T, false>(silu, zv, none);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) xv[i][e] *= gate_sigmoid<T>(zv[e]) * (silu ? zv[e] : 1.f);
+                for (int e = 0; e < 4; ++e) xv[i][e] = mul2(xv[i][e], zv[e]);
             }
             if (res) {
-                float rv[8];
+                f32x2 rv[4];
                 staged<R>(at(2), c, lw, rv);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) xv[i][e] = fmaf(a.residual_scale, rv[e], xv[i][e]);
+                for (int e = 0; e < 4; ++e) xv[i][e] = fma2(both(a.residual_scale), rv[e], xv[i][e]);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss[0] = fmaf(xv[i][e], xv[i][e], ss[0]);  // h
+            for (int e = 0; e < 4; ++e) ss = fma2(xv[i][e], xv[i][e], ss);  // h
         }
         __syncthreads();  // the stage has been read
-        if (leader) pipe.fetch(sg, it + kFwdStages);
+        if (leader) pipe.fetch(sg, pipe.stage);
+        pipe.advance();
         if (live && a.h)
 #pragma unroll
-            for (int i = 0; i < kGroups; ++i) row_store<true>(static_cast<R *>(a.h) + base, i, t, n, width, xv[i]);
+            for (int i = 0; i < kGroups; ++i)
+                if (8 * (i * n + t) < width) store_pairs(static_cast<R *>(a.h) + base + 8 * i * n, xv[i]);
         if (!pre) continue;
-        row_sum(ss, red, t, n);
-        const float scale2 = rsqrtf(fmaf(ss[0], inv_width, a.eps));
+        float s2[1] = {lo_of(ss) + hi_of(ss)};
+        row_sum<1, kWarps>(s2, red, t, n);
+        const float scale2 = rsqrtf(fmaf(s2[0], inv_width, a.eps));
         if (!live) continue;
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
             if constexpr (!kKeep) weights(i, w1s[0], w2[0]);
-            float yv[8];
+            f32x2 yv[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) yv[e] = xv[i][e] * (scale2 * w2[kKeep ? i : 0][e]);
-            row_store<true>(static_cast<T *>(a.y) + base, i, t, n, width, yv);
+            for (int e = 0; e < 4; ++e) yv[e] = mul2(mul2(xv[i][e], both(scale2)), w2[kKeep ? i : 0][e]);
+            if (8 * (i * n + t) < width) store_pairs(static_cast<T *>(a.y) + base + 8 * i * n, yv);
         }
     }
 }
@@ -309,11 +369,12 @@ block_norm_forward_kernel(const BlockNormArgs a, const Stages sg) {
 template <typename T, typename R, int kGroups>
 __global__ void __launch_bounds__(kMaxThreads)
 block_norm_forward_any_kernel(const BlockNormArgs a) {
-    __shared__ float red_all[32 * 8];
+    __shared__ __align__(16) float red_all[16 * 8];
+    clear_red(red_all);
     const int n = blockDim.x, t = threadIdx.x, width = a.width;
     const int64_t row = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
     const bool live = row < a.rows;
-    float *red = red_all + 32 * threadIdx.y;
+    float *red = red_all + 16 * threadIdx.y;
     const int64_t at = (live ? row : 0) * width;
     const T *x = static_cast<const T *>(a.x) + at, *z = a.gate ? static_cast<const T *>(a.gate) + at : nullptr;
     const R *r = a.residual ? static_cast<const R *>(a.residual) + at : nullptr;
@@ -330,7 +391,7 @@ block_norm_forward_any_kernel(const BlockNormArgs a) {
         for (int i = 0; i < kGroups; ++i)
 #pragma unroll
             for (int e = 0; e < 8; ++e) ss[0] = fmaf(xv[i][e], xv[i][e], ss[0]);
-        row_sum(ss, red, t, n);
+        row_sum<1, 16>(ss, red, t, n);
         scale1 = 1.f / sqrtf(ss[0] / float(width) + a.eps);
     }
     float ss[1] = {0.f};
@@ -355,9 +416,9 @@ block_norm_forward_any_kernel(const BlockNormArgs a) {
     }
     if (live && a.h)
 #pragma unroll
-        for (int i = 0; i < kGroups; ++i) row_store<false>(static_cast<R *>(a.h) + at, i, t, n, width, hv[i]);
+        for (int i = 0; i < kGroups; ++i) row_store(static_cast<R *>(a.h) + at, i, t, n, width, hv[i]);
     if (!(a.flags & GDN_BLOCK_PRE_NORM)) return;
-    row_sum(ss, red, t, n);
+    row_sum<1, 16>(ss, red, t, n);
     const float scale2 = 1.f / sqrtf(ss[0] / float(width) + a.eps);
     if (!live) return;
 #pragma unroll
@@ -366,7 +427,7 @@ block_norm_forward_any_kernel(const BlockNormArgs a) {
         weight_load<false>(a.pre_weight, none, zc, i, t, n, width, w2);
 #pragma unroll
         for (int e = 0; e < 8; ++e) w2[e] *= hv[i][e] * scale2;
-        row_store<false>(static_cast<T *>(a.y) + at, i, t, n, width, w2);
+        row_store(static_cast<T *>(a.y) + at, i, t, n, width, w2);
     }
 }
 
@@ -379,156 +440,163 @@ template <typename T, typename R, int kGroups>
 __global__ void __launch_bounds__(512, 1)
 block_norm_backward_kernel(const BlockNormArgs a, const Stages sg) {
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ float red_all[64 * 16];
+    __shared__ __align__(16) float red_all[32 * 8];
+    clear_red(red_all);
     constexpr bool kKeep = kGroups == 1;
     const int n = blockDim.x, t = threadIdx.x, width = a.width;
     const bool leader = threadIdx.x == 0 && threadIdx.y == 0;
-    float *red = red_all + 64 * threadIdx.y;
+    float *red = red_all + 32 * threadIdx.y;
     Pipe<kBwdStages> pipe;
-    pipe.init(smem, a.rows, blockDim.y);
+    pipe.init(smem, int(a.rows), blockDim.y);
     const bool post = a.flags & GDN_BLOCK_POST_NORM, pre = sg.src[3] != nullptr;
     const bool silu = a.flags & GDN_BLOCK_GATE_SILU, gated = sg.src[1] != nullptr, res = sg.src[2] != nullptr;
     const bool has_dh = sg.src[4] != nullptr;
     const float inv_width = 1.f / float(width);
-    const int64_t groups = (a.rows + blockDim.y - 1) / blockDim.y;
+    const int rows = int(a.rows), stride = int(gridDim.x * blockDim.y);
     if (leader)
-        for (int i = 0; i < kBwdStages; ++i) pipe.fetch(sg, i);
+        for (uint32_t i = 0; i < kBwdStages; ++i) pipe.fetch(sg, i);
     Weights w;
     if constexpr (kKeep) w.load(a, 0, t, n, width);
-    float sw1[kGroups][8], sw2[kGroups][8], ssc[kGroups][8];
+    f32x2 sw1[kGroups][4], sw2[kGroups][4], ssc[kGroups][4];
 #pragma unroll
     for (int i = 0; i < kGroups; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sw1[i][e] = sw2[i][e] = ssc[i][e] = 0.f;
-    for (int64_t it = 0; it * gridDim.x + blockIdx.x < groups; ++it) {
-        const int64_t row = (it * gridDim.x + blockIdx.x) * blockDim.y + threadIdx.y;
-        const bool live = row < a.rows && pipe.wait(it);
-        const unsigned char *st = smem + 64 + (it % kBwdStages) * sg.stage_bytes;
+        for (int e = 0; e < 4; ++e) sw1[i][e] = sw2[i][e] = ssc[i][e] = both(0.f);
+    for (int first = int(blockIdx.x * blockDim.y), left = 1; left > 0; first += stride) {
+        left = rows - first - stride;  // (rows < 2^31, and so is first: `left` > 0 while another group follows)
+        const int row = first + int(threadIdx.y);
+        const bool live = row < rows && pipe.wait();
+        const unsigned char *st = smem + 64 + pipe.stage * sg.stage_bytes;
         auto at = [&](int i) { return st + sg.off[i] + threadIdx.y * sg.row_bytes[i]; };
-        const int64_t base = row * width;
+        const int64_t base = int64_t(row) * width + 8 * t;
         const int lw = live ? width : 0;  // rows past the end read as zeros and add zeros
-        float nv[kGroups][8], scale1 = 1.f;
+        f32x2 nv[kGroups][4];
+        float scale1 = 1.f;
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) staged<T>(at(0), 8 * (i * n + t), lw, nv[i]);
         if (post) {
-            float ss[1] = {0.f};
+            f32x2 ss = both(0.f);
 #pragma unroll
             for (int i = 0; i < kGroups; ++i)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ss[0] = fmaf(nv[i][e], nv[i][e], ss[0]);
-            row_sum(ss, red, t, n);
-            scale1 = rsqrtf(fmaf(ss[0], inv_width, a.eps));
+                for (int e = 0; e < 4; ++e) ss = fma2(nv[i][e], nv[i][e], ss);
+            float s1[1] = {lo_of(ss) + hi_of(ss)};
+            row_sum<1, 16>(s1, red, t, n);
+            scale1 = rsqrtf(fmaf(s1[0], inv_width, a.eps));
         }
         // n1, the gate and its derivative, h, and the sums of h^2 and dy w2 h
-        float hv[kGroups][8], gv[kGroups][8], dv[kGroups][8], s2[2] = {0.f, 0.f};
+        f32x2 hv[kGroups][4], gv[kGroups][4], dv[kGroups][4], sh = both(0.f), sy = both(0.f);
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
             const int c = 8 * (i * n + t);
             if constexpr (!kKeep) w.load(a, i, t, n, width);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) nv[i][e] *= scale1;
+            for (int e = 0; e < 4; ++e) {
+                nv[i][e] = mul2(nv[i][e], both(scale1));
+                hv[i][e] = mul2(mul2(nv[i][e], w.w1[e]), w.s[e]);
+            }
             if (gated) {
                 staged<T>(at(1), c, lw, gv[i]);
+                gate<T, true>(silu, gv[i], dv[i]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float g = gate_sigmoid<T>(gv[i][e]), act = silu ? gv[i][e] * g : g;
-                    dv[i][e] = fmaf(act, 1.f - g, silu ? g : 0.f);  // act' = g + act (1 - g), or g (1 - g)
-                    gv[i][e] = act;
-                }
+                for (int e = 0; e < 4; ++e) hv[i][e] = mul2(hv[i][e], gv[i][e]);
             } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    gv[i][e] = 1.f;
-                    dv[i][e] = 0.f;
+                for (int e = 0; e < 4; ++e) {
+                    gv[i][e] = both(1.f);
+                    dv[i][e] = both(0.f);
                 }
             }
             if (res) {
-                staged<R>(at(2), c, lw, hv[i]);
+                f32x2 rv[4];
+                staged<R>(at(2), c, lw, rv);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) hv[i][e] *= a.residual_scale;
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) hv[i][e] = 0.f;
+                for (int e = 0; e < 4; ++e) hv[i][e] = fma2(both(a.residual_scale), rv[e], hv[i][e]);
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) hv[i][e] = fmaf(nv[i][e] * w.w1[e] * gv[i][e], w.s[e], hv[i][e]);
             if (pre) {
-                float yv[8];
+                f32x2 yv[4];
                 staged<T>(at(3), c, lw, yv);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    s2[0] = fmaf(hv[i][e], hv[i][e], s2[0]);
-                    s2[1] = fmaf(yv[e] * w.w2[e], hv[i][e], s2[1]);
+                for (int e = 0; e < 4; ++e) {
+                    sh = fma2(hv[i][e], hv[i][e], sh);
+                    sy = fma2(mul2(yv[e], w.w2[e]), hv[i][e], sy);
                 }
             }
         }
         float scale2 = 0.f, mean2 = 0.f;
         if (pre) {
-            row_sum(s2, red, t, n);
+            float s2[2] = {lo_of(sh) + hi_of(sh), lo_of(sy) + hi_of(sy)};
+            row_sum<2, 16>(s2, red, t, n);
             scale2 = rsqrtf(fmaf(s2[0], inv_width, a.eps));
             mean2 = scale2 * s2[1] * inv_width;  // mean(dn2 . n2)
         }
-        float s3[1] = {0.f};
+        f32x2 sd = both(0.f);
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
             const int c = 8 * (i * n + t);
+            const bool in = live && c < width;
             if constexpr (!kKeep) w.load(a, i, t, n, width);
-            float ev[8];  // h's whole gradient
+            f32x2 ev[4];  // h's whole gradient
             if (has_dh) {
                 staged<R>(at(4), c, lw, ev);
             } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ev[e] = 0.f;
+                for (int e = 0; e < 4; ++e) ev[e] = both(0.f);
             }
             if (pre) {
-                float yv[8];
+                f32x2 yv[4];
                 staged<T>(at(3), c, lw, yv);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float n2 = hv[i][e] * scale2;
-                    sw2[i][e] = fmaf(yv[e], n2, sw2[i][e]);
-                    ev[e] = fmaf(scale2, fmaf(-n2, mean2, yv[e] * w.w2[e]), ev[e]);
+                for (int e = 0; e < 4; ++e) {
+                    const f32x2 n2 = mul2(hv[i][e], both(scale2));
+                    sw2[i][e] = fma2(yv[e], n2, sw2[i][e]);
+                    ev[e] = fma2(both(scale2), fma2(n2, both(-mean2), mul2(yv[e], w.w2[e])), ev[e]);
                 }
             }
-            if (live && a.d_residual) {
-                float dr[8];
+            if (in && a.d_residual) {
+                f32x2 dr[4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) dr[e] = a.residual_scale * ev[e];
-                row_store<true>(static_cast<R *>(a.d_residual) + base, i, t, n, width, dr);
+                for (int e = 0; e < 4; ++e) dr[e] = mul2(both(a.residual_scale), ev[e]);
+                store_pairs(static_cast<R *>(a.d_residual) + base + 8 * i * n, dr);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float n1 = nv[i][e], u = n1 * w.w1[e], db = ev[e] * w.s[e], du = db * gv[i][e];
-                ssc[i][e] = fmaf(ev[e], u * gv[i][e], ssc[i][e]);  // (branch_scale at the end)
-                dv[i][e] *= db * u;                                 // dz
-                sw1[i][e] = fmaf(du, n1, sw1[i][e]);
-                hv[i][e] = du * w.w1[e];                            // dn1 (dx without the norm)
-                s3[0] = fmaf(hv[i][e], n1, s3[0]);
+            for (int e = 0; e < 4; ++e) {
+                const f32x2 n1 = nv[i][e], u = mul2(n1, w.w1[e]), db = mul2(ev[e], w.s[e]), du = mul2(db, gv[i][e]);
+                ssc[i][e] = fma2(ev[e], mul2(u, gv[i][e]), ssc[i][e]);  // (branch_scale at the end)
+                dv[i][e] = mul2(dv[i][e], mul2(db, u));                  // dz
+                sw1[i][e] = fma2(du, n1, sw1[i][e]);
+                hv[i][e] = mul2(du, w.w1[e]);                            // dn1 (dx without the norm)
+                sd = fma2(hv[i][e], n1, sd);
             }
-            if (live && a.d_gate) row_store<true>(static_cast<T *>(a.d_gate) + base, i, t, n, width, dv[i]);
+            if (in && a.d_gate) store_pairs(static_cast<T *>(a.d_gate) + base + 8 * i * n, dv[i]);
         }
         __syncthreads();  // the stage has been read
-        if (leader) pipe.fetch(sg, it + kBwdStages);
+        if (leader) pipe.fetch(sg, pipe.stage);
+        pipe.advance();
         if (post) {
-            row_sum(s3, red, t, n);
+            float s3[1] = {lo_of(sd) + hi_of(sd)};
+            row_sum<1, 16>(s3, red, t, n);
             const float mean1 = s3[0] * inv_width;
 #pragma unroll
             for (int i = 0; i < kGroups; ++i)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) hv[i][e] = scale1 * fmaf(-nv[i][e], mean1, hv[i][e]);
+                for (int e = 0; e < 4; ++e)
+                    hv[i][e] = mul2(both(scale1), fma2(nv[i][e], both(-mean1), hv[i][e]));
         }
         if (live && a.dx)
 #pragma unroll
-            for (int i = 0; i < kGroups; ++i) row_store<true>(static_cast<T *>(a.dx) + base, i, t, n, width, hv[i]);
+            for (int i = 0; i < kGroups; ++i)
+                if (8 * (i * n + t) < width) store_pairs(static_cast<T *>(a.dx) + base + 8 * i * n, hv[i]);
     }
-    float *out = a.partial + (int64_t(blockIdx.x) * blockDim.y + threadIdx.y) * 3 * width;
+    float *out = a.partial + (int64_t(blockIdx.x) * blockDim.y + threadIdx.y) * 3 * width + 8 * t;
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
+        if (8 * (i * n + t) >= width) continue;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ssc[i][e] *= a.branch_scale;
-        if (a.d_post_weight) row_store<true>(out, i, t, n, width, sw1[i]);
-        if (a.d_scale) row_store<true>(out + width, i, t, n, width, ssc[i]);
-        if (a.d_pre_weight) row_store<true>(out + 2 * width, i, t, n, width, sw2[i]);
+        for (int e = 0; e < 4; ++e) ssc[i][e] = mul2(ssc[i][e], both(a.branch_scale));
+        if (a.d_post_weight) store_pairs(out + 8 * i * n, sw1[i]);
+        if (a.d_scale) store_pairs(out + width + 8 * i * n, ssc[i]);
+        if (a.d_pre_weight) store_pairs(out + 2 * width + 8 * i * n, sw2[i]);
     }
 }
 
@@ -537,9 +605,10 @@ block_norm_backward_kernel(const BlockNormArgs a, const Stages sg) {
 template <typename T, typename R, int kGroups>
 __global__ void __launch_bounds__(512)
 block_norm_backward_any_kernel(const BlockNormArgs a) {
-    __shared__ float red_all[64 * 8];
+    __shared__ __align__(16) float red_all[32 * 8];
+    clear_red(red_all);
     const int n = blockDim.x, t = threadIdx.x, width = a.width;
-    float *red = red_all + 64 * threadIdx.y;
+    float *red = red_all + 32 * threadIdx.y;
     const int64_t lines = int64_t(gridDim.x) * blockDim.y, line = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
     const float zc = (a.flags & GDN_BLOCK_ZERO_CENTRED) ? 1.f : 0.f;
     const float none = zc != 0.f ? 0.f : 1.f;
@@ -583,7 +652,7 @@ block_norm_backward_any_kernel(const BlockNormArgs a) {
             for (int i = 0; i < kGroups; ++i)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) ss[0] = fmaf(xv[i][e], xv[i][e], ss[0]);
-            row_sum(ss, red, t, n);
+            row_sum<1, 16>(ss, red, t, n);
             scale1 = 1.f / sqrtf(ss[0] / float(width) + a.eps);
         }
         // h, and the sums of h^2 and dy w2 h
@@ -611,7 +680,7 @@ block_norm_backward_any_kernel(const BlockNormArgs a) {
         }
         float scale2 = 0.f, mean2 = 0.f;
         if (pre) {
-            row_sum(s2, red, t, n);
+            row_sum<2, 16>(s2, red, t, n);
             scale2 = 1.f / sqrtf(s2[0] / float(width) + a.eps);
             mean2 = scale2 * s2[1] / float(width);  // mean(dn2 . n2)
         }
@@ -648,11 +717,11 @@ block_norm_backward_any_kernel(const BlockNormArgs a) {
                 ev[i][e] = du * w1[e];  // dn1 (dx without the norm)
                 s3[0] = fmaf(ev[i][e], n1, s3[0]);
             }
-            if (live && a.d_residual) row_store<false>(static_cast<R *>(a.d_residual) + at, i, t, n, width, dr);
-            if (live && a.d_gate) row_store<false>(static_cast<T *>(a.d_gate) + at, i, t, n, width, dzv);
+            if (live && a.d_residual) row_store(static_cast<R *>(a.d_residual) + at, i, t, n, width, dr);
+            if (live && a.d_gate) row_store(static_cast<T *>(a.d_gate) + at, i, t, n, width, dzv);
         }
         if (post) {
-            row_sum(s3, red, t, n);
+            row_sum<1, 16>(s3, red, t, n);
             const float mean1 = s3[0] / float(width);
 #pragma unroll
             for (int i = 0; i < kGroups; ++i)
@@ -661,14 +730,14 @@ block_norm_backward_any_kernel(const BlockNormArgs a) {
         }
         if (live && a.dx)
 #pragma unroll
-            for (int i = 0; i < kGroups; ++i) row_store<false>(static_cast<T *>(a.dx) + at, i, t, n, width, ev[i]);
+            for (int i = 0; i < kGroups; ++i) row_store(static_cast<T *>(a.dx) + at, i, t, n, width, ev[i]);
     }
     float *out = a.partial + line * 3 * width;
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
-        if (a.d_post_weight) row_store<false>(out, i, t, n, width, sw1[i]);
-        if (a.d_scale) row_store<false>(out + width, i, t, n, width, ssc[i]);
-        if (a.d_pre_weight) row_store<false>(out + 2 * width, i, t, n, width, sw2[i]);
+        if (a.d_post_weight) row_store(out, i, t, n, width, sw1[i]);
+        if (a.d_scale) row_store(out + width, i, t, n, width, ssc[i]);
+        if (a.d_pre_weight) row_store(out + 2 * width, i, t, n, width, sw2[i]);
     }
 }
 
