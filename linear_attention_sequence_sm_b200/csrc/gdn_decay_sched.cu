@@ -19,20 +19,45 @@ __host__ __device__ inline int64_t balanced_tokens(int64_t tokens, int hv) {
     return (tokens * hv + kDecayPlanSms - 1) / kDecayPlanSms;
 }
 
-// Exclusive prefix sums over the block of one value per thread; *total gets the sum.
-__device__ int block_scan(int v, int *part, int *total) {
-    part[threadIdx.x] = v;
-    __syncthreads();
-    for (int d = 1; d < kSchedThreads; d <<= 1) {
-        const int add = threadIdx.x >= unsigned(d) ? part[threadIdx.x - d] : 0;
-        __syncthreads();
-        part[threadIdx.x] += add;
-        __syncthreads();
+// Whether any sequence may be cut: the longest has at most seq_len tokens (all
+// of them, with cu_seqlens).
+inline bool may_split(const gdn_shape_t &s) {
+    return s.seq_len > kDecayMinSeg &&
+           s.seq_len >= 2 * balanced_tokens(int64_t(s.batch) * s.seq_len, s.num_v_heads);
+}
+
+// Exclusive prefix sums over the block of kN values per thread; totals gets the sums.
+template <int kN>
+__device__ void block_scan(int (&v)[kN], int (&totals)[kN], int *part) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int mine[kN];
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+        mine[j] = v[j];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, mine[j], d);
+            if (lane >= d) mine[j] += u;
+        }
+        if (lane == 31) part[32 * j + warp] = mine[j];
     }
-    const int mine = part[threadIdx.x] - v;
-    *total = part[kSchedThreads - 1];
     __syncthreads();
-    return mine;
+    if (warp < kN) {
+        int x = part[32 * warp + lane];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += u;
+        }
+        part[32 * warp + lane] = x;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+        totals[j] = part[32 * j + 31];
+        v[j] = mine[j] - v[j] + (warp ? part[32 * j + warp - 1] : 0);
+    }
+    __syncthreads();
 }
 
 // Checks cu_seqlens and writes the segment table, longest sequences first.
@@ -47,7 +72,7 @@ __global__ void __launch_bounds__(kSchedThreads)
 decay_schedule_kernel(int32_t num_seqs, int32_t tokens, int32_t batched_len, int32_t hv,
                       const int32_t *__restrict__ cu, DecaySched sc, int32_t *order) {
     __shared__ int bad, longest;
-    __shared__ int part[kSchedThreads];
+    __shared__ int part[96];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     DecayHeader *hdr = sc.hdr;
     if (threadIdx.x == 0) {
@@ -112,13 +137,13 @@ decay_schedule_kernel(int32_t num_seqs, int32_t tokens, int32_t batched_len, int
     // chunks and checkpoint slots before each sequence: each thread takes a run of sequences
     const int per = (num_seqs + kSchedThreads - 1) / kSchedThreads;
     const int n0 = min(num_seqs, int(threadIdx.x) * per), n1 = min(num_seqs, n0 + per);
-    int chunks = 0, cks = 0, total_chunks, total_cks;
+    int two[2] = {0, 0}, total2[2];
     for (int n = n0; n < n1; ++n) {
-        chunks += (len_of(n) + kDecayChunk - 1) / kDecayChunk;
-        cks += (len_of(n) + ick - 1) / ick;
+        two[0] += (len_of(n) + kDecayChunk - 1) / kDecayChunk;
+        two[1] += (len_of(n) + ick - 1) / ick;
     }
-    chunks = block_scan(chunks, part, &total_chunks);
-    cks = block_scan(cks, part, &total_cks);
+    block_scan(two, total2, part);
+    int chunks = two[0], cks = two[1];
     for (int n = n0; n < n1; ++n) {
         sc.chunk_base[n] = chunks;
         sc.ck_base[n] = cks;
@@ -128,16 +153,15 @@ decay_schedule_kernel(int32_t num_seqs, int32_t tokens, int32_t batched_len, int
     __syncthreads();  // order, ck_base
     // segments, sequences by rank
     auto segs_of = [&](int n) { return len_of(n) <= seg_len ? 1 : (len_of(n) + seg_len - 1) / seg_len; };
-    int segs = 0, cut = 0, slots = 0, total_segs, total_cut, total_slots;
+    int three[3] = {0, 0, 0}, total3[3];
     for (int r = n0; r < n1; ++r) {
         const int c = segs_of(order[r]);
-        segs += c;
-        cut += c > 1;
-        slots += c > 1 ? c : 0;
+        three[0] += c;
+        three[1] += c > 1;
+        three[2] += c > 1 ? c : 0;
     }
-    segs = block_scan(segs, part, &total_segs);
-    cut = block_scan(cut, part, &total_cut);
-    slots = block_scan(slots, part, &total_slots);
+    block_scan(three, total3, part);
+    int segs = three[0], cut = three[1], slots = three[2];
     for (int r = n0; r < n1; ++r) {
         const int n = order[r], c = segs_of(n), len = len_of(n);
         if (c > 1) sc.split[cut++] = segs;
@@ -155,14 +179,14 @@ decay_schedule_kernel(int32_t num_seqs, int32_t tokens, int32_t batched_len, int
         }
     }
     if (threadIdx.x == 0) {
-        sc.chunk_base[num_seqs] = total_chunks;
-        sc.ck_base[num_seqs] = total_cks;
-        hdr->num_segs = total_segs;
-        hdr->num_split = total_cut;
+        sc.chunk_base[num_seqs] = total2[0];
+        sc.ck_base[num_seqs] = total2[1];
+        hdr->num_segs = total3[0];
+        hdr->num_split = total3[1];
         hdr->ick = ick;
         hdr->seg_len = seg_len;
-        hdr->num_cks = total_cks;
-        hdr->total_chunks = total_chunks;
+        hdr->num_cks = total2[1];
+        hdr->total_chunks = total2[0];
     }
 }
 
@@ -314,12 +338,12 @@ DecayLayout decay_layout(const gdn_shape_t &s, bool backward) {
     const int64_t balanced = balanced_tokens(tokens, s.num_v_heads);
     const int64_t shortest = std::max<int64_t>(kDecayMinSeg, balanced);
     DecayLayout L = {};
-    L.max_slots = tokens > kDecayMinSeg ? 2 * tokens / shortest + 1 : 0;
-    L.max_split = tokens > kDecayMinSeg ? tokens / shortest + 1 : 0;
+    L.max_slots = may_split(s) ? 2 * tokens / shortest + 1 : 0;
+    L.max_split = may_split(s) ? tokens / shortest + 1 : 0;
     L.max_segs = N + L.max_slots;
     L.max_chunks = (tokens + 63 * N) / kDecayChunk;
     // checkpoints are `ick` apart, 1024 unless segments are shorter
-    L.max_cks = tokens / (balanced >= kDecayMaxIck ? kDecayMaxIck : kDecayMinSeg) + N;
+    L.max_cks = tokens / (balanced >= kDecayMaxIck || !may_split(s) ? kDecayMaxIck : kDecayMinSeg) + N;
     size_t off = 256;
     auto take = [&](size_t bytes) {
         const size_t at = off;

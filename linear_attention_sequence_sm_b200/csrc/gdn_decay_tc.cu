@@ -918,13 +918,13 @@ cudaError_t launch_as(const Maps &tm, const DecayPass &p, int64_t max_units, cud
     cudaError_t e = cudaFuncSetAttribute(decay_pass_tc_kernel<kKind>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          int(Cfg<kKind>::kSmem));
     if (e != cudaSuccess) return e;
-    cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, decay_pass_tc_kernel<kKind>)) != cudaSuccess) return e;
-    if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidKernelImage;  // the roles' registers are dealt out of these
-    int dev = 0, sms = kDecayPlanSms;
-    if ((e = cudaGetDevice(&dev)) != cudaSuccess ||
-        (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
-        return e;
+    static const int regs = [] {
+        cudaFuncAttributes fa;
+        return cudaFuncGetAttributes(&fa, decay_pass_tc_kernel<kKind>) == cudaSuccess ? fa.numRegs : -1;
+    }();
+    if (regs != kRegsLaunch) return cudaErrorInvalidKernelImage;  // the roles' registers are dealt out of these
+    const int sms = device_sm_count(nullptr);
+    if (sms <= 0) return cudaErrorInvalidDevice;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(std::min<int64_t>(max_units, sms)));
     cfg.blockDim = dim3(kThreads);

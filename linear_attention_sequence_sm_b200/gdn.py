@@ -678,6 +678,35 @@ def short_conv(x, weight, cu_seqlens=None, state=None, silu=True, out=None, stat
     return out, state_out
 
 
+class _Here:
+    """A device context that changes nothing (the tensors' device is current)."""
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE_NOW = _Here()
+
+
+def _on(dev):
+    """torch.cuda.device(dev), without its cost where ``dev`` is current already."""
+    return _HERE_NOW if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _raw_stream(stream, dev):
+    """_stream_handle as the integer ctypes takes."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev.index)
+    return _stream_handle(stream, dev).value
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _decay_layout(g, per_token):
     """GDN_DECAY_PER_HEAD for g [Hv], GDN_DECAY_PER_TOKEN for g shaped
     ``per_token``; any other shape is an error."""
@@ -691,9 +720,17 @@ def _decay_layout(g, per_token):
 def _decay_prefill_shapes(q, k, v, g, initial_state, cu_seqlens):
     """Shape checks of the decayed linear attention's prefill and backward:
     _prefill_shapes, with g [..., Hv] or [Hv] and no beta."""
-    full = torch.empty(v.shape[:-1], device="meta")  # stands in for beta, which there is none of
-    n_seqs, hv, dv, dk = _prefill_shapes(q, k, v, full, full, initial_state, cu_seqlens)
+    per_token = g if g.dim() == v.dim() - 1 else None
+    n_seqs, hv, dv, dk = _prefill_shapes(q, k, v, per_token, None, initial_state, cu_seqlens)
     return n_seqs, hv, dv, dk, _decay_layout(g, tuple(v.shape[:-1]))
+
+
+def decay_workspace_size(shape: Shape, backward=False) -> int:
+    """Bytes of workspace gdn_decay_forward (or gdn_decay_backward) needs."""
+    n = ctypes.c_size_t(0)
+    fn = LIB.gdn_decay_backward_workspace_size if backward else LIB.gdn_decay_forward_workspace_size
+    _check(fn(ctypes.byref(shape), ctypes.byref(n)))
+    return n.value
 
 
 def decay_forward(q, k, v, g, initial_state=None, cu_seqlens=None, output_final_state=True, out=None,
@@ -709,61 +746,49 @@ def decay_forward(q, k, v, g, initial_state=None, cu_seqlens=None, output_final_
     _expect(out, "out", v.shape)
     _expect(final_state, "final_state", (n_seqs, hv, dv, dk))
     dev, dt = q.device, q.dtype
-    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+    for t, n in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
         _need(t, n, dt, dev)
-    _need(g, "g", torch.float32, dev)
-    _need(initial_state, "initial_state", torch.float32, dev)
+    for t, n in ((g, "g"), (initial_state, "initial_state"), (final_state, "final_state")):
+        _need(t, n, torch.float32, dev)
     _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
     shape = make_shape(q, v, cu_seqlens, 64, force_simt)
     if out is None:
         out = torch.empty(v.shape, dtype=dt, device=dev)
-    _need(out, "out", dt, dev)
     if final_state is None and output_final_state:
         final_state = torch.empty((n_seqs, hv, dv, dk), dtype=torch.float32, device=dev)
-    _need(final_state, "final_state", torch.float32, dev)
     nbytes = decay_workspace_size(shape)
     if workspace is None or workspace.numel() < nbytes:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     osc = output_norm.c_struct(out) if output_norm is not None else None
-    with torch.cuda.device(dev):  # the library launches on the current device
-        _check(LIB.gdn_decay_forward(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), layout,
-                                     _ptr(initial_state), _ptr(cu_seqlens), None if osc is None else ctypes.byref(osc),
-                                     _ptr(out), _ptr(final_state), _ptr(workspace), workspace.numel(),
-                                     _stream_handle(stream, dev)))
+    with _on(dev):  # the library launches on the current device
+        _check(LIB.gdn_decay_forward(ctypes.byref(shape), _addr(q), _addr(k), _addr(v), _addr(g), layout,
+                                     _addr(initial_state), _addr(cu_seqlens),
+                                     None if osc is None else ctypes.byref(osc), _addr(out), _addr(final_state),
+                                     _addr(workspace), workspace.numel(), _raw_stream(stream, dev)))
     return out, final_state
-
-
-def decay_workspace_size(shape: Shape, backward=False) -> int:
-    """Bytes of workspace gdn_decay_forward (or gdn_decay_backward) needs."""
-    n = ctypes.c_size_t(0)
-    fn = LIB.gdn_decay_backward_workspace_size if backward else LIB.gdn_decay_forward_workspace_size
-    _check(fn(ctypes.byref(shape), ctypes.byref(n)))
-    return n.value
 
 
 def decay_decode_step(q, k, v, g, state, out=None, stream=None, output_norm: OutputNorm | None = None):
     """One token per sequence of the decayed linear attention: q, k
     [N, Hk, d_k], v [N, Hv, d_v], g [N, Hv] or [Hv] fp32; ``state``
     [N, Hv, d_v, d_k] fp32 is updated in place.  Returns o [N, Hv, d_v]."""
-    full = torch.empty(v.shape[:-1], device="meta")
-    _decode_shapes(q, k, v, full, full, state)
+    _decode_shapes(q, k, v, None, None, state)
     layout = _decay_layout(g, tuple(v.shape[:-1]))
     _expect(out, "out", v.shape)
     dev, dt = q.device, q.dtype
-    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+    for t, n in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
         _need(t, n, dt, dev)
     _need(g, "g", torch.float32, dev)
     _need(state, "state", torch.float32, dev)
     if out is None:
         out = torch.empty(v.shape, dtype=dt, device=dev)
-    _need(out, "out", dt, dev)
     N, hk, dk = q.shape
     hv, dv = v.shape[1], v.shape[2]
     osc = output_norm.c_struct(out) if output_norm is not None else None
-    with torch.cuda.device(dev):  # the library launches on the current device
-        _check(LIB.gdn_decay_decode_step(N, hk, hv, dk, dv, _dtype_code(q), _ptr(q), _ptr(k), _ptr(v), _ptr(g), layout,
-                                         _ptr(state), None if osc is None else ctypes.byref(osc), _ptr(out),
-                                         _stream_handle(stream, dev)))
+    with _on(dev):  # the library launches on the current device
+        _check(LIB.gdn_decay_decode_step(N, hk, hv, dk, dv, _dtype_code(q), _addr(q), _addr(k), _addr(v), _addr(g),
+                                         layout, _addr(state), None if osc is None else ctypes.byref(osc), _addr(out),
+                                         _raw_stream(stream, dev)))
     return out
 
 
@@ -779,24 +804,24 @@ def decay_backward(q, k, v, g, d_o, d_final_state=None, initial_state=None, cu_s
     dev, dt = q.device, q.dtype
     for t, n in ((q, "q"), (k, "k"), (v, "v"), (d_o, "d_o")):
         _need(t, n, dt, dev)
-    _need(g, "g", torch.float32, dev)
-    _need(initial_state, "initial_state", torch.float32, dev)
-    _need(d_final_state, "d_final_state", torch.float32, dev)
+    for t, n in ((g, "g"), (initial_state, "initial_state"), (d_final_state, "d_final_state")):
+        _need(t, n, torch.float32, dev)
     _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
     shape = make_shape(q, v, cu_seqlens, 64, force_simt)
     nbytes = decay_workspace_size(shape, backward=True)
     if workspace is None or workspace.numel() < nbytes:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    f32 = dict(dtype=torch.float32, device=dev)
     out = {"dq": torch.empty(q.shape, dtype=dt, device=dev), "dk": torch.empty(k.shape, dtype=dt, device=dev),
-           "dv": torch.empty(v.shape, dtype=dt, device=dev), "dg": torch.empty(g.shape, **f32) if want_dg else None,
-           "d_initial_state": torch.empty((n_seqs, hv, dv, dk), **f32) if want_d_initial_state else None}
-    with torch.cuda.device(dev):  # the library launches on the current device
-        _check(LIB.gdn_decay_backward(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), layout,
-                                      _ptr(initial_state), _ptr(cu_seqlens), _ptr(d_o), _ptr(d_final_state),
-                                      _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dg"]),
-                                      _ptr(out["d_initial_state"]), _ptr(workspace), workspace.numel(),
-                                      _stream_handle(stream, dev)))
+           "dv": torch.empty(v.shape, dtype=dt, device=dev),
+           "dg": torch.empty(g.shape, dtype=torch.float32, device=dev) if want_dg else None,
+           "d_initial_state": torch.empty((n_seqs, hv, dv, dk), dtype=torch.float32, device=dev)
+           if want_d_initial_state else None}
+    with _on(dev):  # the library launches on the current device
+        _check(LIB.gdn_decay_backward(ctypes.byref(shape), _addr(q), _addr(k), _addr(v), _addr(g), layout,
+                                      _addr(initial_state), _addr(cu_seqlens), _addr(d_o), _addr(d_final_state),
+                                      _addr(out["dq"]), _addr(out["dk"]), _addr(out["dv"]), _addr(out["dg"]),
+                                      _addr(out["d_initial_state"]), _addr(workspace), workspace.numel(),
+                                      _raw_stream(stream, dev)))
     return out
 
 
@@ -828,16 +853,15 @@ class BlockNorm:
         self.activation, self.zero_centred = activation, bool(zero_centred)
 
     def c_struct(self, x: torch.Tensor, gate) -> BlockNormC:
+        dev = x.device
         for w, n in ((self.post_weight, "post_weight"), (self.scale, "scale"), (self.pre_weight, "pre_weight")):
-            _expect(w, n, x.shape[-1:])
-            _need(w, n, torch.float32, x.device)
+            _need(w, n, torch.float32, dev)  # (their shapes: _block_norm_inputs)
         flags = ((GDN_BLOCK_POST_NORM if self.post_norm else 0) | (GDN_BLOCK_PRE_NORM if self.pre_norm else 0) |
                  (GDN_BLOCK_ZERO_CENTRED if self.zero_centred else 0))
         if gate is not None:
             flags |= GDN_BLOCK_GATE_SILU if self.activation == "silu" else GDN_BLOCK_GATE_SIGMOID
-        p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-        return BlockNormC(p(self.post_weight), p(self.scale), p(self.pre_weight), self.eps, self.residual_scale,
-                          self.branch_scale, flags)
+        return BlockNormC(_addr(self.post_weight), _addr(self.scale), _addr(self.pre_weight), self.eps,
+                          self.residual_scale, self.branch_scale, flags)
 
 
 def _block_norm_inputs(x, residual, norm, gate, more):
@@ -846,17 +870,20 @@ def _block_norm_inputs(x, residual, norm, gate, more):
     if x.dim() < 1:
         raise ValueError("x must be [..., width]")
     rt = x.dtype if residual is None else residual.dtype
-    for t, n, _ in ((residual, "residual", None), (gate, "gate", None), *more):
+    _expect(residual, "residual", x.shape)
+    _expect(gate, "gate", x.shape)
+    for t, n, _ in more:
         _expect(t, n, x.shape)
     for w, n in ((norm.post_weight, "post_weight"), (norm.scale, "scale"), (norm.pre_weight, "pre_weight")):
         _expect(w, n, x.shape[-1:])
     if rt not in (x.dtype, torch.float32):
         raise TypeError(f"residual must be {x.dtype} or torch.float32, got {rt}")
-    _need(x, "x", x.dtype, x.device)
-    _need(residual, "residual", rt, x.device)
-    _need(gate, "gate", x.dtype, x.device)
+    dev = x.device
+    _need(x, "x", x.dtype, dev)
+    _need(residual, "residual", rt, dev)
+    _need(gate, "gate", x.dtype, dev)
     for t, n, wide in more:
-        _need(t, n, rt if wide else x.dtype, x.device)
+        _need(t, n, rt if wide else x.dtype, dev)
     width = x.shape[-1]
     return (x.numel() // width if width else 0), width, rt
 
@@ -875,10 +902,10 @@ def block_norm_forward(x, residual, norm: BlockNorm, gate=None, h=None, y=None, 
     if y is None and norm.pre_norm:
         y = torch.empty_like(x)
     c = norm.c_struct(x, gate)
-    with torch.cuda.device(x.device):  # the library launches on the current device
-        _check(LIB.gdn_block_norm_forward(rows, width, _dtype_code(x), _dtype_code(h), _ptr(x), _ptr(residual),
-                                          _ptr(gate), ctypes.byref(c), _ptr(h), _ptr(y),
-                                          _stream_handle(stream, x.device)))
+    dev = x.device
+    with _on(dev):  # the library launches on the current device
+        _check(LIB.gdn_block_norm_forward(rows, width, _dtype_code(x), _dtype_code(h), _addr(x), _addr(residual),
+                                          _addr(gate), ctypes.byref(c), _addr(h), _addr(y), _raw_stream(stream, dev)))
     return h, y
 
 
@@ -907,12 +934,14 @@ def block_norm_backward(x, residual, norm: BlockNorm, gate=None, d_h=None, d_y=N
            "d_post_weight": like(norm.post_weight), "d_scale": like(norm.scale), "d_pre_weight": like(norm.pre_weight)}
     c = norm.c_struct(x, gate)
     code = GDN_DTYPE_F32 if rt == torch.float32 else GDN_DTYPE_BF16
-    with torch.cuda.device(x.device):  # the library launches on the current device
-        _check(LIB.gdn_block_norm_backward(rows, width, _dtype_code(x), code, _ptr(x), _ptr(residual), _ptr(gate),
-                                           ctypes.byref(c), _ptr(d_h), _ptr(d_y), _ptr(out["dx"]),
-                                           _ptr(out["d_residual"]), _ptr(out["d_gate"]), _ptr(out["d_post_weight"]),
-                                           _ptr(out["d_scale"]), _ptr(out["d_pre_weight"]), _ptr(workspace),
-                                           workspace.numel(), _stream_handle(stream, x.device)))
+    dev = x.device
+    with _on(dev):  # the library launches on the current device
+        _check(LIB.gdn_block_norm_backward(rows, width, _dtype_code(x), code, _addr(x), _addr(residual), _addr(gate),
+                                           ctypes.byref(c), _addr(d_h), _addr(d_y), _addr(out["dx"]),
+                                           _addr(out["d_residual"]), _addr(out["d_gate"]),
+                                           _addr(out["d_post_weight"]), _addr(out["d_scale"]),
+                                           _addr(out["d_pre_weight"]), _addr(workspace), workspace.numel(),
+                                           _raw_stream(stream, dev)))
     return out
 
 
