@@ -31,23 +31,26 @@
 // until the products set the pace):
 //   0-7     state      two warps per tensor-memory quarter, 64 columns each
 //   8-15    out        X1, X2 -> out (and the dot with aux), 32 tokens a warpgroup
-//   16-23   split      w z in three terms, 32 tokens a warpgroup
+//   16-23   split      w z in three terms, 16 tokens at a time, the warpgroups in turn
 //   24-27   mask       P from QK
 //   28 TMA loads, 29 issues X1, X2 and QK, 30 decays, 31 issues KV
 // The registers go where the state is (setmaxnreg).  A chunk's products are 32
 // instructions with a dozen waits and commits between them; issued by one
 // thread these took 3300 cycles a chunk, more than the products themselves.
 //
-// Two chains run side by side, each bound by its own hand-overs: KV(n) -> L
-// read by the state warps -> KV(n + 1), and QK(n + 1) -> P(n + 1) -> X2(n + 1).
-// With three copies of Sigma tensor memory is full: X2 shares QK's columns,
-// and w z has room for half a chunk.
+// Chains run side by side, each bound by its own hand-overs: KV(n) -> L read by
+// the state warps -> KV(n + 1); QK(n) -> P(n) -> X2(n); X1(n), X2(n) -> out.
+// What tensor memory has room for is buffered: X2 twice in plain passes (QK
+// takes the columns of its chunk's X2 and runs a chunk ahead), L twice in
+// passes for the state alone, w z in quarters of a chunk, four or (with three
+// copies of Sigma) two.
 // All hand-overs are mbarriers with bounded waits; a timeout records
 // GDN_ERR_DEVICE_CHECK (bad_index -2).  A CTA takes units (segment, head) with
 // a stride of the grid; nothing synchronises it between units.
 #include <algorithm>
 
 #include "gdn_decay.cuh"
+#include "gdn_f32x2.cuh"
 #include "gdn_sm100.cuh"
 
 namespace gdn {
@@ -76,7 +79,8 @@ constexpr uint32_t kStage = 2304;  // an out warp's staging: 32 rows of 64 bytes
 
 template <int kKind> struct Cfg {
     static constexpr int kCopies = kKind == kDot ? 3 : 1;        // bf16 terms of Sigma's copy
-    static constexpr int kWz = kKind == kDot ? 1 : 2;            // half chunks of w z
+    static constexpr int kBufs = kKind == kDot ? 1 : 2;          // of X2 and QK
+    static constexpr int kQuarters = kKind == kDot ? 2 : 4;      // of w z
     // shared memory, from a 1024-byte-aligned base
     static constexpr uint32_t kOffX = 0;
     static constexpr uint32_t kOffZ = kOffX + kRing * kTile;
@@ -87,13 +91,24 @@ template <int kKind> struct Cfg {
     static constexpr uint32_t kOffVec = kOffOut + 8 * kStage;                           // [4]
     static constexpr uint32_t kOffRed = kOffVec + 4 * kVecFloats * 4;              // [4 warps][64]
     static constexpr uint32_t kOffBar = kOffRed + 1024;
-    static constexpr uint32_t kSmem = kOffBar + 384 + 1024;
+    static constexpr uint32_t kSmem = kOffBar + 432 + 1024;
     static_assert(kSmem <= 232448, "shared memory over the sm_100 per-block limit");
     // tensor memory columns
-    // L; the copies of Sigma (64 columns a term); X1; X2; QK; w z (48 a half chunk, 16 a term)
-    static constexpr uint32_t kColL = 0, kColC = 128, kColX1 = kColC + 64 * kCopies, kColX2 = kColX1 + 64;
-    static constexpr uint32_t kColQK = kKind == kDot ? kColX2 : kColX2 + 64, kColW = kColQK + 64;
-    static_assert(kColW + 48 * kWz <= kTmemCols, "tensor memory");
+    // L (two for the state alone); quarters of w z (8 columns a term); the copies of Sigma (64 columns a term);
+    // X1; X2 or QK (64 each)
+    static constexpr uint32_t kColL = 0, kColW = kKind == kStateOnly ? 256 : 128, kColC = kColW + 24 * kQuarters;
+    static constexpr uint32_t kColX1 = kColC + 64 * kCopies, kColX2 = kColX1 + 64;
+    static_assert(kKind == kStateOnly || kColX2 + 64 * kBufs <= kTmemCols, "tensor memory");
+    // columns and barrier phases of chunk m
+    static __device__ __forceinline__ uint32_t buf(uint32_t m) { return kBufs == 2 ? (m & 1u) : 0u; }
+    static __device__ __forceinline__ uint32_t phase(uint32_t m) { return (kBufs == 2 ? m >> 1 : m) & 1u; }
+    static __device__ __forceinline__ uint32_t col_x2(uint32_t m) { return kColX2 + 64u * buf(m); }
+    // quarter q of chunk m: its buffer, and which use of it this is
+    static __device__ __forceinline__ uint32_t qbuf(uint32_t q) { return kQuarters == 4 ? q : q & 1u; }
+    static __device__ __forceinline__ uint32_t qturn(uint32_t m, uint32_t q) { return kQuarters == 4 ? m : 2 * m + (q >> 1); }
+    static __device__ __forceinline__ uint32_t lbuf(uint32_t m) { return kKind == kStateOnly ? (m & 1u) : 0u; }
+    static __device__ __forceinline__ uint32_t lphase(uint32_t m) { return (kKind == kStateOnly ? m >> 1 : m) & 1u; }
+    static __device__ __forceinline__ uint32_t col_l(uint32_t m) { return kColL + 128u * lbuf(m); }
 };
 
 // mbarriers
@@ -106,21 +121,21 @@ enum {
     kBZFree = 14,   // [3] X2 done, w z taken (8 split warps)
     kBYFree = 17,   // [3] KV done, QK done
     kBAFree = 20,   // [2] dot taken (8 out warps)
-    kBW = 22,       // [2] first, second half of w z written (4 split warps each)
-    kBKV0 = 24,     // KV of the first half done
-    kBKV1 = 25,     // KV done (and an arrival of the issuing thread, which orders the token vectors)
-    kBLFree = 26,   // L read (8 state warps)
-    kBSt = 27,      // copies of Sigma written (8 state warps)
-    kBX1 = 28,      // X1 done
-    kBQK = 29,      // QK done
-    kBP = 30,       // [2] P written (4 mask warps)
-    kBPFree = 32,   // [2] X2 done
-    kBOut = 34,     // X1, X2 done (and an arrival of the issuing thread)
-    kBOutFree = 35, // X1, X2 read (8 out warps)
-    kBVec = 36,     // [4] token vectors written
-    kBVecFree = 40, // [4] token vectors read (8 state warps, 8 out warps)
-    kBDrain = 44,
-    kNumBars = 45
+    kBW = 22,       // [4] a quarter of w z written (4 split warps)
+    kBKq = 26,      // [4] its KV done
+    kBKV = 30,      // [2] KV done (and an arrival of the issuing thread, which orders the token vectors)
+    kBLFree = 32,   // [2] L read (8 state warps)
+    kBSt = 34,      // copies of Sigma written (8 state warps)
+    kBX1 = 35,      // X1 done
+    kBQK = 36,      // [2] QK done
+    kBP = 38,       // [2] P written (4 mask warps)
+    kBPFree = 40,   // [2] X2 done
+    kBOut = 42,     // X1, X2 done (and an arrival of the issuing thread)
+    kBOutFree = 43, // X1, X2 read (8 out warps)
+    kBVec = 44,     // [4] token vectors written
+    kBVecFree = 48, // [4] token vectors read (8 state warps, 8 out warps)
+    kBDrain = 52,
+    kNumBars = 53
 };
 
 struct Maps {
@@ -205,10 +220,14 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&v)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
-// 4 columns of 16 lanes: column lane % 4 of lane / 4 and of lane / 4 + 8.
-__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)[2]) {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x1.b32 [%0], {%1, %2};" ::"r"(taddr), "r"(r[0]), "r"(r[1]) : "memory");
+// 8 columns of 16 lanes: column lane % 4 of lane / 4 (a) and of lane / 4 + 8
+// (b), and four columns further (c, d).
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
 }
+// x minus the two bf16 values of w (exact where w is x rounded).
+__device__ __forceinline__ f32x2 sub_bf16x2(f32x2 x, uint32_t w) { return fma2(from_bf16x2(w), both(-1.f), x); }
 // Four 8 x 8 tiles of 16-bit values, transposed on the way: lane l gives the
 // address of row l % 8 of tile l / 8, and holds elements (row 2 (l % 4) and
 // the next, column l / 4) of each tile.
@@ -246,10 +265,11 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
     if (tid == 0) {
         for (int i = 0; i < kNumBars; ++i) {
             int n = 1;
-            if (i == kBW || i == kBW + 1 || i == kBP || i == kBP + 1) n = 4;
-            if (i == kBSt || i == kBLFree || i == kBOutFree || i == kBAFree || i == kBAFree + 1) n = 8;
-            if (i == kBOut || i == kBKV1) n = 2;
-            if (i >= kBZFree && i < kBZFree + kRing) n = kSt ? 8 : 9;
+            if ((i >= kBW && i < kBW + 4) || i == kBP || i == kBP + 1) n = 4;
+            if (i == kBSt || i == kBLFree || i == kBLFree + 1 || i == kBOutFree || i == kBAFree || i == kBAFree + 1)
+                n = 8;
+            if (i == kBOut || i == kBKV || i == kBKV + 1) n = 2;
+            if (i >= kBZFree && i < kBZFree + kRing) n = kSt ? 8 : 9;  // (each split warp once a chunk)
             if (i >= kBYFree && i < kBYFree + kRing) n = kSt ? 1 : 2;
             if (i == kBDrain) n = 2;
             if (i >= kBVecFree && i < kBVecFree + 4) n = kSt ? 8 : 16;
@@ -351,7 +371,7 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(kBSt));
                 }
-                ok = warp_wait(bar(kBKV1), mm & 1u);
+                ok = warp_wait(bar(kBKV + int(K::lbuf(mm))), K::lphase(mm));
                 if (!ok) break;
                 tc_fence_after();
                 const float gamma = vecs(mm)[kVecGamma];
@@ -359,17 +379,21 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         float v[16];
-                        tmem_ld16(trow + K::kColL + uint32_t(c0 + 16 * q), v);
+                        tmem_ld16(trow + K::col_l(mm) + uint32_t(c0 + 16 * q), v);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) S[16 * q + j] = fmaf(gamma, S[16 * q + j], v[j]);
+                        for (int j = 0; j < 16; j += 2) {
+                            const f32x2 r = fma2(both(gamma), pair(S[16 * q + j], S[16 * q + j + 1]), pair(v[j], v[j + 1]));
+                            S[16 * q + j] = lo_of(r);
+                            S[16 * q + j + 1] = hi_of(r);
+                        }
                     }
                 }
                 dec *= gamma;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(bar(kBLFree));
+                    mbar_arrive(bar(kBLFree + int(K::lbuf(mm))));
                     mbar_arrive(bar(kBVecFree + int(mm & 3u)));
                 }
                 if (kDots && a.zsum && p % a.sched.hdr->ick == 0) {
@@ -455,7 +479,7 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
 #pragma unroll
                         for (int l = 0; l < 2; ++l) {
                             tmem_ld_frag(tq + (uint32_t(16 * l) << 16) + K::kColX1 + 16 * p, x1[l]);
-                            tmem_ld_frag(tq + (uint32_t(16 * l) << 16) + K::kColX2 + 16 * p, x2[l]);
+                            tmem_ld_frag(tq + (uint32_t(16 * l) << 16) + K::col_x2(mm) + 16 * p, x2[l]);
                         }
                         tmem_wait_ld();
                         if (pp == 1) {
@@ -465,13 +489,24 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                         }
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            const float2 wi = *reinterpret_cast<const float2 *>(win + 16 * p + 8 * j + tp);
+                            const f32x2 wi = *reinterpret_cast<const f32x2 *>(win + 16 * p + 8 * j + tp);
 #pragma unroll
                             for (int l = 0; l < 2; ++l)
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    x1[l][4 * j + e] *= (e & 1) ? wi.y : wi.x;
-                                    x2[l][4 * j + e] += x1[l][4 * j + e];
+                                for (int e = 0; e < 4; e += 2) {
+                                    float *u = &x1[l][4 * j + e], *v = &x2[l][4 * j + e];
+                                    const f32x2 a1 = pair(u[0], u[1]), a2 = pair(v[0], v[1]);
+                                    f32x2 o2;
+                                    if constexpr (kDots) {
+                                        const f32x2 w1 = mul2(a1, wi);
+                                        u[0] = lo_of(w1);
+                                        u[1] = hi_of(w1);
+                                        o2 = add2(a2, w1);
+                                    } else {
+                                        o2 = fma2(a1, wi, a2);
+                                    }
+                                    v[0] = lo_of(o2);
+                                    v[1] = hi_of(o2);
                                 }
                         }
                         if constexpr (kDots) {
@@ -572,16 +607,17 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
             }
         }
     } else if (warp < kWarpMask) {
-        // ============ split warps: w z of 32 tokens, in three terms ============
+        // ============ split warps: w z of 16 tokens, in three terms ============
         regs_down<kRegsWork>();
-        const int quarter = warp & 3, hf = (warp - kWarpSplit) >> 2, st = tid - 32 * kWarpSplit - 128 * hf;
-        const uint32_t tq = tmem + (uint32_t(quarter * 32) << 16) + K::kColW + (K::kWz == 2 ? 48u * hf : 0u);
+        const int quarter = warp & 3, grp = (warp - kWarpSplit) >> 2, st = tid - 32 * kWarpSplit - 128 * grp;
+        const uint32_t tw = tmem + (uint32_t(quarter * 32) << 16) + K::kColW;
+        const uint32_t ch = uint32_t(4 * (quarter & 1) + (lane >> 3)), r7 = uint32_t(lane & 7);
+        const uint32_t src = uint32_t(quarter >> 1) * kAtom + r7 * 128 + ((ch ^ r7) << 4);
         while (w.next(kSt)) {
             for (int n = 0; n < w.nch; ++n) {
                 const uint32_t mm = m + uint32_t(n);
                 const int L = min(kDecayChunk, w.seg.len - w.chunk_at(n));
                 const uint32_t s = mm % kRing, ring_phase = (mm / kRing) & 1u;
-                const uint32_t zt = sb + K::kOffZ + s * kTile;
                 if (ok) ok = warp_wait(bar(kBZ + int(s)), ring_phase) && warp_wait(bar(kBVec + int(mm & 3u)), (mm >> 2) & 1u);
                 if (L < kDecayChunk) {
                     // tokens past the end are another sequence's: their y, whatever it holds, must not meet a zero
@@ -589,72 +625,65 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                     if (ok) ok = warp_wait(bar(kBY + int(s)), ring_phase);
                     const uint32_t yt = sb + K::kOffY + s * kTile;
                     for (int e = st; e < 256 * ya && ok; e += 128) {
-                        const int r = 32 * hf + ((e >> 3) & 31);  // pieces of 16 bytes: 8 a row, 32 rows, column halves
+                        // pieces of 16 bytes: 8 a row, this group's 32 rows (its two quarters), column halves
+                        const int r = 16 * grp + ((e >> 3) & 15) + ((e >> 2) & 32);
                         if (r >= L)
                             st_shared_v4(yt + uint32_t(e >> 8) * kAtom + uint32_t(r) * 128 + uint32_t(e & 7) * 16,
                                          make_uint4(0u, 0u, 0u, 0u));
                     }
                     fence_proxy_async_shared();
                     // all four warps' rows are written before any of them arrives; they go on, or stop, together
-                    if (named_sync_or(kBarSplit + hf, 128, !ok)) {
+                    if (named_sync_or(kBarSplit + grp, 128, !ok)) {
                         ok = false;
                         goto split_done;
                     }
                 }
                 if (!ok) continue;  // (on to the next meeting of the four, or out)
-                {
-                    // KV has read these columns: the chunk before's, or (room for one half) the half before's
-                    if (K::kWz == 2) {
-                        if (mm > 0) ok = warp_wait(bar(kBKV0 + hf), (mm - 1) & 1u);
-                    } else if (hf) {
-                        ok = warp_wait(bar(kBKV0), mm & 1u);
-                    } else if (mm > 0) {
-                        ok = warp_wait(bar(kBKV1), (mm - 1) & 1u);
-                    }
-                    if (!ok) continue;
-                    tc_fence_after();
-                    // transposed reads give token pairs of a z row, the layout of a tensor-memory A operand
-                    const float *wst = vecs(mm) + kVecSt + 32 * hf + 2 * (lane & 3);
-                    const uint32_t ch = uint32_t(4 * (quarter & 1) + (lane >> 3)), r7 = uint32_t(lane & 7);
-                    const uint32_t src = zt + uint32_t(quarter >> 1) * kAtom + uint32_t(32 * hf + r7) * 128 + ((ch ^ r7) << 4);
-#pragma unroll 2
-                    for (int j = 0; j < 4; ++j) {  // groups of 8 tokens
+                const float *wst = vecs(mm) + kVecSt + 2 * (lane & 3);
+                const uint32_t zt = sb + K::kOffZ + s * kTile + src;
+#pragma unroll 1
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int t16 = 16 * grp + 32 * hf;  // the quarter's first token
+                    const uint32_t qq = uint32_t(grp + 2 * hf), turn = K::qturn(mm, qq);
+                    uint32_t w0[2][4], w1[2][4], w2[2][4];  // two groups of 8 tokens; 8-row blocks of z
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        // transposed reads give token pairs of a z row, the layout of a tensor-memory A operand
                         uint32_t q[4];
-                        ldmatrix_t(src + 1024 * j, q);
+                        ldmatrix_t(zt + 128u * uint32_t(t16 + 8 * j), q);
                         if (L < kDecayChunk) {
-                            const int tk = 32 * hf + 8 * j + 2 * (lane & 3);
+                            const int tk = t16 + 8 * j + 2 * (lane & 3);
                             const uint32_t keep = (tk < L ? 0xffffu : 0u) | (tk + 1 < L ? 0xffff0000u : 0u);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) q[i] &= keep;
                         }
-                        const float2 wt = *reinterpret_cast<const float2 *>(wst + 8 * j);
+                        const f32x2 wt = *reinterpret_cast<const f32x2 *>(wst + t16 + 8 * j);
 #pragma unroll
-                        for (int l = 0; l < 2; ++l) {  // 16 z rows
-                            uint32_t w0[2], w1[2], w2[2];
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                float lo = bf_lo(q[2 * l + i]) * wt.x, hi = bf_hi(q[2 * l + i]) * wt.y;
-                                w0[i] = pack_bf16x2(lo, hi);
-                                lo -= bf_lo(w0[i]);
-                                hi -= bf_hi(w0[i]);
-                                w1[i] = pack_bf16x2(lo, hi);
-                                lo -= bf_lo(w1[i]);
-                                hi -= bf_hi(w1[i]);
-                                w2[i] = pack_bf16x2(lo, hi);
-                            }
-                            const uint32_t dst = tq + (uint32_t(16 * l) << 16) + 4 * j;
-                            tmem_st_frag(dst, w0);
-                            tmem_st_frag(dst + 16, w1);
-                            tmem_st_frag(dst + 32, w2);
+                        for (int i = 0; i < 4; ++i) {
+                            f32x2 x = mul2(from_bf16x2(q[i]), wt);
+                            w0[j][i] = to_bf16x2(x);
+                            x = sub_bf16x2(x, w0[j][i]);
+                            w1[j][i] = to_bf16x2(x);
+                            x = sub_bf16x2(x, w1[j][i]);
+                            w2[j][i] = to_bf16x2(x);
                         }
+                    }
+                    if (hf == 1 && lane == 0) mbar_arrive(bar(kBZFree + int(s)));  // (its last read of z)
+                    // KV has read these columns' previous quarter
+                    if (turn > 0) ok = warp_wait(bar(kBKq + int(K::qbuf(qq))), (turn - 1) & 1u);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int l = 0; l < 2; ++l) {  // 16 z rows: two columns groups of 8 tokens, two 8-row blocks
+                        const uint32_t at = tw + 24u * K::qbuf(qq) + (uint32_t(16 * l) << 16);
+                        tmem_st_frag(at, w0[0][2 * l], w0[0][2 * l + 1], w0[1][2 * l], w0[1][2 * l + 1]);
+                        tmem_st_frag(at + 8, w1[0][2 * l], w1[0][2 * l + 1], w1[1][2 * l], w1[1][2 * l + 1]);
+                        tmem_st_frag(at + 16, w2[0][2 * l], w2[0][2 * l + 1], w2[1][2 * l], w2[1][2 * l + 1]);
                     }
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(bar(kBW + hf));
-                        mbar_arrive(bar(kBZFree + int(s)));
-                    }
+                    if (lane == 0) mbar_arrive(bar(kBW + int(K::qbuf(qq))));
                 }
             }
             m += uint32_t(w.nch);
@@ -674,7 +703,7 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                     const float *G = vecs(mm) + kVecG;
                     ok = warp_wait(bar(kBVec + int(mm & 3u)), (mm >> 2) & 1u);
                     if (ok && mm >= 2) ok = warp_wait(bar(kBPFree + int(mm & 1u)), ((mm >> 1) - 1) & 1u);
-                    if (ok) ok = warp_wait(bar(kBQK), mm & 1u);
+                    if (ok) ok = warp_wait(bar(kBQK + int(K::buf(mm))), K::phase(mm));
                     const uint32_t s = mm % kRing;
                     if (ok && L < kDecayChunk) ok = warp_wait(bar(kBZ + int(s)), (mm / kRing) & 1u);
                     if (!ok) break;
@@ -690,7 +719,7 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
 #pragma unroll 1
                     for (int p = 0; p < 2; ++p) {
                         float v[16];
-                        tmem_ld_m64(tq + K::kColQK + 16 * p, v);
+                        tmem_ld_m64(tq + K::col_x2(mm) + 16 * p, v);
                         tmem_wait_ld();
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
@@ -814,47 +843,49 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
         const uint32_t id_qk = idesc_bf16(64, 64, false, false), id_kv = idesc_bf16(128, 64 * ya, false, true);
         const uint32_t id_x1 = idesc_bf16(128, 64, false, false), id_x2 = idesc_bf16(128, 64, true, false);
         auto koff = [](int s) { return uint64_t(((s >> 2) * kAtom + (s & 3) * 32) >> 4); };  // K-major steps
-        auto out_read = [&](uint32_t c) { return c == 0 || mbar_wait(bar(kBOutFree), (c - 1) & 1u); };
+        // the out warps have read chunk c's X1 and X2
+        auto out_read = [&](uint32_t c) { return mbar_wait(bar(kBOutFree), c & 1u); };
         auto issue_qk = [&](uint32_t c) {
             const uint32_t s = c % kRing, ph = (c / kRing) & 1u;
             if (!mbar_wait(bar(kBX + int(s)), ph) || !mbar_wait(bar(kBY + int(s)), ph)) return false;
-            if (K::kColQK == K::kColX2 && !out_read(c)) return false;
+            if (c >= uint32_t(K::kBufs) && !out_read(c - K::kBufs)) return false;
             tc_fence_after();
             const uint64_t dx = smem_desc(sb + K::kOffX + s * kTile, 16, 1024), dyd = smem_desc(sb + K::kOffY + s * kTile, 16, 1024);
 #pragma unroll 1
             for (int j = 0; j < ya; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    mma_bf16(tmem + K::kColQK, dx + koff(4 * j) + koff(i), dyd + koff(4 * j) + koff(i), id_qk, i > 0 || j > 0);
-            mma_commit(bar(kBQK));
+                    mma_bf16(tmem + K::col_x2(c), dx + koff(4 * j) + koff(i), dyd + koff(4 * j) + koff(i), id_qk, i > 0 || j > 0);
+            mma_commit(bar(kBQK + int(K::buf(c))));
             mma_commit(bar(kBYFree + int(s)));
             return true;
         };
-        auto issue_kv = [&](uint32_t c, int hf) {
+        auto issue_kv = [&](uint32_t c) {
             const uint32_t s = c % kRing;
-            if (hf == 0) {
-                if (!mbar_wait(bar(kBY + int(s)), (c / kRing) & 1u)) return false;
-                if (c > 0 && !mbar_wait(bar(kBLFree), (c - 1) & 1u)) return false;
-            }
-            if (!mbar_wait(bar(kBW + hf), c & 1u)) return false;
-            tc_fence_after();
-            const uint64_t db = smem_desc(sb + K::kOffY + s * kTile + 4096u * uint32_t(hf), 8192, 1024);
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
+            if (!mbar_wait(bar(kBY + int(s)), (c / kRing) & 1u)) return false;
+            const uint32_t back = kSt ? 2u : 1u;  // the chunk whose L these columns held
+            if (c >= back && !mbar_wait(bar(kBLFree + int(K::lbuf(c))), K::lphase(c - back))) return false;
+            const uint64_t db = smem_desc(sb + K::kOffY + s * kTile, 8192, 1024);
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t b = K::qbuf(uint32_t(q));
+                if (!mbar_wait(bar(kBW + int(b)), K::qturn(c, uint32_t(q)) & 1u)) return false;
+                tc_fence_after();
+                const uint32_t col = tmem + K::kColW + 24u * b;
 #pragma unroll
                 for (int t = 0; t < 3; ++t)
-                    mma_bf16_ts(tmem + K::kColL, tmem + K::kColW + (K::kWz == 2 ? 48u * hf : 0u) + 16 * t + 8 * i, db + uint64_t((i * 2048) >> 4), id_kv,
-                                hf > 0 || i > 0 || t > 0);
-            mma_commit(bar(kBKV0 + hf));
-            if (hf) {
-                mbar_arrive(bar(kBKV1));
-                mma_commit(bar(kBYFree + int(s)));
+                    mma_bf16_ts(tmem + K::col_l(c), col + 8 * t, db + uint64_t((q * 2048) >> 4), id_kv, q > 0 || t > 0);
+                mma_commit(bar(kBKq + int(b)));
             }
+            mma_commit(bar(kBKV + int(K::lbuf(c))));
+            mbar_arrive(bar(kBKV + int(K::lbuf(c))));
+            mma_commit(bar(kBYFree + int(s)));
             return true;
         };
         auto issue_x1 = [&](uint32_t c) {
             const uint32_t s = c % kRing;
-            if (!mbar_wait(bar(kBSt), c & 1u) || !out_read(c)) return false;
+            if (!mbar_wait(bar(kBSt), c & 1u)) return false;
+            if (c > 0 && !out_read(c - 1)) return false;
             tc_fence_after();
             const uint64_t dx = smem_desc(sb + K::kOffX + s * kTile, 16, 1024);
 #pragma unroll 1
@@ -869,16 +900,16 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
             mma_commit(bar(kBXFree + int(s)));
             return true;
         };
-        auto issue_x2 = [&](uint32_t c, bool first) {  // (first: P(c) has not been waited for)
+        auto issue_x2 = [&](uint32_t c) {
             const uint32_t s = c % kRing;
-            if (first && !mbar_wait(bar(kBP + int(c & 1u)), (c >> 1) & 1u)) return false;
+            if (!mbar_wait(bar(kBP + int(c & 1u)), (c >> 1) & 1u)) return false;
             if (!mbar_wait(bar(kBZ + int(s)), (c / kRing) & 1u)) return false;
             tc_fence_after();
             const uint64_t da = smem_desc(sb + K::kOffZ + s * kTile, 8192, 1024);
             const uint64_t db = smem_desc(sb + K::kOffP + (c & 1u) * kPTile, 16, 1024);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                mma_bf16(tmem + K::kColX2, da + uint64_t((i * 2048) >> 4), db + uint64_t((i * 32) >> 4), id_x2, i > 0);
+                mma_bf16(tmem + K::col_x2(c), da + uint64_t((i * 2048) >> 4), db + uint64_t((i * 32) >> 4), id_x2, i > 0);
             mma_commit(bar(kBOut));
             mbar_arrive(bar(kBOut));
             mma_commit(bar(kBZFree + int(s)));
@@ -886,18 +917,16 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
             return true;
         };
         if (warp == kWarpKv) {
-            for (uint32_t c = 0; ok && c < total; ++c) ok = issue_kv(c, 0) && issue_kv(c, 1);
+            for (uint32_t c = 0; ok && c < total; ++c) ok = issue_kv(c);
         } else if constexpr (kKind == kPlain) {
-            // QK(c + 1) as soon as the mask warps have read QK(c)
+            // QK a chunk ahead
             if (total > 0) ok = ok && issue_qk(0);
-            for (uint32_t c = 0; ok && c < total; ++c) {
-                ok = issue_x1(c) && mbar_wait(bar(kBP + int(c & 1u)), (c >> 1) & 1u) &&
-                     (c + 1 == total || issue_qk(c + 1)) && issue_x2(c, false);
-            }
+            for (uint32_t c = 0; ok && c < total; ++c)
+                ok = (c + 1 == total || issue_qk(c + 1)) && issue_x1(c) && issue_x2(c);
         } else if constexpr (kDots) {
             if (total > 0) ok = ok && issue_qk(0);
             for (uint32_t c = 0; ok && c < total; ++c)
-                ok = issue_x1(c) && issue_x2(c, true) && (c + 1 == total || issue_qk(c + 1));
+                ok = issue_x1(c) && issue_x2(c) && (c + 1 == total || issue_qk(c + 1));
         }
         // every product done before the tensor memory goes
         mma_commit(bar(kBDrain));
