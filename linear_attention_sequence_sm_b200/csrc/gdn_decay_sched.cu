@@ -14,16 +14,27 @@ constexpr int kSchedThreads = 1024;
 // skipped and sequences keep their given order.
 constexpr int kMaxRankedSeqs = 8192;
 
-// Tokens times heads each SM takes when the work is spread evenly.
-__host__ __device__ inline int64_t balanced_tokens(int64_t tokens, int hv) {
-    return (tokens * hv + kDecayPlanSms - 1) / kDecayPlanSms;
+// Tokens times heads each of `ways` CTAs takes when the work is spread evenly.
+__host__ __device__ inline int64_t balanced_tokens(int64_t tokens, int hv, int ways) {
+    return (tokens * hv + ways - 1) / ways;
+}
+
+// How finely a pass is cut: a tensor-core CTA has an SM to itself and a long
+// prologue; the CUDA-core pass runs two blocks an SM, bound by their latency,
+// and gains from a third in reserve.
+struct DecayPlan {
+    int ways, min_seg;
+};
+inline DecayPlan plan_of(const gdn_shape_t &s) {
+    return decay_tc_supported(s) ? DecayPlan{kDecayPlanSms, kDecayMinSeg} : DecayPlan{3 * kDecayPlanSms, kDecayMinSeg / 2};
 }
 
 // Whether any sequence may be cut: the longest has at most seq_len tokens (all
 // of them, with cu_seqlens).
 inline bool may_split(const gdn_shape_t &s) {
-    return s.seq_len > kDecayMinSeg &&
-           s.seq_len >= 2 * balanced_tokens(int64_t(s.batch) * s.seq_len, s.num_v_heads);
+    const DecayPlan p = plan_of(s);
+    return s.seq_len > p.min_seg &&
+           s.seq_len >= 2 * balanced_tokens(int64_t(s.batch) * s.seq_len, s.num_v_heads, p.ways);
 }
 
 // Exclusive prefix sums over the block of kN values per thread; totals gets the sums.
@@ -62,14 +73,14 @@ __device__ void block_scan(int (&v)[kN], int (&totals)[kN], int *part) {
 
 // Checks cu_seqlens and writes the segment table, longest sequences first.
 // A sequence is a chain of dependent chunks, so a call with few sequences and
-// heads would leave SMs idle: with B = tokens * Hv / 148 (a perfect spread) and
+// heads would leave SMs idle: with B = tokens * Hv / ways (a perfect spread) and
 // the longest sequence at least 2 B, sequences are cut into segments of
-// ceil(longest / floor(longest / B)) tokens, whose start states come from a
+// ceil(longest / floor(longest / B)) tokens, rounded up, whose start states come from a
 // first sweep over all segments but one end's (k and v are then read twice, a
 // third of the prefill's traffic; the uncut chain would take at least twice as
 // long).  At 1 x 65,536 tokens and 48 heads: 3 segments of 22,528 tokens.
 __global__ void __launch_bounds__(kSchedThreads)
-decay_schedule_kernel(int32_t num_seqs, int32_t tokens, int32_t batched_len, int32_t hv,
+decay_schedule_kernel(int32_t num_seqs, int32_t tokens, int32_t batched_len, int32_t hv, DecayPlan plan,
                       const int32_t *__restrict__ cu, DecaySched sc, int32_t *order) {
     __shared__ int bad, longest;
     __shared__ int part[96];
@@ -110,12 +121,14 @@ decay_schedule_kernel(int32_t num_seqs, int32_t tokens, int32_t batched_len, int
     // segment length and checkpoint spacing
     int seg_len = INT32_MAX, ick = kDecayMaxIck;
     {
-        const int64_t balanced = balanced_tokens(tokens, hv);
+        const int64_t balanced = balanced_tokens(tokens, hv, plan.ways);
         const int64_t k = balanced > 0 ? longest / balanced : 1;
-        if (k >= 2 && longest > kDecayMinSeg) {
+        if (k >= 2 && longest > plan.min_seg) {
             int64_t L = (longest + k - 1) / k;
-            L = L <= kDecayMinSeg ? kDecayMinSeg : L <= 2 * kDecayMinSeg ? 2 * kDecayMinSeg
-                                                                         : (L + kDecayMaxIck - 1) / kDecayMaxIck * kDecayMaxIck;
+            // (checkpoints fall on the cuts: up to 1024 tokens a power of two, then a multiple of 1024)
+            int64_t up = plan.min_seg;
+            while (up < L && up < kDecayMaxIck) up *= 2;
+            L = L <= up ? up : (L + kDecayMaxIck - 1) / kDecayMaxIck * kDecayMaxIck;
             seg_len = int(L);
             ick = min(seg_len, kDecayMaxIck);
         }
@@ -333,17 +346,18 @@ decay_group_sum_any_kernel(const DecayHeader *hdr, const float *__restrict__ par
 
 DecayLayout decay_layout(const gdn_shape_t &s, bool backward) {
     const int64_t tokens = int64_t(s.batch) * s.seq_len, N = s.num_seqs, hv = s.num_v_heads;
-    // segments are at least max(256, tokens * hv / 148) tokens long, and a cut
-    // sequence is longer than one: it has at most 2 len / L of them
-    const int64_t balanced = balanced_tokens(tokens, s.num_v_heads);
-    const int64_t shortest = std::max<int64_t>(kDecayMinSeg, balanced);
+    // segments are at least max(min_seg, tokens * hv / ways) tokens long, and a
+    // cut sequence is longer than one: it has at most 2 len / L of them
+    const DecayPlan plan = plan_of(s);
+    const int64_t balanced = balanced_tokens(tokens, s.num_v_heads, plan.ways);
+    const int64_t shortest = std::max<int64_t>(plan.min_seg, balanced);
     DecayLayout L = {};
     L.max_slots = may_split(s) ? 2 * tokens / shortest + 1 : 0;
     L.max_split = may_split(s) ? tokens / shortest + 1 : 0;
     L.max_segs = N + L.max_slots;
     L.max_chunks = (tokens + 63 * N) / kDecayChunk;
     // checkpoints are `ick` apart, 1024 unless segments are shorter
-    L.max_cks = tokens / (balanced >= kDecayMaxIck || !may_split(s) ? kDecayMaxIck : kDecayMinSeg) + N;
+    L.max_cks = tokens / (balanced >= kDecayMaxIck || !may_split(s) ? kDecayMaxIck : plan.min_seg) + N;
     size_t off = 256;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -384,7 +398,7 @@ DecaySched decay_sched(char *ws, const DecayLayout &L) {
 cudaError_t launch_decay_schedule(const gdn_shape_t &s, const int32_t *cu, char *ws, const DecayLayout &L,
                                   cudaStream_t stream) {
     decay_schedule_kernel<<<1, kSchedThreads, 0, stream>>>(s.num_seqs, s.batch * s.seq_len, cu ? 0 : s.seq_len,
-                                                           s.num_v_heads, cu, decay_sched(ws, L),
+                                                           s.num_v_heads, plan_of(s), cu, decay_sched(ws, L),
                                                            reinterpret_cast<int32_t *>(ws + L.order_off));
     count_launch();
     return cudaGetLastError();

@@ -18,23 +18,30 @@ namespace {
 
 constexpr int C = kDecayChunk;
 constexpr int kThreads = 256;
-constexpr int LD = 132;   // row pitch of 128-wide tiles (floats)
-constexpr int LP = 68;    // row pitch of the 64 x 64 mask tile
+constexpr int LP = 68;    // row pitch of the 64 x 64 mask tile (floats)
 
-struct SimtSmem {
-    float x[C * LD], y[C * LD], z[C * LD];
-    float S[128 * LD];
-    float p[C * LP];
+__host__ __device__ constexpr int padded(int d) { return (d + 7) & ~7; }
+__host__ __device__ constexpr int pitch(int d) { return padded(d) + 4; }  // of a tile of d columns
+
+// Token vectors, then the tiles x, y, z (64 rows), S (dz x dy) and P, sized by
+// the head sizes: up to 64 x 96 two blocks fit on an SM.
+struct SimtVec {
     double G[C];
     float w_in[C], w_st[C];
     float red[kThreads / 32];
     float gamma;
+    float pad[3];
 };
+static_assert(sizeof(SimtVec) % 16 == 0, "tiles are 16-byte aligned");
+inline size_t simt_smem(int dy, int dz, bool state_only) {
+    const size_t tiles = size_t(state_only ? 1 : 2) * C * pitch(dy) + size_t(C) * pitch(dz) + size_t(padded(dz)) * pitch(dy);
+    return sizeof(SimtVec) + 4 * (tiles + (state_only ? 0 : C * LP));
+}
 
 // rows [0, L) of a [tokens, heads, d] tensor's head into a tile, the rest of
 // the 64 rows and of the columns up to a multiple of 8 zero
 template <typename T>
-__device__ void load_tile(float *dst, const T *src, size_t stride, int d, int L, int dpad) {
+__device__ void load_tile(float *dst, int ld, const T *src, size_t stride, int d, int L, int dpad) {
     if (d % 4 == 0) {
         const int n4 = dpad / 4;
         for (int e = threadIdx.x; e < C * n4; e += kThreads) {
@@ -49,18 +56,18 @@ __device__ void load_tile(float *dst, const T *src, size_t stride, int d, int L,
                                     __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
                 }
             }
-            *reinterpret_cast<float4 *>(dst + r * LD + c) = v;
+            *reinterpret_cast<float4 *>(dst + r * ld + c) = v;
         }
     } else {
         for (int e = threadIdx.x; e < C * dpad; e += kThreads) {
             const int r = e / dpad, c = e % dpad;
-            dst[r * LD + c] = (r < L && c < d) ? to_f32(src[r * stride + c]) : 0.f;
+            dst[r * ld + c] = (r < L && c < d) ? to_f32(src[r * stride + c]) : 0.f;
         }
     }
 }
 
 // Prefix sums of a chunk's floored log-decays (warp 0), and the weights.
-__device__ void load_gates(SimtSmem &sm, const float *g, size_t g_stride, int L, bool reverse) {
+__device__ void load_gates(SimtVec &sm, const float *g, size_t g_stride, int L, bool reverse) {
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
         const float g0 = 2 * lane < L ? fmaxf(g[(2 * lane) * g_stride], kGFloor) : 0.f;
@@ -91,7 +98,7 @@ __device__ __forceinline__ float dot4(const float4 &a, const float4 &b, float c)
 __device__ __forceinline__ float4 ld4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 
 // 4 x 4 tile of a 64 x 64 product of rows: acc[i][j] = a[r0 + 16 i] . b[c0 + 16 j]
-__device__ __forceinline__ void gram(float (&acc)[4][4], const float *a, const float *b, int r0, int c0, int d) {
+__device__ __forceinline__ void gram(float (&acc)[4][4], const float *a, const float *b, int ld, int r0, int c0, int d) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -99,9 +106,9 @@ __device__ __forceinline__ void gram(float (&acc)[4][4], const float *a, const f
     for (int k = 0; k < d; k += 4) {
         float4 u[4], v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) u[i] = ld4(a + (r0 + 16 * i) * LD + k);
+        for (int i = 0; i < 4; ++i) u[i] = ld4(a + (r0 + 16 * i) * ld + k);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = ld4(b + (c0 + 16 * j) * LD + k);
+        for (int j = 0; j < 4; ++j) v[j] = ld4(b + (c0 + 16 * j) * ld + k);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -110,15 +117,17 @@ __device__ __forceinline__ void gram(float (&acc)[4][4], const float *a, const f
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 decay_pass_simt_kernel(const DecayPass a) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    SimtSmem &sm = *reinterpret_cast<SimtSmem *>(smem_raw);
+    SimtVec &sm = *reinterpret_cast<SimtVec *>(smem_raw);
     const DecayHeader *hdr = a.sched.hdr;
     if (hdr->status != GDN_OK) return;
     const int tid = threadIdx.x, rg = tid >> 4, cg = tid & 15;
     const int dy = a.dy, dz = a.dz, hv = a.hv;
-    const int dyp = (dy + 7) & ~7, dzp = (dz + 7) & ~7;
+    const int dyp = padded(dy), dzp = padded(dz), ly = pitch(dy), lz = pitch(dz);
+    float *ty = reinterpret_cast<float *>(smem_raw + sizeof(SimtVec)), *tz = ty + C * ly, *tS = tz + C * lz;
+    float *tx = tS + dzp * ly, *tp = tx + C * ly;
     const int64_t units = int64_t(hdr->num_segs) * hv;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
         const DecaySeg seg = a.sched.segs[u / hv];
@@ -143,7 +152,7 @@ decay_pass_simt_kernel(const DecayPass a) {
             float v = 0.f;
             if (src && r < dz && c < dy)
                 v = own ? src[a.seg_trans ? c * 128 + r : r * 128 + c] : src[a.s_trans ? c * dz + r : r * dy + c];
-            sm.S[r * LD + c] = v;
+            tS[r * ly + c] = v;
         }
         const int nch = (seg.len + C - 1) / C;
         float seg_sum = 0.f;
@@ -151,20 +160,20 @@ decay_pass_simt_kernel(const DecayPass a) {
             const int n = a.reverse ? nch - 1 - i : i;
             const int t0 = n * C, L = min(C, seg.len - t0);
             __syncthreads();
-            load_tile(sm.y, y + size_t(t0) * a.hy * dy, size_t(a.hy) * dy, dy, L, dyp);
-            load_tile(sm.z, z + size_t(t0) * a.hz * dz, size_t(a.hz) * dz, dz, L, dzp);
-            if (!a.state_only) load_tile(sm.x, x + size_t(t0) * a.hx * dy, size_t(a.hx) * dy, dy, L, dyp);
+            load_tile(ty, ly, y + size_t(t0) * a.hy * dy, size_t(a.hy) * dy, dy, L, dyp);
+            load_tile(tz, lz, z + size_t(t0) * a.hz * dz, size_t(a.hz) * dz, dz, L, dzp);
+            if (!a.state_only) load_tile(tx, ly, x + size_t(t0) * a.hx * dy, size_t(a.hx) * dy, dy, L, dyp);
             load_gates(sm, g + size_t(t0) * gs, gs, L, a.reverse);
             __syncthreads();
             seg_sum += float(sm.G[C - 1]);
             if (a.ckpt && !a.zsum && seg.pos + t0 > 0 && (seg.pos + t0) % hdr->ick == 0) {
                 float *dst = a.ckpt + (size_t(seg.ck + (seg.pos + t0) / hdr->ick) * hv + h) * 16384;
-                for (int q = tid; q < dz * dy; q += kThreads) dst[q] = sm.S[(q / dy) * LD + q % dy];
+                for (int q = tid; q < dz * dy; q += kThreads) dst[q] = tS[(q / dy) * ly + q % dy];
             }
             if (!a.state_only) {
                 {
                     float acc[4][4];
-                    gram(acc, sm.x, sm.y, rg, cg, dyp);
+                    gram(acc, tx, ty, ly, rg, cg, dyp);
 #pragma unroll
                     for (int p = 0; p < 4; ++p)
 #pragma unroll
@@ -172,7 +181,7 @@ decay_pass_simt_kernel(const DecayPass a) {
                             const int r = rg + 16 * p, c = cg + 16 * q;
                             const bool in = a.reverse ? c >= r : c <= r;
                             const double d = a.reverse ? sm.G[c] - sm.G[r] : sm.G[r] - sm.G[c];
-                            sm.p[r * LP + c] = in ? acc[p][q] * expf(float(d)) : 0.f;
+                            tp[r * LP + c] = in ? acc[p][q] * expf(float(d)) : 0.f;
                         }
                 }
                 __syncthreads();
@@ -187,11 +196,11 @@ decay_pass_simt_kernel(const DecayPass a) {
                     for (int c = 0; c < C; c += 4) {
                         float4 pr[4];
 #pragma unroll
-                        for (int p = 0; p < 4; ++p) pr[p] = ld4(sm.p + (4 * rg + p) * LP + c);
+                        for (int p = 0; p < 4; ++p) pr[p] = ld4(tp + (4 * rg + p) * LP + c);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float4 z0 = ld4(sm.z + (c + e) * LD + 4 * cg);
-                            const float4 z1 = hi ? ld4(sm.z + (c + e) * LD + 64 + 4 * cg) : make_float4(0, 0, 0, 0);
+                            const float4 z0 = ld4(tz + (c + e) * lz + 4 * cg);
+                            const float4 z1 = hi ? ld4(tz + (c + e) * lz + 64 + 4 * cg) : make_float4(0, 0, 0, 0);
 #pragma unroll
                             for (int p = 0; p < 4; ++p) {
                                 const float w = e == 0 ? pr[p].x : e == 1 ? pr[p].y : e == 2 ? pr[p].z : pr[p].w;
@@ -205,11 +214,11 @@ decay_pass_simt_kernel(const DecayPass a) {
                     for (int k = 0; k < dyp; k += 4) {
                         float4 xr[4];
 #pragma unroll
-                        for (int p = 0; p < 4; ++p) xr[p] = ld4(sm.x + (4 * rg + p) * LD + k);
+                        for (int p = 0; p < 4; ++p) xr[p] = ld4(tx + (4 * rg + p) * ly + k);
 #pragma unroll
                         for (int q = 0; q < 8; ++q) {
                             if (q >= 4 && !hi) break;
-                            const float4 s = ld4(sm.S + ((q < 4 ? 0 : 64) + 4 * cg + (q & 3)) * LD + k);
+                            const float4 s = ld4(tS + ((q < 4 ? 0 : 64) + 4 * cg + (q & 3)) * ly + k);
 #pragma unroll
                             for (int p = 0; p < 4; ++p) ex[p][q] = dot4(xr[p], s, ex[p][q]);
                         }
@@ -246,13 +255,13 @@ decay_pass_simt_kernel(const DecayPass a) {
                     float acc[4][4];
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
-                        const float4 s = ld4(sm.S + (zb + p) * LD + yb);
+                        const float4 s = ld4(tS + (zb + p) * ly + yb);
                         acc[p][0] = sm.gamma * s.x; acc[p][1] = sm.gamma * s.y;
                         acc[p][2] = sm.gamma * s.z; acc[p][3] = sm.gamma * s.w;
                     }
                     for (int c = 0; c < L; ++c) {
                         const float w = sm.w_st[c];
-                        const float4 zv = ld4(sm.z + c * LD + zb), yv = ld4(sm.y + c * LD + yb);
+                        const float4 zv = ld4(tz + c * lz + zb), yv = ld4(ty + c * ly + yb);
                         const float zw[4] = {w * zv.x, w * zv.y, w * zv.z, w * zv.w};
 #pragma unroll
                         for (int p = 0; p < 4; ++p) {
@@ -262,7 +271,7 @@ decay_pass_simt_kernel(const DecayPass a) {
                     }
 #pragma unroll
                     for (int p = 0; p < 4; ++p)
-                        *reinterpret_cast<float4 *>(sm.S + (zb + p) * LD + yb) =
+                        *reinterpret_cast<float4 *>(tS + (zb + p) * ly + yb) =
                             make_float4(acc[p][0], acc[p][1], acc[p][2], acc[p][3]);
                 }
             if (a.zsum && (seg.pos + t0) % hdr->ick == 0) {
@@ -276,7 +285,7 @@ decay_pass_simt_kernel(const DecayPass a) {
                 if (cp)
                     for (int q = tid; q < dz * dy; q += kThreads) {
                         const bool tr = start && a.s_trans;
-                        s = fmaf(cp[q], sm.S[(tr ? q % dz : q / dy) * LD + (tr ? q / dz : q % dy)], s);
+                        s = fmaf(cp[q], tS[(tr ? q % dz : q / dy) * ly + (tr ? q / dz : q % dy)], s);
                     }
 #pragma unroll
                 for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
@@ -288,7 +297,7 @@ decay_pass_simt_kernel(const DecayPass a) {
         __syncthreads();
         if (a.state_only) {
             float *dst = a.seg_local + (size_t(seg.slot) * hv + h) * 16384;
-            for (int e = tid; e < dz * dy; e += kThreads) dst[(e / dy) * 128 + e % dy] = sm.S[(e / dy) * LD + e % dy];
+            for (int e = tid; e < dz * dy; e += kThreads) dst[(e / dy) * 128 + e % dy] = tS[(e / dy) * ly + e % dy];
             if (tid == 0) a.seg_dec[size_t(seg.slot) * hv + h] = expf(seg_sum);
             continue;
         }
@@ -296,7 +305,7 @@ decay_pass_simt_kernel(const DecayPass a) {
             float *dst = a.s_out + (size_t(seg.seq) * hv + h) * dz * dy;
             for (int e = tid; e < dz * dy; e += kThreads) {
                 const int r = a.s_trans ? e % dz : e / dy, c = a.s_trans ? e / dz : e % dy;
-                dst[e] = sm.S[r * LD + c];
+                dst[e] = tS[r * ly + c];
             }
         }
     }
@@ -305,6 +314,7 @@ decay_pass_simt_kernel(const DecayPass a) {
 // The pairs inside one chunk: intra_t = sum of W_ij over j < t <= i,
 // W_ij = e^{G_i - G_j} (q_i . k_j) (do_i . v_j).  Row i's running sums over j
 // give X_i,t = sum_{j < t} W_ij; column t then sums X_i,t over i >= t.
+constexpr int LD = 132;  // row pitch of 128-wide tiles
 struct IntraSmem {
     float q[C * LD], k[C * LD], v[C * LD], o[C * LD];
     float w[C * LP];
@@ -331,10 +341,10 @@ decay_intra_simt_kernel(const DecaySched sc, int num_seqs, int hk, int hv, int d
         const int t0 = (gc - sc.chunk_base[n]) * C, L = min(C, len - t0);
         const size_t tok = size_t(start) + t0;
         __syncthreads();
-        load_tile(sm.q, q + (tok * hk + hq) * dk, size_t(hk) * dk, dk, L, dkp);
-        load_tile(sm.k, k + (tok * hk + hq) * dk, size_t(hk) * dk, dk, L, dkp);
-        load_tile(sm.v, v + (tok * hv + h) * dv, size_t(hv) * dv, dv, L, dvp);
-        load_tile(sm.o, d_o + (tok * hv + h) * dv, size_t(hv) * dv, dv, L, dvp);
+        load_tile(sm.q, LD, q + (tok * hk + hq) * dk, size_t(hk) * dk, dk, L, dkp);
+        load_tile(sm.k, LD, k + (tok * hk + hq) * dk, size_t(hk) * dk, dk, L, dkp);
+        load_tile(sm.v, LD, v + (tok * hv + h) * dv, size_t(hv) * dv, dv, L, dvp);
+        load_tile(sm.o, LD, d_o + (tok * hv + h) * dv, size_t(hv) * dv, dv, L, dvp);
         if (tid < 32) {
             const float *gp = g_const ? g + h : g + tok * hv + h;
             const size_t gs = g_const ? 0 : hv;
@@ -352,8 +362,8 @@ decay_intra_simt_kernel(const DecaySched sc, int num_seqs, int hk, int hv, int d
         __syncthreads();
         {
             float A[4][4], B[4][4];
-            gram(A, sm.q, sm.k, rg, cg, dkp);
-            gram(B, sm.o, sm.v, rg, cg, dvp);
+            gram(A, sm.q, sm.k, LD, rg, cg, dkp);
+            gram(B, sm.o, sm.v, LD, rg, cg, dvp);
 #pragma unroll
             for (int p = 0; p < 4; ++p)
 #pragma unroll
@@ -402,13 +412,12 @@ cudaError_t launch_decay_pass_simt(const DecayPass &p, int32_t dtype, int64_t ma
     if (max_units <= 0) return cudaSuccess;
     const void *kern = dtype == GDN_DTYPE_BF16 ? reinterpret_cast<const void *>(decay_pass_simt_kernel<__nv_bfloat16>)
                                                : reinterpret_cast<const void *>(decay_pass_simt_kernel<float>);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(SimtSmem)));
+    const size_t bytes = simt_smem(p.dy, p.dz, p.state_only);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
     if (e != cudaSuccess) return e;
     const unsigned grid = unsigned(std::min<int64_t>(max_units, kDecayPlanSms * 8));
-    if (dtype == GDN_DTYPE_BF16)
-        decay_pass_simt_kernel<__nv_bfloat16><<<grid, kThreads, sizeof(SimtSmem), stream>>>(p);
-    else
-        decay_pass_simt_kernel<float><<<grid, kThreads, sizeof(SimtSmem), stream>>>(p);
+    if (dtype == GDN_DTYPE_BF16) decay_pass_simt_kernel<__nv_bfloat16><<<grid, kThreads, bytes, stream>>>(p);
+    else decay_pass_simt_kernel<float><<<grid, kThreads, bytes, stream>>>(p);
     count_launch();
     return cudaGetLastError();
 }
