@@ -203,31 +203,49 @@ decay_schedule_kernel(int32_t num_seqs, int32_t tokens, int32_t batched_len, int
     }
 }
 
-// Start states of cut sequences: thread = one element of a (cut sequence,
+// Start states of cut sequences: thread = four elements of a (cut sequence,
 // head) state, walking its segments in pass order; each slot's local state
-// becomes the state its segment starts from.
+// becomes the state its segment starts from.  Four segments' local states are
+// read ahead of the chain.
 __global__ void __launch_bounds__(256)
 decay_combine_kernel(DecaySched sc, float *__restrict__ states, const float *__restrict__ seg_dec,
                      const float *__restrict__ s_in, int s_trans, int hv, int dz, int dy, int reverse) {
     if (sc.hdr->status != GDN_OK) return;
     const int h = blockIdx.y;
-    const int el = blockIdx.x * 256 + threadIdx.x;  // of the 128 x 128 padded state
-    const int r = el >> 7, c = el & 127;            // z row, y column
+    const int el = 4 * (blockIdx.x * 256 + threadIdx.x);  // of the 128 x 128 padded state
+    const int r = el >> 7, c = el & 127;                  // z row, y columns c .. c + 3
     for (int j = blockIdx.z; j < sc.hdr->num_split; j += gridDim.z) {
-        const int s0 = sc.split[j];
-        const DecaySeg first = sc.segs[s0];
+        const DecaySeg first = sc.segs[sc.split[j]];
         const int n = (first.seq_len + sc.hdr->seg_len - 1) / sc.hdr->seg_len;
-        float run = 0.f;
-        if (s_in && r < dz && c < dy) {
-            const size_t base = (size_t(first.seq) * hv + h) * dz * dy;
-            run = s_in[base + (s_trans ? size_t(c) * dz + r : size_t(r) * dy + c)];
+        float run[4] = {0.f, 0.f, 0.f, 0.f};
+        if (s_in && r < dz) {
+            const float *src = s_in + (size_t(first.seq) * hv + h) * dz * dy;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < dy) run[e] = src[s_trans ? size_t(c + e) * dz + r : size_t(r) * dy + c + e];
         }
-        for (int i = 0; i < n; ++i) {
-            const int slot = first.slot + (reverse ? n - 1 - i : i);
-            float *p = states + (size_t(slot) * hv + h) * 16384 + el;
-            const float local = i + 1 < n ? *p : 0.f;  // the last segment's local state is not needed
-            *p = run;
-            run = fmaf(seg_dec[size_t(slot) * hv + h], run, local);
+        auto slot = [&](int i) { return size_t(first.slot + (reverse ? n - 1 - i : i)) * hv + h; };
+        for (int i0 = 0; i0 < n; i0 += 4) {
+            float4 local[4];
+            float dec[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                local[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                dec[i] = 0.f;
+                if (i0 + i + 1 < n) {  // the last segment's local state is not needed
+                    local[i] = *reinterpret_cast<const float4 *>(states + slot(i0 + i) * 16384 + el);
+                    dec[i] = seg_dec[slot(i0 + i)];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i0 + i >= n) break;
+                *reinterpret_cast<float4 *>(states + slot(i0 + i) * 16384 + el) = make_float4(run[0], run[1], run[2], run[3]);
+                run[0] = fmaf(dec[i], run[0], local[i].x);
+                run[1] = fmaf(dec[i], run[1], local[i].y);
+                run[2] = fmaf(dec[i], run[2], local[i].z);
+                run[3] = fmaf(dec[i], run[3], local[i].w);
+            }
         }
     }
 }
@@ -255,11 +273,20 @@ decay_dg_kernel(int num_seqs, int hv, int tokens, const int32_t *__restrict__ cu
         const float *in = intra + size_t(h) * tokens + start;
         float across = 0.f;
         for (int e = 0; e < 8; ++e) across += zsum[(size_t(ck) * hv + h) * 8 + e];
+        float2 nq, nk, ni;  // this lane's two tokens of the next chunk
+        auto fetch = [&](int b) {
+            const int t = b + 2 * lane;
+            const bool v0 = t < p1, v1 = t + 1 < p1;
+            nq = make_float2(v0 ? dq[t] : 0.f, v1 ? dq[t + 1] : 0.f);
+            nk = make_float2(v0 ? dk[t] : 0.f, v1 ? dk[t + 1] : 0.f);
+            ni = make_float2(v0 ? in[t] : 0.f, v1 ? in[t + 1] : 0.f);
+        };
+        fetch(p0);
         for (int b = p0; b < p1; b += kDecayChunk) {
-            const int t0 = b + 2 * lane, t1 = t0 + 1;
-            const bool v0 = t0 < p1, v1 = t1 < p1;
-            const float q0 = v0 ? dq[t0] : 0.f, q1 = v1 ? dq[t1] : 0.f;
-            const float k0 = v0 ? dk[t0] : 0.f, k1 = v1 ? dk[t1] : 0.f;
+            const int t0 = b + 2 * lane;
+            const float q0 = nq.x, q1 = nq.y, k0 = nk.x, k1 = nk.y;
+            const float2 ii = ni;
+            fetch(b + kDecayChunk);
             float qs = q0 + q1, ks = k0 + k1;  // inclusive: qs from the end, ks from the start
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -277,7 +304,7 @@ decay_dg_kernel(int num_seqs, int hv, int tokens, const int32_t *__restrict__ cu
                 const int t = t0 + e;
                 if (t >= p1) continue;
                 const float r = e ? q1 + q_after : qs, f = e ? k_before + k0 : k_before;
-                float val = in[t] + r + f + outside;
+                float val = (e ? ii.y : ii.x) + r + f + outside;
                 const size_t at = size_t(start + t) * hv + h;
                 if ((g_const ? g[h] : g[at]) < kGFloor) val = 0.f;
                 if (g_const) dg_tok[size_t(h) * tokens + start + t] = val;
@@ -410,7 +437,7 @@ cudaError_t launch_decay_combine(const gdn_shape_t &s, const DecayLayout &L, con
     if (L.max_split == 0) return cudaSuccess;
     const int hv = s.num_v_heads;
     const int deep = int(std::min<int64_t>(L.max_split, std::max(1, 64 / hv)));
-    decay_combine_kernel<<<dim3(64, unsigned(hv), unsigned(deep)), 256, 0, stream>>>(sc, states, seg_dec, s_in,
+    decay_combine_kernel<<<dim3(16, unsigned(hv), unsigned(deep)), 256, 0, stream>>>(sc, states, seg_dec, s_in,
                                                                                      s_trans, hv, dz, dy, reverse);
     count_launch();
     return cudaGetLastError();

@@ -185,43 +185,36 @@ decay_pass_simt_kernel(const DecayPass a) {
                         }
                 }
                 __syncthreads();
-                // out rows 4 rg .. 4 rg + 3, columns 4 cg .. and 64 + 4 cg ..
+                // out rows 4 rg .. 4 rg + 3, columns cg + 16 q (the rows of Sigma a quarter-warp reads are then
+                // next to one another and fall into different banks)
                 float in[4][8], ex[4][8];
 #pragma unroll
                 for (int p = 0; p < 4; ++p)
 #pragma unroll
                     for (int q = 0; q < 8; ++q) in[p][q] = ex[p][q] = 0.f;
-                const bool hi = 64 + 4 * cg < dzp, lo = 4 * cg < dzp;
-                if (lo) {
-                    for (int c = 0; c < C; c += 4) {
-                        float4 pr[4];
+                for (int c = 0; c < C; c += 4) {
+                    float4 pr[4];
 #pragma unroll
-                        for (int p = 0; p < 4; ++p) pr[p] = ld4(tp + (4 * rg + p) * LP + c);
+                    for (int p = 0; p < 4; ++p) pr[p] = ld4(tp + (4 * rg + p) * LP + c);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float4 z0 = ld4(tz + (c + e) * lz + 4 * cg);
-                            const float4 z1 = hi ? ld4(tz + (c + e) * lz + 64 + 4 * cg) : make_float4(0, 0, 0, 0);
+                    for (int q = 0; q < 8; ++q) {
+                        if (16 * q >= dzp) break;
+                        const float *zc = tz + c * lz + cg + 16 * q;  // (past dz: the row's padding, not used)
+                        const float4 zv = make_float4(zc[0], zc[lz], zc[2 * lz], zc[3 * lz]);
 #pragma unroll
-                            for (int p = 0; p < 4; ++p) {
-                                const float w = e == 0 ? pr[p].x : e == 1 ? pr[p].y : e == 2 ? pr[p].z : pr[p].w;
-                                in[p][0] = fmaf(w, z0.x, in[p][0]); in[p][1] = fmaf(w, z0.y, in[p][1]);
-                                in[p][2] = fmaf(w, z0.z, in[p][2]); in[p][3] = fmaf(w, z0.w, in[p][3]);
-                                in[p][4] = fmaf(w, z1.x, in[p][4]); in[p][5] = fmaf(w, z1.y, in[p][5]);
-                                in[p][6] = fmaf(w, z1.z, in[p][6]); in[p][7] = fmaf(w, z1.w, in[p][7]);
-                            }
-                        }
+                        for (int p = 0; p < 4; ++p) in[p][q] = dot4(pr[p], zv, in[p][q]);
                     }
-                    for (int k = 0; k < dyp; k += 4) {
-                        float4 xr[4];
+                }
+                for (int k = 0; k < dyp; k += 4) {
+                    float4 xr[4];
 #pragma unroll
-                        for (int p = 0; p < 4; ++p) xr[p] = ld4(tx + (4 * rg + p) * ly + k);
+                    for (int p = 0; p < 4; ++p) xr[p] = ld4(tx + (4 * rg + p) * ly + k);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            if (q >= 4 && !hi) break;
-                            const float4 s = ld4(tS + ((q < 4 ? 0 : 64) + 4 * cg + (q & 3)) * ly + k);
+                    for (int q = 0; q < 8; ++q) {
+                        if (16 * q >= dzp) break;
+                        const float4 s = ld4(tS + min(cg + 16 * q, dzp - 1) * ly + k);
 #pragma unroll
-                            for (int p = 0; p < 4; ++p) ex[p][q] = dot4(xr[p], s, ex[p][q]);
-                        }
+                        for (int p = 0; p < 4; ++p) ex[p][q] = dot4(xr[p], s, ex[p][q]);
                     }
                 }
 #pragma unroll
@@ -232,7 +225,7 @@ decay_pass_simt_kernel(const DecayPass a) {
                     float dot = 0.f;
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
-                        const int c = (q < 4 ? 0 : 64) + 4 * cg + (q & 3);
+                        const int c = cg + 16 * q;
                         const float e = w * ex[p][q];
                         if (r < L && c < dz) {
                             const size_t at = (row * hv + h) * dz + c;
