@@ -19,14 +19,13 @@ __host__ __device__ inline int64_t balanced_tokens(int64_t tokens, int hv, int w
     return (tokens * hv + ways - 1) / ways;
 }
 
-// How finely a pass is cut: a tensor-core CTA has an SM to itself and a long
-// prologue; the CUDA-core pass runs two blocks an SM, bound by their latency,
-// and gains from a third in reserve.
+// How finely a pass is cut: a tensor-core CTA has an SM to itself, of the
+// CUDA-core pass's blocks two share one.
 struct DecayPlan {
     int ways, min_seg;
 };
 inline DecayPlan plan_of(const gdn_shape_t &s) {
-    return decay_tc_supported(s) ? DecayPlan{kDecayPlanSms, kDecayMinSeg} : DecayPlan{3 * kDecayPlanSms, kDecayMinSeg / 2};
+    return decay_tc_supported(s) ? DecayPlan{kDecayPlanSms, kDecayMinSeg} : DecayPlan{2 * kDecayPlanSms, kDecayMinSeg / 2};
 }
 
 // Whether any sequence may be cut: the longest has at most seq_len tokens (all
@@ -125,10 +124,9 @@ decay_schedule_kernel(int32_t num_seqs, int32_t tokens, int32_t batched_len, int
         const int64_t k = balanced > 0 ? longest / balanced : 1;
         if (k >= 2 && longest > plan.min_seg) {
             int64_t L = (longest + k - 1) / k;
-            // (checkpoints fall on the cuts: up to 1024 tokens a power of two, then a multiple of 1024)
-            int64_t up = plan.min_seg;
-            while (up < L && up < kDecayMaxIck) up *= 2;
-            L = L <= up ? up : (L + kDecayMaxIck - 1) / kDecayMaxIck * kDecayMaxIck;
+            // cuts fall on checkpoints: one a segment up to 1024 tokens, then every 1024
+            const int64_t unit = L <= kDecayMaxIck ? kDecayChunk : kDecayMaxIck;
+            L = max(int64_t(plan.min_seg), (L + unit - 1) / unit * unit);
             seg_len = int(L);
             ick = min(seg_len, kDecayMaxIck);
         }

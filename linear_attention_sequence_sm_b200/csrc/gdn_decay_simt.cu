@@ -11,6 +11,7 @@
 #include <algorithm>
 
 #include "gdn_decay.cuh"
+#include "gdn_f32x2.cuh"
 
 namespace gdn {
 
@@ -40,28 +41,49 @@ inline size_t simt_smem(int dy, int dz, bool state_only) {
 
 // rows [0, L) of a [tokens, heads, d] tensor's head into a tile, the rest of
 // the 64 rows and of the columns up to a multiple of 8 zero
+// (read four at a time before any is stored: one trip's latency, not four)
 template <typename T>
-__device__ void load_tile(float *dst, int ld, const T *src, size_t stride, int d, int L, int dpad) {
+__device__ __forceinline__ void load_tile(float *__restrict__ dst, int ld, const T *__restrict__ src, size_t stride,
+                                          int d, int L, int dpad) {
+    constexpr int kBatch = 4;
     if (d % 4 == 0) {
-        const int n4 = dpad / 4;
-        for (int e = threadIdx.x; e < C * n4; e += kThreads) {
-            const int r = e / n4, c = 4 * (e % n4);
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < L && c < d) {
-                if constexpr (sizeof(T) == 4) {
-                    v = *reinterpret_cast<const float4 *>(src + r * stride + c);
-                } else {
-                    const uint2 u = *reinterpret_cast<const uint2 *>(src + r * stride + c);
-                    v = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                                    __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+        const int n4 = dpad / 4, total = C * n4;
+        for (int e0 = threadIdx.x; e0 < total; e0 += kBatch * kThreads) {
+            float4 v[kBatch];
+            int at[kBatch];
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                const int e = e0 + b * kThreads, r = e / n4, c = 4 * (e - r * n4);
+                v[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+                at[b] = e < total ? r * ld + c : -1;
+                if (e < total && r < L && c < d) {
+                    if constexpr (sizeof(T) == 4) {
+                        v[b] = *reinterpret_cast<const float4 *>(src + r * stride + c);
+                    } else {
+                        const uint2 u = *reinterpret_cast<const uint2 *>(src + r * stride + c);
+                        v[b] = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                                           __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+                    }
                 }
             }
-            *reinterpret_cast<float4 *>(dst + r * ld + c) = v;
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b)
+                if (at[b] >= 0) *reinterpret_cast<float4 *>(dst + at[b]) = v[b];
         }
     } else {
-        for (int e = threadIdx.x; e < C * dpad; e += kThreads) {
-            const int r = e / dpad, c = e % dpad;
-            dst[r * ld + c] = (r < L && c < d) ? to_f32(src[r * stride + c]) : 0.f;
+        const int total = C * dpad;
+        for (int e0 = threadIdx.x; e0 < total; e0 += kBatch * kThreads) {
+            float v[kBatch];
+            int at[kBatch];
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                const int e = e0 + b * kThreads, r = e / dpad, c = e - r * dpad;
+                at[b] = e < total ? r * ld + c : -1;
+                v[b] = (e < total && r < L && c < d) ? to_f32(src[r * stride + c]) : 0.f;
+            }
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b)
+                if (at[b] >= 0) dst[at[b]] = v[b];
         }
     }
 }
@@ -92,19 +114,23 @@ __device__ void load_gates(SimtVec &sm, const float *g, size_t g_stride, int L, 
     }
 }
 
-__device__ __forceinline__ float dot4(const float4 &a, const float4 &b, float c) {
-    return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
+// Four floats as two pairs, and their product sums kept as a pair (even and
+// odd terms), added at the end.
+__device__ __forceinline__ ulonglong2 ld4(const float *p) { return *reinterpret_cast<const ulonglong2 *>(p); }
+__device__ __forceinline__ f32x2 dot4(const ulonglong2 &a, const ulonglong2 &b, f32x2 c) {
+    return fma2(a.x, b.x, fma2(a.y, b.y, c));
 }
-__device__ __forceinline__ float4 ld4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float sum_of(f32x2 x) { return lo_of(x) + hi_of(x); }
 
 // 4 x 4 tile of a 64 x 64 product of rows: acc[i][j] = a[r0 + 16 i] . b[c0 + 16 j]
-__device__ __forceinline__ void gram(float (&acc)[4][4], const float *a, const float *b, int ld, int r0, int c0, int d) {
+__device__ __forceinline__ void gram(float (&out)[4][4], const float *a, const float *b, int ld, int r0, int c0, int d) {
+    f32x2 acc[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+        for (int j = 0; j < 4; ++j) acc[i][j] = both(0.f);
     for (int k = 0; k < d; k += 4) {
-        float4 u[4], v[4];
+        ulonglong2 u[4], v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) u[i] = ld4(a + (r0 + 16 * i) * ld + k);
 #pragma unroll
@@ -114,6 +140,10 @@ __device__ __forceinline__ void gram(float (&acc)[4][4], const float *a, const f
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = dot4(u[i], v[j], acc[i][j]);
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) out[i][j] = sum_of(acc[i][j]);
 }
 
 template <typename T>
@@ -147,12 +177,20 @@ decay_pass_simt_kernel(const DecayPass a) {
         const float *src = own ? a.seg_state + (size_t(seg.slot) * hv + h) * 16384
                                : (a.s_in && first && !a.state_only) ? a.s_in + (size_t(seg.seq) * hv + h) * dz * dy : nullptr;
         __syncthreads();
-        for (int e = tid; e < dzp * dyp; e += kThreads) {
-            const int r = e / dyp, c = e % dyp;
-            float v = 0.f;
-            if (src && r < dz && c < dy)
-                v = own ? src[a.seg_trans ? c * 128 + r : r * 128 + c] : src[a.s_trans ? c * dz + r : r * dy + c];
-            tS[r * ly + c] = v;
+        for (int e0 = tid; e0 < dzp * dyp; e0 += 8 * kThreads) {
+            float v[8];
+            int at[8];
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+                const int e = e0 + b * kThreads, r = e / dyp, c = e - r * dyp;
+                at[b] = e < dzp * dyp ? r * ly + c : -1;
+                v[b] = 0.f;
+                if (src && at[b] >= 0 && r < dz && c < dy)
+                    v[b] = own ? src[a.seg_trans ? c * 128 + r : r * 128 + c] : src[a.s_trans ? c * dz + r : r * dy + c];
+            }
+#pragma unroll
+            for (int b = 0; b < 8; ++b)
+                if (at[b] >= 0) tS[at[b]] = v[b];
         }
         const int nch = (seg.len + C - 1) / C;
         float seg_sum = 0.f;
@@ -188,41 +226,60 @@ decay_pass_simt_kernel(const DecayPass a) {
                 // out rows 4 rg .. 4 rg + 3, columns cg + 16 q (the rows of Sigma a quarter-warp reads are then
                 // next to one another and fall into different banks)
                 float in[4][8], ex[4][8];
+                {
+                    f32x2 acc[4][8];
 #pragma unroll
-                for (int p = 0; p < 4; ++p)
+                    for (int p = 0; p < 4; ++p)
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) in[p][q] = ex[p][q] = 0.f;
-                for (int c = 0; c < C; c += 4) {
-                    float4 pr[4];
+                        for (int q = 0; q < 8; ++q) acc[p][q] = both(0.f);
+                    for (int c = 0; c < C; c += 4) {
+                        ulonglong2 pr[4];
 #pragma unroll
-                    for (int p = 0; p < 4; ++p) pr[p] = ld4(tp + (4 * rg + p) * LP + c);
+                        for (int p = 0; p < 4; ++p) pr[p] = ld4(tp + (4 * rg + p) * LP + c);
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        if (16 * q >= dzp) break;
-                        const float *zc = tz + c * lz + cg + 16 * q;  // (past dz: the row's padding, not used)
-                        const float4 zv = make_float4(zc[0], zc[lz], zc[2 * lz], zc[3 * lz]);
+                        for (int q = 0; q < 8; ++q) {
+                            if (16 * q >= dzp) break;
+                            const float *zc = tz + c * lz + cg + 16 * q;  // (past dz: the row's padding, not used)
+                            const ulonglong2 zv = make_ulonglong2(pair(zc[0], zc[lz]), pair(zc[2 * lz], zc[3 * lz]));
 #pragma unroll
-                        for (int p = 0; p < 4; ++p) in[p][q] = dot4(pr[p], zv, in[p][q]);
+                            for (int p = 0; p < 4; ++p) acc[p][q] = dot4(pr[p], zv, acc[p][q]);
+                        }
                     }
-                }
-                for (int k = 0; k < dyp; k += 4) {
-                    float4 xr[4];
 #pragma unroll
-                    for (int p = 0; p < 4; ++p) xr[p] = ld4(tx + (4 * rg + p) * ly + k);
+                    for (int p = 0; p < 4; ++p)
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        if (16 * q >= dzp) break;
-                        const float4 s = ld4(tS + min(cg + 16 * q, dzp - 1) * ly + k);
+                        for (int q = 0; q < 8; ++q) {
+                            in[p][q] = sum_of(acc[p][q]);
+                            acc[p][q] = both(0.f);
+                        }
+                    for (int k = 0; k < dyp; k += 4) {
+                        ulonglong2 xr[4];
 #pragma unroll
-                        for (int p = 0; p < 4; ++p) ex[p][q] = dot4(xr[p], s, ex[p][q]);
+                        for (int p = 0; p < 4; ++p) xr[p] = ld4(tx + (4 * rg + p) * ly + k);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            if (16 * q >= dzp) break;
+                            const ulonglong2 s = ld4(tS + min(cg + 16 * q, dzp - 1) * ly + k);
+#pragma unroll
+                            for (int p = 0; p < 4; ++p) acc[p][q] = dot4(xr[p], s, acc[p][q]);
+                        }
                     }
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) ex[p][q] = sum_of(acc[p][q]);
                 }
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
                     const int r = 4 * rg + p;
                     const float w = sm.w_in[r];
                     const size_t row = size_t(seg.start + t0 + r);
-                    float dot = 0.f;
+                    float dot = 0.f, av[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const int c = cg + 16 * q;
+                        av[q] = aux && r < L && c < dz ? to_f32(aux[(size_t(t0) + r) * a.haux * dz + c]) : 0.f;
+                    }
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
                         const int c = cg + 16 * q;
@@ -231,7 +288,7 @@ decay_pass_simt_kernel(const DecayPass a) {
                             const size_t at = (row * hv + h) * dz + c;
                             if (a.out_f32) static_cast<float *>(a.out)[at] = in[p][q] + e;
                             else static_cast<T *>(a.out)[at] = from_f32<T>(in[p][q] + e);
-                            if (aux) dot = fmaf(to_f32(aux[(size_t(t0) + r) * a.haux * dz + c]), e, dot);
+                            dot = fmaf(av[q], e, dot);
                         }
                     }
                     if (aux) {
@@ -245,27 +302,29 @@ decay_pass_simt_kernel(const DecayPass a) {
             // Sigma = gamma Sigma + z^T (w y): z rows 4 rg (and 64 +), y columns 4 cg (and 64 +)
             for (int zb = 4 * rg; zb < dzp; zb += 64)
                 for (int yb = 4 * cg; yb < dyp; yb += 64) {
-                    float acc[4][4];
+                    f32x2 acc[4][2];
+                    const f32x2 gamma = both(sm.gamma);
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
-                        const float4 s = ld4(tS + (zb + p) * ly + yb);
-                        acc[p][0] = sm.gamma * s.x; acc[p][1] = sm.gamma * s.y;
-                        acc[p][2] = sm.gamma * s.z; acc[p][3] = sm.gamma * s.w;
+                        const ulonglong2 s = ld4(tS + (zb + p) * ly + yb);
+                        acc[p][0] = mul2(gamma, s.x);
+                        acc[p][1] = mul2(gamma, s.y);
                     }
+#pragma unroll 2
                     for (int c = 0; c < L; ++c) {
-                        const float w = sm.w_st[c];
-                        const float4 zv = ld4(tz + c * lz + zb), yv = ld4(ty + c * ly + yb);
-                        const float zw[4] = {w * zv.x, w * zv.y, w * zv.z, w * zv.w};
+                        const f32x2 w = both(sm.w_st[c]);
+                        const ulonglong2 zv = ld4(tz + c * lz + zb), yv = ld4(ty + c * ly + yb);
+                        const f32x2 z01 = mul2(w, zv.x), z23 = mul2(w, zv.y);
+                        const f32x2 zw[4] = {both(lo_of(z01)), both(hi_of(z01)), both(lo_of(z23)), both(hi_of(z23))};
 #pragma unroll
                         for (int p = 0; p < 4; ++p) {
-                            acc[p][0] = fmaf(zw[p], yv.x, acc[p][0]); acc[p][1] = fmaf(zw[p], yv.y, acc[p][1]);
-                            acc[p][2] = fmaf(zw[p], yv.z, acc[p][2]); acc[p][3] = fmaf(zw[p], yv.w, acc[p][3]);
+                            acc[p][0] = fma2(zw[p], yv.x, acc[p][0]);
+                            acc[p][1] = fma2(zw[p], yv.y, acc[p][1]);
                         }
                     }
 #pragma unroll
                     for (int p = 0; p < 4; ++p)
-                        *reinterpret_cast<float4 *>(tS + (zb + p) * ly + yb) =
-                            make_float4(acc[p][0], acc[p][1], acc[p][2], acc[p][3]);
+                        *reinterpret_cast<ulonglong2 *>(tS + (zb + p) * ly + yb) = make_ulonglong2(acc[p][0], acc[p][1]);
                 }
             if (a.zsum && (seg.pos + t0) % hdr->ick == 0) {
                 // <Sigma, checkpoint> at the chunk's start
