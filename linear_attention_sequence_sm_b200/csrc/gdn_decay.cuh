@@ -57,9 +57,8 @@ struct DecaySeg {
 // Header of the workspace (shares its status word with the other operators').
 struct DecayHeader {
     int32_t status, bad_index;
-    uint32_t next_unit[6];  // work counters of up to six persistent launches
     int32_t num_segs, num_split, ick, seg_len, num_cks, total_chunks;
-    int32_t pad[50];
+    int32_t pad[56];
 };
 static_assert(sizeof(DecayHeader) == 256, "header must be 256 bytes");
 
@@ -76,7 +75,7 @@ struct DecaySched {
 struct DecayLayout {
     size_t segs_off, split_off, cbase_off, ckbase_off, order_off;
     size_t state_off[2];    // start states of cut sequences, [slots][Hv][128][128] fp32 (backward: two directions)
-    size_t segdec_off;      // [slots][Hv] decay across each segment
+    size_t segdec_off[2];   // [slots][Hv] decay across each segment (each direction writes its own)
     size_t ckpt_off, zsum_off, dot_off[2], intra_off, part_off[2], dgtok_off;
     size_t total;
     int64_t max_segs, max_split, max_slots, max_cks, max_chunks;
@@ -104,7 +103,6 @@ struct DecayPass {
     float *ckpt;                  // [cks][hv][128 * 128], or NULL
     float *zsum;                  // backward in time: <Sigma, checkpoint>, [cks][hv][8 parts]; NULL: write checkpoints
     const float *s_first;         // the checkpoint at a sequence's start, stored as s_in, or NULL for zeros
-    int32_t counter;              // which work counter
     DecaySched sched;
 };
 
@@ -117,9 +115,11 @@ cudaError_t launch_decay_combine(const gdn_shape_t &s, const DecayLayout &L, con
                                  const float *seg_dec, const float *s_in, bool s_trans, int dz, int dy, bool reverse,
                                  cudaStream_t stream);
 
-// The pass on CUDA cores (fp32 or bf16 storage, any d <= 128), and on the
-// tensor cores (bf16, d a multiple of 8).
-cudaError_t launch_decay_pass_simt(const DecayPass &p, int32_t dtype, int64_t max_units, cudaStream_t stream);
+// The pass on CUDA cores (fp32 or bf16 storage, any d <= 128; with `also`, two
+// independent passes in one launch), and on the tensor cores (bf16, d a
+// multiple of 8).
+cudaError_t launch_decay_pass_simt(const DecayPass &p, const DecayPass *also, int32_t dtype, int64_t max_units,
+                                   cudaStream_t stream);
 bool decay_tc_supported(const gdn_shape_t &s);
 cudaError_t launch_decay_pass_tc(const DecayPass &p, int64_t max_units, cudaStream_t stream);
 

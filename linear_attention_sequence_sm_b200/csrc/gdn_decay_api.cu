@@ -56,12 +56,16 @@ gdn_status_t check_gate_layout(int32_t g_layout) {
     return GDN_OK;
 }
 
-cudaError_t run_pass(const DecayPass &p, const gdn_shape_t &s, int64_t max_units, cudaStream_t stream) {
+cudaError_t run_pass(const DecayPass &p, const gdn_shape_t &s, int64_t max_units, cudaStream_t stream,
+                     const DecayPass *also = nullptr) {
     int major = 0;
     device_sm_count(&major);
     // the tensor-core form where it applies (bf16, head sizes multiples of 8)
-    if (major == 10 && decay_tc_supported(s)) return launch_decay_pass_tc(p, max_units, stream);
-    return launch_decay_pass_simt(p, s.dtype, max_units, stream);
+    if (major == 10 && decay_tc_supported(s)) {
+        const cudaError_t e = launch_decay_pass_tc(p, max_units, stream);
+        return e == cudaSuccess && also ? launch_decay_pass_tc(*also, max_units, stream) : e;
+    }
+    return launch_decay_pass_simt(p, also, s.dtype, max_units, stream);
 }
 
 DecayPass pass_of(const gdn_shape_t &s, const DecaySched &sc, const float *g, int32_t g_layout) {
@@ -123,13 +127,13 @@ gdn_status_t gdn_decay_forward(const gdn_shape_t *s, const void *q, const void *
     p.dy = s->head_dim_k;
     p.dz = s->head_dim_v;
     p.s_in = initial_state;
-    float *states = reinterpret_cast<float *>(ws + L.state_off[0]), *dec = reinterpret_cast<float *>(ws + L.segdec_off);
+    float *states = reinterpret_cast<float *>(ws + L.state_off[0]);
+    float *dec = reinterpret_cast<float *>(ws + L.segdec_off[0]);
     if (L.max_slots > 0) {
         DecayPass w = p;
         w.state_only = 1;
         w.seg_local = states;
         w.seg_dec = dec;
-        w.counter = 1;
         e = run_pass(w, *s, L.max_slots * s->num_v_heads, stream);
         if (e != cudaSuccess) return cuda_fail(e, "segment state launch");
         e = launch_decay_combine(*s, L, sc, states, dec, initial_state, false, p.dz, p.dy, false, stream);
@@ -241,17 +245,16 @@ gdn_status_t gdn_decay_backward(const gdn_shape_t *s, const void *q, const void 
     pk.s_in = d_final_state;
     pk.s_trans = 1;
     if (L.max_slots > 0) {
+        DecayPass w[2] = {pq, pk};
         for (int i = 0; i < 2; ++i) {
-            DecayPass w = i ? pk : pq;
-            w.state_only = 1;
-            w.seg_local = at(L.state_off[i]);
-            w.seg_dec = at(L.segdec_off);
-            w.counter = 1 + i;
-            e = run_pass(w, *s, L.max_slots * hv, stream);
-            if (e == cudaSuccess)
-                e = launch_decay_combine(*s, L, sc, w.seg_local, w.seg_dec, w.s_in, true, d_k, d_v, i == 1, stream);
-            if (e != cudaSuccess) return cuda_fail(e, "segment state launch");
+            w[i].state_only = 1;
+            w[i].seg_local = at(L.state_off[i]);
+            w[i].seg_dec = at(L.segdec_off[i]);
         }
+        e = run_pass(w[0], *s, L.max_slots * hv, stream, &w[1]);
+        for (int i = 0; i < 2 && e == cudaSuccess; ++i)
+            e = launch_decay_combine(*s, L, sc, w[i].seg_local, w[i].seg_dec, w[i].s_in, true, d_k, d_v, i == 1, stream);
+        if (e != cudaSuccess) return cuda_fail(e, "segment state launch");
     }
     const int64_t units = L.max_segs * hv;
     pq.seg_state = at(L.state_off[0]);
@@ -269,8 +272,6 @@ gdn_status_t gdn_decay_backward(const gdn_shape_t *s, const void *q, const void 
         pk.ckpt = at(L.ckpt_off);
         pk.zsum = at(L.zsum_off);
     }
-    pq.counter = 3;
-    pk.counter = 4;
     // dv: out_t = dS_t k_t, backward in time
     DecayPass pv = base;
     pv.reverse = 1;
@@ -283,9 +284,8 @@ gdn_status_t gdn_decay_backward(const gdn_shape_t *s, const void *q, const void 
     pv.seg_state = at(L.state_off[1]);
     pv.seg_trans = 1;
     pv.out = dv;
-    pv.counter = 5;
-    if ((e = run_pass(pq, *s, units, stream)) != cudaSuccess || (e = run_pass(pk, *s, units, stream)) != cudaSuccess ||
-        (e = run_pass(pv, *s, units, stream)) != cudaSuccess)
+    // (dk's decay sums read the checkpoints that dq's pass writes)
+    if ((e = run_pass(pq, *s, units, stream, &pv)) != cudaSuccess || (e = run_pass(pk, *s, units, stream)) != cudaSuccess)
         return cuda_fail(e, "backward launch");
     if (tokens == 0) return GDN_OK;
     if (dg) {

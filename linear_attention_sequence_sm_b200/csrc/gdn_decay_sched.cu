@@ -90,7 +90,6 @@ decay_schedule_kernel(int32_t num_seqs, int32_t tokens, int32_t batched_len, int
         longest = 0;
         hdr->status = GDN_OK;
         hdr->bad_index = -1;
-        for (int i = 0; i < 6; ++i) hdr->next_unit[i] = 0;
         hdr->num_segs = hdr->num_split = hdr->num_cks = hdr->total_chunks = 0;
         hdr->ick = kDecayMaxIck;
         hdr->seg_len = 0;
@@ -394,9 +393,10 @@ DecayLayout decay_layout(const gdn_shape_t &s, bool backward) {
     L.order_off = take(size_t(N) * 4);
     L.cbase_off = take(size_t(N + 1) * 4);
     L.ckbase_off = take(size_t(N + 1) * 4);
-    L.segdec_off = take(size_t(L.max_slots) * hv * 4);
+    L.segdec_off[0] = take(size_t(L.max_slots) * hv * 4);
     L.state_off[0] = take(size_t(L.max_slots) * hv * 65536);
     if (backward) {
+        L.segdec_off[1] = take(size_t(L.max_slots) * hv * 4);
         L.state_off[1] = take(size_t(L.max_slots) * hv * 65536);
         L.ckpt_off = take(size_t(L.max_cks) * hv * 65536);
         L.zsum_off = take(size_t(L.max_cks) * hv * 32);

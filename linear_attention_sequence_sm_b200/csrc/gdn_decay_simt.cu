@@ -148,7 +148,8 @@ __device__ __forceinline__ void gram(float (&out)[4][4], const float *a, const f
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2)
-decay_pass_simt_kernel(const DecayPass a) {
+decay_pass_simt_kernel(const __grid_constant__ DecayPass a0, const __grid_constant__ DecayPass a1) {
+    const DecayPass &a = blockIdx.y ? a1 : a0;  // two passes that do not wait for one another share a launch
     extern __shared__ __align__(16) unsigned char smem_raw[];
     SimtVec &sm = *reinterpret_cast<SimtVec *>(smem_raw);
     const DecayHeader *hdr = a.sched.hdr;
@@ -460,16 +461,18 @@ decay_intra_simt_kernel(const DecaySched sc, int num_seqs, int hk, int hv, int d
 
 }  // namespace
 
-cudaError_t launch_decay_pass_simt(const DecayPass &p, int32_t dtype, int64_t max_units, cudaStream_t stream) {
+cudaError_t launch_decay_pass_simt(const DecayPass &p, const DecayPass *also, int32_t dtype, int64_t max_units,
+                                   cudaStream_t stream) {
     if (max_units <= 0) return cudaSuccess;
     const void *kern = dtype == GDN_DTYPE_BF16 ? reinterpret_cast<const void *>(decay_pass_simt_kernel<__nv_bfloat16>)
                                                : reinterpret_cast<const void *>(decay_pass_simt_kernel<float>);
-    const size_t bytes = simt_smem(p.dy, p.dz, p.state_only);
+    const size_t bytes = std::max(simt_smem(p.dy, p.dz, p.state_only),
+                                  also ? simt_smem(also->dy, also->dz, also->state_only) : 0);
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
     if (e != cudaSuccess) return e;
-    const unsigned grid = unsigned(std::min<int64_t>(max_units, kDecayPlanSms * 8));
-    if (dtype == GDN_DTYPE_BF16) decay_pass_simt_kernel<__nv_bfloat16><<<grid, kThreads, bytes, stream>>>(p);
-    else decay_pass_simt_kernel<float><<<grid, kThreads, bytes, stream>>>(p);
+    const dim3 grid(unsigned(std::min<int64_t>(max_units, kDecayPlanSms * 8)), also ? 2 : 1);
+    if (dtype == GDN_DTYPE_BF16) decay_pass_simt_kernel<__nv_bfloat16><<<grid, kThreads, bytes, stream>>>(p, also ? *also : p);
+    else decay_pass_simt_kernel<float><<<grid, kThreads, bytes, stream>>>(p, also ? *also : p);
     count_launch();
     return cudaGetLastError();
 }
