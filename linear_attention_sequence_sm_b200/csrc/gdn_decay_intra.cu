@@ -33,7 +33,7 @@ constexpr int kThreads = 128;
 constexpr uint32_t kTile = C * 256;  // 64 rows of up to 128 bf16, 16-byte pieces swizzled by the row
 
 struct IntraVec {
-    float hi[C], lo[C];  // prefix sums of the log-decays in log2 units, as a sum of two floats
+    float hi[2][C], lo[2][C];  // prefix sums of the log-decays in log2 units, as a sum of two floats (two heads)
     float part[4][C];
 };
 constexpr uint32_t kSmem = 4 * kTile + sizeof(IntraVec);
@@ -43,6 +43,11 @@ __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr)
                  : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {  // within 2^-22
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -55,9 +60,10 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 // Rows [0, L) of a head into a swizzled tile by 16-byte asynchronous copies;
 // the other rows, and columns past d up to dpad, zero.
 __device__ __forceinline__ void tile_in(uint32_t dst, const __nv_bfloat16 *src, size_t stride, int d, int dpad, int L) {
-    const int pieces = dpad / 8;
-    for (int e = threadIdx.x; e < C * pieces; e += kThreads) {
-        const int r = e / pieces, c = e % pieces;
+    const int pieces = dpad / 8, c = threadIdx.x & 15;
+    if (c >= pieces) return;
+#pragma unroll
+    for (int r = threadIdx.x >> 4; r < C; r += kThreads / 16) {
         const bool in = r < L && 8 * c < d;
         const uint32_t at = dst + uint32_t(r) * 256 + (uint32_t(c ^ (r & 7)) << 4);
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(src + (in ? r * stride + 8 * c : 0)),
@@ -109,14 +115,13 @@ decay_intra_kernel(const DecaySched sc, int num_seqs, int hk, int hv, int dk, in
         const int t0 = (gc - sc.chunk_base[n]) * C, L = min(C, len - t0);
         const size_t tok = size_t(start) + t0;
         __syncthreads();  // the previous unit's tiles have been read
-        tile_in(sb, q + (tok * hk + hq) * dk, size_t(hk) * dk, dk, dkp, L);
-        tile_in(sb + kTile, k + (tok * hk + hq) * dk, size_t(hk) * dk, dk, dkp, L);
-        float A[8][4];
-        for (int j = 0; j < group; ++j) {
+        // v and do of the j-th head of the group: tiles 2 and 3, then (q and k have been used) 0 and 1, in turn
+        auto head_in = [&](int j) {
             const int h = hq * group + j;
-            if (j > 0) __syncthreads();
-            tile_in(sb + 2 * kTile, v + (tok * hv + h) * dv, size_t(hv) * dv, dv, dvp, L);
-            tile_in(sb + 3 * kTile, d_o + (tok * hv + h) * dv, size_t(hv) * dv, dv, dvp, L);
+            const uint32_t at = sb + ((j & 1) ? 0u : 2 * kTile);
+            tile_in(at, v + (tok * hv + h) * dv, size_t(hv) * dv, dv, dvp, L);
+            tile_in(at + kTile, d_o + (tok * hv + h) * dv, size_t(hv) * dv, dv, dvp, L);
+            asm volatile("cp.async.commit_group;" ::: "memory");
             if (warp == 0) {
                 const float *gp = g_const ? g + h : g + tok * hv + h;
                 const size_t gs = g_const ? 0 : hv;
@@ -131,14 +136,26 @@ decay_intra_kernel(const DecaySched sc, int num_seqs, int hk, int hv, int dk, in
                 constexpr double kLog2e = 1.4426950408889634;
                 const double G0 = (s - double(g1)) * kLog2e, G1 = s * kLog2e;
                 const float h0 = float(G0), h1 = float(G1);
-                *reinterpret_cast<float2 *>(sm.hi + 2 * lane) = make_float2(h0, h1);
-                *reinterpret_cast<float2 *>(sm.lo + 2 * lane) = make_float2(float(G0 - h0), float(G1 - h1));
+                *reinterpret_cast<float2 *>(sm.hi[j & 1] + 2 * lane) = make_float2(h0, h1);
+                *reinterpret_cast<float2 *>(sm.lo[j & 1] + 2 * lane) = make_float2(float(G0 - h0), float(G1 - h1));
             }
-            asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-            __syncthreads();
-            if (j == 0) gram(A, sb, sb + kTile, dkp, warp, lane, tiles);
+        };
+        tile_in(sb, q + (tok * hk + hq) * dk, size_t(hk) * dk, dk, dkp, L);
+        tile_in(sb + kTile, k + (tok * hk + hq) * dk, size_t(hk) * dk, dk, dkp, L);
+        head_in(0);
+        float A[8][4];
+        for (int j = 0; j < group; ++j) {
+            const int h = hq * group + j;
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncthreads();  // this head's tiles are here, and the one before has been read
+            if (j == 0) {
+                gram(A, sb, sb + kTile, dkp, warp, lane, tiles);
+                if (group > 1) __syncthreads();  // q and k have been read
+            }
+            if (j + 1 < group) head_in(j + 1);
             float W[8][4];
-            gram(W, sb + 3 * kTile, sb + 2 * kTile, dvp, warp, lane, tiles);
+            const uint32_t at = sb + ((j & 1) ? 0u : 2 * kTile);
+            gram(W, at + kTile, at, dvp, warp, lane, tiles);
             // rows of this thread: i = 16 warp + lane / 4 (and + 8); columns 8 n + 2 (lane % 4) (and the next)
             const int i0 = 16 * warp + (lane >> 2), c0 = 2 * (lane & 3);
             float X[16];  // column sums of this thread's rows
@@ -147,16 +164,16 @@ decay_intra_kernel(const DecaySched sc, int num_seqs, int hk, int hv, int dk, in
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const int i = i0 + 8 * r;
-                const float Ghi = sm.hi[i], Glo = sm.lo[i];
+                const float Ghi = sm.hi[j & 1][i], Glo = sm.lo[j & 1][i];
                 float base = 0.f;
 #pragma unroll
                 for (int m = 0; m < 8; ++m) {
                     if (m >= tiles) break;
-                    const float2 hi = *reinterpret_cast<const float2 *>(sm.hi + 8 * m + c0);
-                    const float2 lo = *reinterpret_cast<const float2 *>(sm.lo + 8 * m + c0);
+                    const float2 hi = *reinterpret_cast<const float2 *>(sm.hi[j & 1] + 8 * m + c0);
+                    const float2 lo = *reinterpret_cast<const float2 *>(sm.lo[j & 1] + 8 * m + c0);
                     const int c = 8 * m + c0;
-                    const float w0 = c < i ? W[m][2 * r] * A[m][2 * r] * exp2f((Ghi - hi.x) + (Glo - lo.x)) : 0.f;
-                    const float w1 = c + 1 < i ? W[m][2 * r + 1] * A[m][2 * r + 1] * exp2f((Ghi - hi.y) + (Glo - lo.y)) : 0.f;
+                    const float w0 = c < i ? W[m][2 * r] * A[m][2 * r] * ex2((Ghi - hi.x) + (Glo - lo.x)) : 0.f;
+                    const float w1 = c + 1 < i ? W[m][2 * r + 1] * A[m][2 * r + 1] * ex2((Ghi - hi.y) + (Glo - lo.y)) : 0.f;
                     float s = w0 + w1;
                     const float a = __shfl_up_sync(0xffffffffu, s, 1, 4);
                     if ((lane & 3) >= 1) s += a;
