@@ -91,7 +91,7 @@ template <int kKind> struct Cfg {
     static constexpr uint32_t kOffVec = kOffOut + 8 * kStage;                           // [4]
     static constexpr uint32_t kOffRed = kOffVec + 4 * kVecFloats * 4;              // [4 warps][64]
     static constexpr uint32_t kOffBar = kOffRed + 1024;
-    static constexpr uint32_t kSmem = kOffBar + 432 + 1024;
+    static constexpr uint32_t kSmem = kOffBar + 448 + 1024;
     static_assert(kSmem <= 232448, "shared memory over the sm_100 per-block limit");
     // tensor memory columns
     // L (two for the state alone); quarters of w z (8 columns a term); the copies of Sigma (64 columns a term);
@@ -134,8 +134,9 @@ enum {
     kBOutFree = 43, // X1, X2 read (8 out warps)
     kBVec = 44,     // [4] token vectors written
     kBVecFree = 48, // [4] token vectors read (8 state warps, 8 out warps)
-    kBDrain = 52,
-    kNumBars = 53
+    kBX2Free = 52,  // X2 read (8 out warps; where QK needs its columns)
+    kBDrain = 53,
+    kNumBars = 54
 };
 
 struct Maps {
@@ -228,6 +229,12 @@ __device__ __forceinline__ void tmem_st_frag(uint32_t taddr, uint32_t a, uint32_
 }
 // x minus the two bf16 values of w (exact where w is x rounded).
 __device__ __forceinline__ f32x2 sub_bf16x2(f32x2 x, uint32_t w) { return fma2(from_bf16x2(w), both(-1.f), x); }
+// 8 consecutive 32-bit columns of this thread's lane, written (raw bits).
+__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 // Four 8 x 8 tiles of 16-bit values, transposed on the way: lane l gives the
 // address of row l % 8 of tile l / 8, and holds elements (row 2 (l % 4) and
 // the next, column l / 4) of each tile.
@@ -266,7 +273,8 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
         for (int i = 0; i < kNumBars; ++i) {
             int n = 1;
             if ((i >= kBW && i < kBW + 4) || i == kBP || i == kBP + 1) n = 4;
-            if (i == kBSt || i == kBLFree || i == kBLFree + 1 || i == kBOutFree || i == kBAFree || i == kBAFree + 1)
+            if (i == kBSt || i == kBLFree || i == kBLFree + 1 || i == kBOutFree || i == kBX2Free || i == kBAFree ||
+                i == kBAFree + 1)
                 n = 8;
             if (i == kBOut || i == kBKV || i == kBKV + 1) n = 2;
             if (i >= kBZFree && i < kBZFree + kRing) n = kSt ? 8 : 9;  // (each split warp once a chunk)
@@ -346,23 +354,23 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                     if (mine) {
                         const uint32_t ca = trow + K::kColC + uint32_t(c0 / 2);
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            uint32_t pk[16];
+                        for (int q = 0; q < 4; ++q) {  // 16 columns
+                            uint32_t pk[8];
+                            f32x2 r[8];
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(S[32 * q + 2 * j], S[32 * q + 2 * j + 1]);
-                            tmem_st16u(ca + 16 * q, pk);
-                            if constexpr (K::kCopies == 3) {
-                                float r[32];
+                            for (int j = 0; j < 8; ++j) {
+                                r[j] = pair(S[16 * q + 2 * j], S[16 * q + 2 * j + 1]);
+                                pk[j] = to_bf16x2(r[j]);
+                            }
+                            tmem_st8u(ca + 8 * q, pk);
 #pragma unroll
-                                for (int t = 1; t < 3; ++t) {
+                            for (int t = 1; t < K::kCopies; ++t) {
 #pragma unroll
-                                    for (int j = 0; j < 16; ++j) {
-                                        r[2 * j] = (t == 1 ? S[32 * q + 2 * j] : r[2 * j]) - bf_lo(pk[j]);
-                                        r[2 * j + 1] = (t == 1 ? S[32 * q + 2 * j + 1] : r[2 * j + 1]) - bf_hi(pk[j]);
-                                        pk[j] = pack_bf16x2(r[2 * j], r[2 * j + 1]);
-                                    }
-                                    tmem_st16u(ca + 64 * t + 16 * q, pk);
+                                for (int j = 0; j < 8; ++j) {
+                                    r[j] = sub_bf16x2(r[j], pk[j]);
+                                    pk[j] = to_bf16x2(r[j]);
                                 }
+                                tmem_st8u(ca + 64 * t + 8 * q, pk);
                             }
                         }
                         tmem_wait_st();
@@ -472,14 +480,32 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                     const size_t tok = size_t(w.seg.start) + t0;
                     const size_t step = size_t(hv) * dz;
                     const size_t at = (tok * hv + w.h) * dz + 32 * quarter;
-#pragma unroll 1
+                    float y2[kDots ? 2 : 1][2][8];
+                    if constexpr (kDots) {
+                        // X2 first: QK waits for its columns
+#pragma unroll
+                        for (int pp = 0; pp < 2; ++pp)
+#pragma unroll
+                            for (int l = 0; l < 2; ++l)
+                                tmem_ld_frag(tq + (uint32_t(16 * l) << 16) + K::col_x2(mm) + 16 * (2 * part + pp), y2[pp][l]);
+                        tmem_wait_ld();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(kBX2Free));
+                    }
+#pragma unroll(kDots ? 2 : 1)
                     for (int pp = 0; pp < 2; ++pp) {  // 16 tokens (rolled: the roles share the instruction caches)
                         const int p = 2 * part + pp;
                         float x1[2][8], x2[2][8];
 #pragma unroll
                         for (int l = 0; l < 2; ++l) {
                             tmem_ld_frag(tq + (uint32_t(16 * l) << 16) + K::kColX1 + 16 * p, x1[l]);
-                            tmem_ld_frag(tq + (uint32_t(16 * l) << 16) + K::col_x2(mm) + 16 * p, x2[l]);
+                            if constexpr (kDots) {
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) x2[l][e] = y2[pp][l][e];
+                            } else {
+                                tmem_ld_frag(tq + (uint32_t(16 * l) << 16) + K::col_x2(mm) + 16 * p, x2[l]);
+                            }
                         }
                         tmem_wait_ld();
                         if (pp == 1) {
@@ -848,7 +874,8 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
         auto issue_qk = [&](uint32_t c) {
             const uint32_t s = c % kRing, ph = (c / kRing) & 1u;
             if (!mbar_wait(bar(kBX + int(s)), ph) || !mbar_wait(bar(kBY + int(s)), ph)) return false;
-            if (c >= uint32_t(K::kBufs) && !out_read(c - K::kBufs)) return false;
+            // (its columns were the X2 of kBufs chunks ago)
+            if (kDots ? c > 0 && !mbar_wait(bar(kBX2Free), (c - 1) & 1u) : c > 1 && !out_read(c - 2)) return false;
             tc_fence_after();
             const uint64_t dx = smem_desc(sb + K::kOffX + s * kTile, 16, 1024), dyd = smem_desc(sb + K::kOffY + s * kTile, 16, 1024);
 #pragma unroll 1
