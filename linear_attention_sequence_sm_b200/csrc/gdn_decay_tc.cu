@@ -31,7 +31,7 @@
 // until the products set the pace):
 //   0-7     state      two warps per tensor-memory quarter, 64 columns each
 //   8-15    out        X1, X2 -> out (and the dot with aux), 32 tokens a warpgroup
-//   16-23   split      w z in three terms, 16 tokens at a time, the warpgroups in turn
+//   16-23   split      w z in three terms, 16 tokens at a time, the warpgroups in turn (8-23 where there is no out)
 //   24-27   mask       P from QK
 //   28 TMA loads, 29 issues X1, X2 and QK, 30 decays, 31 issues KV
 // The registers go where the state is (setmaxnreg).  A chunk's products are 32
@@ -118,7 +118,7 @@ enum {
     kBY = 6,        // [3] y
     kBA = 9,        // [2] aux
     kBXFree = 11,   // [3] X1 (and QK) of the slot's chunk done
-    kBZFree = 14,   // [3] X2 done, w z taken (8 split warps)
+    kBZFree = 14,   // [3] X2 done, w z taken (every split warp)
     kBYFree = 17,   // [3] KV done, QK done
     kBAFree = 20,   // [2] dot taken (8 out warps)
     kBW = 22,       // [4] a quarter of w z written (4 split warps)
@@ -277,7 +277,7 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                 i == kBAFree + 1)
                 n = 8;
             if (i == kBOut || i == kBKV || i == kBKV + 1) n = 2;
-            if (i >= kBZFree && i < kBZFree + kRing) n = kSt ? 8 : 9;  // (each split warp once a chunk)
+            if (i >= kBZFree && i < kBZFree + kRing) n = kSt ? 16 : 9;  // (each split warp once a chunk)
             if (i >= kBYFree && i < kBYFree + kRing) n = kSt ? 1 : 2;
             if (i == kBDrain) n = 2;
             if (i >= kBVecFree && i < kBVecFree + 4) n = kSt ? 8 : 16;
@@ -455,7 +455,7 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
             }
             m += uint32_t(w.nch);
         }
-    } else if (warp < kWarpSplit) {
+    } else if (!kSt && warp < kWarpSplit) {
         // ==================== out warps: 32 z rows each, read in fragments ====================
         regs_up<kRegsOut>();
         if constexpr (!kSt) {
@@ -635,7 +635,8 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
     } else if (warp < kWarpMask) {
         // ============ split warps: w z of 16 tokens, in three terms ============
         regs_down<kRegsWork>();
-        const int quarter = warp & 3, grp = (warp - kWarpSplit) >> 2, st = tid - 32 * kWarpSplit - 128 * grp;
+        constexpr int kGroups = kSt ? 4 : 2;  // warpgroups at it; quarter q of a chunk is the (q % kGroups)-th's
+        const int quarter = warp & 3, grp = ((warp - kWarpSplit) >> 2) & (kGroups - 1), st = tid & 127;
         const uint32_t tw = tmem + (uint32_t(quarter * 32) << 16) + K::kColW;
         const uint32_t ch = uint32_t(4 * (quarter & 1) + (lane >> 3)), r7 = uint32_t(lane & 7);
         const uint32_t src = uint32_t(quarter >> 1) * kAtom + r7 * 128 + ((ch ^ r7) << 4);
@@ -651,9 +652,10 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                     if (ok) ok = warp_wait(bar(kBY + int(s)), ring_phase);
                     const uint32_t yt = sb + K::kOffY + s * kTile;
                     for (int e = st; e < 256 * ya && ok; e += 128) {
-                        // pieces of 16 bytes: 8 a row, this group's 32 rows (its two quarters), column halves
-                        const int r = 16 * grp + ((e >> 3) & 15) + ((e >> 2) & 32);
-                        if (r >= L)
+                        // pieces of 16 bytes: 8 a row, 32 rows (two quarters, of which this group may have one), column
+                        // halves
+                        const int q = (e >> 7) & 1, r = 16 * (grp % 2 + 2 * q) + ((e >> 3) & 15);
+                        if (r >= L && (kGroups == 2 || q == grp / 2))
                             st_shared_v4(yt + uint32_t(e >> 8) * kAtom + uint32_t(r) * 128 + uint32_t(e & 7) * 16,
                                          make_uint4(0u, 0u, 0u, 0u));
                     }
@@ -668,9 +670,9 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                 const float *wst = vecs(mm) + kVecSt + 2 * (lane & 3);
                 const uint32_t zt = sb + K::kOffZ + s * kTile + src;
 #pragma unroll 1
-                for (int hf = 0; hf < 2; ++hf) {
-                    const int t16 = 16 * grp + 32 * hf;  // the quarter's first token
-                    const uint32_t qq = uint32_t(grp + 2 * hf), turn = K::qturn(mm, qq);
+                for (int hf = 0; hf < 4 / kGroups; ++hf) {
+                    const uint32_t qq = uint32_t(grp + kGroups * hf), turn = K::qturn(mm, qq);
+                    const int t16 = 16 * int(qq);  // the quarter's first token
                     uint32_t w0[2][4], w1[2][4], w2[2][4];  // two groups of 8 tokens; 8-row blocks of z
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
@@ -694,7 +696,7 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                             w2[j][i] = to_bf16x2(x);
                         }
                     }
-                    if (hf == 1 && lane == 0) mbar_arrive(bar(kBZFree + int(s)));  // (its last read of z)
+                    if (hf == 4 / kGroups - 1 && lane == 0) mbar_arrive(bar(kBZFree + int(s)));  // (its last read of z)
                     // KV has read these columns' previous quarter
                     if (turn > 0) ok = warp_wait(bar(kBKq + int(K::qbuf(qq))), (turn - 1) & 1u);
                     if (!ok) break;
