@@ -475,7 +475,8 @@ GDN_API gdn_status_t gdn_short_conv(int32_t num_seqs, int32_t seq_len, const int
  * ("Gated Attention Architectures", section 1: linear attention's state
  * and the decay-masked chunk output).  Layouts, groups of value heads, the
  * floor on g and the states are gdn_chunk_forward's; there is no beta and no
- * normalisation of q and k.  g has one of two layouts:
+ * normalisation of q and k.  (A NaN in g is not floored: the outputs of its
+ * head from that token on are NaN.)  g has one of two layouts:
  *   GDN_DECAY_PER_TOKEN   g [tokens, Hv] fp32 (decode: [N, Hv])
  *   GDN_DECAY_PER_HEAD    g [Hv] fp32, one decay a head for every token     */
 #define GDN_DECAY_PER_TOKEN 0
@@ -509,7 +510,7 @@ GDN_API gdn_status_t gdn_decay_forward(const gdn_shape_t *shape,
 
 /* One token for each of N sequences, state updated in place (one read and
  * one write of S).  Shapes as for gdn_decode_step; d_k <= 256.  out_side
- * (or NULL) is applied as a second pass over o. */
+ * (or NULL) is applied as a second pass over o, and needs d_v <= 128. */
 GDN_API gdn_status_t gdn_decay_decode_step(int32_t num_seqs, int32_t num_qk_heads, int32_t num_v_heads,
                                  int32_t head_dim_k, int32_t head_dim_v, int32_t dtype,
                                  const void *q, const void *k, const void *v,

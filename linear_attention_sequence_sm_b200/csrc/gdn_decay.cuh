@@ -44,6 +44,14 @@ constexpr int kDecayMinSeg = 256;    // shortest segment a split sequence is cut
 constexpr int kDecayMaxIck = 1024;   // checkpoint spacing of the decays' gradient (tokens)
 constexpr int kDecayPlanSms = 148;   // SMs the split aims to fill (B200)
 
+// A log-decay as the recurrence uses it.  A NaN stays one (fmaxf would make it
+// the floor, and the call would answer as if nothing were wrong).
+__device__ __forceinline__ float floored(float g) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(g), "f"(kGFloor));
+    return r;
+}
+
 // A segment: the tokens one CTA walks for one value head.  Sequences are cut
 // only where whole sequences would leave SMs idle (see decay_schedule_kernel).
 struct DecaySeg {
@@ -78,7 +86,7 @@ struct DecayLayout {
     size_t segdec_off[2];   // [slots][Hv] decay across each segment (each direction writes its own)
     size_t ckpt_off, zsum_off, dot_off[2], intra_off, part_off[2], dgtok_off;
     size_t total;
-    int64_t max_segs, max_split, max_slots, max_cks, max_chunks;
+    int64_t max_segs, max_split, max_slots, max_cks, max_ckpt, max_chunks;
 };
 DecayLayout decay_layout(const gdn_shape_t &s, bool backward);
 
@@ -100,7 +108,10 @@ struct DecayPass {
     void *out;                    // [tokens, hv, dz]
     int32_t out_f32;              // 32-bit out whatever the inputs' type
     float *dot;                   // [hv][tokens], or NULL
-    float *ckpt;                  // [cks][hv][128 * 128], or NULL
+    // States at positions p > 0 that are multiples of `ick`, or NULL: [tokens / ick + 1][hv][128 * 128], at slot
+    // (token / ick).  Two of them are at least ick tokens apart, whatever the sequences, so no slot is used twice;
+    // the state at p = 0 is s_first.
+    float *ckpt;
     float *zsum;                  // backward in time: <Sigma, checkpoint>, [cks][hv][8 parts]; NULL: write checkpoints
     const float *s_first;         // the checkpoint at a sequence's start, stored as s_in, or NULL for zeros
     DecaySched sched;

@@ -21,6 +21,8 @@ gdn_status_t check_decay_shape(const gdn_shape_t *s, const int32_t *cu_seqlens, 
         return fail(GDN_ERR_UNSUPPORTED, "the decayed linear attention uses chunks of %d tokens (got %d)", kDecayChunk,
                     s->chunk_size);
     if (s->num_v_heads > 65535) return fail(GDN_ERR_UNSUPPORTED, "more than 65535 value heads");
+    if (int64_t(s->batch) * s->seq_len > INT32_MAX - 2 * kDecayMaxIck)  // (positions past a sequence's end stay in 32 bits)
+        return fail(GDN_ERR_UNSUPPORTED, "more than 2^31 - %d tokens", 2 * kDecayMaxIck + 1);
     if (s->num_seqs > (1 << 24)) return fail(GDN_ERR_UNSUPPORTED, "more than 2^24 sequences");
     if (layout_known) {
         if (cu_seqlens) {
@@ -145,7 +147,7 @@ gdn_status_t gdn_decay_forward(const gdn_shape_t *s, const void *q, const void *
     e = run_pass(p, *s, L.max_segs * s->num_v_heads, stream);
     if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
     if (out.flags && tokens > 0) {
-        e = launch_output_side(o, int32_t(tokens), s->num_v_heads, s->head_dim_v, s->dtype, out, stream);
+        e = launch_output_side(o, int32_t(tokens), s->num_v_heads, s->head_dim_v, s->dtype, out, stream, &sc.hdr->status);
         if (e != cudaSuccess) return cuda_fail(e, "output-side launch");
     }
     return GDN_OK;
@@ -166,6 +168,8 @@ gdn_status_t gdn_decay_decode_step(int32_t n, int32_t hk, int32_t hv, int32_t dk
         return fail(GDN_ERR_INVALID_ARGUMENT, "dtype %d is not GDN_DTYPE_F32 or GDN_DTYPE_BF16", dtype);
     if (dk > 256) return fail(GDN_ERR_UNSUPPORTED, "decode supports d_k <= 256 (got %d)", dk);
     if (dv > (1 << 20)) return fail(GDN_ERR_UNSUPPORTED, "decode supports d_v <= 2^20 (got %d)", dv);
+    if (out.flags && dv > 128)
+        return fail(GDN_ERR_UNSUPPORTED, "decode with an output side supports d_v <= 128 (got %d)", dv);
     if (n == 0) return GDN_OK;
     const void *ptrs[] = {q, k, v, g, state, o};
     const char *names[] = {"q", "k", "v", "g", "state", "o"};
@@ -377,6 +381,7 @@ gdn_status_t gdn_block_norm_forward(int64_t rows, int32_t width, int32_t dtype, 
     const bool pre = norm->flags & GDN_BLOCK_PRE_NORM;
     if (pre != (y != nullptr) && rows > 0)
         return fail(GDN_ERR_INVALID_ARGUMENT, "y goes with GDN_BLOCK_PRE_NORM and only with it");
+    if (h && h == y) return fail(GDN_ERR_INVALID_ARGUMENT, "h and y are the same buffer");
     if (!h && !y && rows > 0) return fail(GDN_ERR_INVALID_ARGUMENT, "neither h nor y is wanted");
     const void *ptrs[] = {h, y};
     const char *names[] = {"h", "y"};

@@ -58,7 +58,7 @@ decay_decode_kernel(int hk, int hv, int dk, int dv, int rows_per_block, const T 
             for (int j = 0; j < 4; ++j) kf[e][j] = qf[e][j] = 0.f;
         }
     }
-    const float alpha = expf(fmaxf(g[g_const ? h : unit], kGFloor));
+    const float alpha = expf(floored(g[g_const ? h : unit]));
     for (int i0 = row0 + grp * kRows; i0 - grp * kRows < row1; i0 += kGroups * kRows) {
         float4 s[kRows][kV];
 #pragma unroll
@@ -112,7 +112,7 @@ decay_decode_any_kernel(int hk, int hv, int dk, int dv, int rows_per_block, cons
         kf[e] = c < dk ? to_f32(k[hq * dk + c]) : 0.f;
         qf[e] = c < dk ? to_f32(q[hq * dk + c]) : 0.f;
     }
-    const float alpha = expf(fmaxf(g[g_const ? h : unit], kGFloor));
+    const float alpha = expf(floored(g[g_const ? h : unit]));
     for (int i = row0 + warp; i < row1; i += kWarps) {
         float *S = state + (size_t(unit) * dv + i) * dk;
         const float vv = to_f32(v[size_t(unit) * dv + i]);

@@ -125,8 +125,8 @@ decay_intra_kernel(const DecaySched sc, int num_seqs, int hk, int hv, int dk, in
             if (warp == 0) {
                 const float *gp = g_const ? g + h : g + tok * hv + h;
                 const size_t gs = g_const ? 0 : hv;
-                const float g0 = 2 * lane < L ? fmaxf(gp[(2 * lane) * gs], kGFloor) : 0.f;
-                const float g1 = 2 * lane + 1 < L ? fmaxf(gp[(2 * lane + 1) * gs], kGFloor) : 0.f;
+                const float g0 = 2 * lane < L ? floored(gp[(2 * lane) * gs]) : 0.f;
+                const float g1 = 2 * lane + 1 < L ? floored(gp[(2 * lane + 1) * gs]) : 0.f;
                 double s = double(g0) + double(g1);
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {

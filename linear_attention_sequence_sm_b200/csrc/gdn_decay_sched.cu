@@ -381,7 +381,9 @@ DecayLayout decay_layout(const gdn_shape_t &s, bool backward) {
     L.max_segs = N + L.max_slots;
     L.max_chunks = (tokens + 63 * N) / kDecayChunk;
     // checkpoints are `ick` apart, 1024 unless segments are shorter
-    L.max_cks = tokens / (balanced >= kDecayMaxIck || !may_split(s) ? kDecayMaxIck : plan.min_seg) + N;
+    const int64_t ick = balanced >= kDecayMaxIck || !may_split(s) ? kDecayMaxIck : plan.min_seg;
+    L.max_cks = tokens / ick + N;
+    L.max_ckpt = tokens / ick + 1;  // (a sequence's first needs no room: it is the initial state)
     size_t off = 256;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -398,7 +400,7 @@ DecayLayout decay_layout(const gdn_shape_t &s, bool backward) {
     if (backward) {
         L.segdec_off[1] = take(size_t(L.max_slots) * hv * 4);
         L.state_off[1] = take(size_t(L.max_slots) * hv * 65536);
-        L.ckpt_off = take(size_t(L.max_cks) * hv * 65536);
+        L.ckpt_off = take(size_t(L.max_ckpt) * hv * 65536);
         L.zsum_off = take(size_t(L.max_cks) * hv * 32);
         for (int i = 0; i < 2; ++i) L.dot_off[i] = take(size_t(tokens) * hv * 4);
         L.intra_off = take(size_t(tokens) * hv * 4);

@@ -92,8 +92,8 @@ __device__ __forceinline__ void load_tile(float *__restrict__ dst, int ld, const
 __device__ void load_gates(SimtVec &sm, const float *g, size_t g_stride, int L, bool reverse) {
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
-        const float g0 = 2 * lane < L ? fmaxf(g[(2 * lane) * g_stride], kGFloor) : 0.f;
-        const float g1 = 2 * lane + 1 < L ? fmaxf(g[(2 * lane + 1) * g_stride], kGFloor) : 0.f;
+        const float g0 = 2 * lane < L ? floored(g[(2 * lane) * g_stride]) : 0.f;
+        const float g1 = 2 * lane + 1 < L ? floored(g[(2 * lane + 1) * g_stride]) : 0.f;
         double s = double(g0) + double(g1);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -206,7 +206,7 @@ decay_pass_simt_kernel(const __grid_constant__ DecayPass a0, const __grid_consta
             __syncthreads();
             seg_sum += float(sm.G[C - 1]);
             if (a.ckpt && !a.zsum && seg.pos + t0 > 0 && (seg.pos + t0) % hdr->ick == 0) {
-                float *dst = a.ckpt + (size_t(seg.ck + (seg.pos + t0) / hdr->ick) * hv + h) * 16384;
+                float *dst = a.ckpt + (size_t((seg.start + t0) / hdr->ick) * hv + h) * 16384;
                 for (int q = tid; q < dz * dy; q += kThreads) dst[q] = tS[(q / dy) * ly + q % dy];
             }
             if (!a.state_only) {
@@ -332,7 +332,7 @@ decay_pass_simt_kernel(const __grid_constant__ DecayPass a0, const __grid_consta
                 const int slot = seg.ck + (seg.pos + t0) / hdr->ick;
                 const bool start = seg.pos + t0 == 0;
                 const float *cp = start ? (a.s_first ? a.s_first + (size_t(seg.seq) * hv + h) * dz * dy : nullptr)
-                                        : a.ckpt + (size_t(slot) * hv + h) * 16384;
+                                        : a.ckpt + (size_t((seg.start + t0) / hdr->ick) * hv + h) * 16384;
                 __syncthreads();
                 float s = 0.f;
                 if (cp)
@@ -401,8 +401,8 @@ decay_intra_simt_kernel(const DecaySched sc, int num_seqs, int hk, int hv, int d
         if (tid < 32) {
             const float *gp = g_const ? g + h : g + tok * hv + h;
             const size_t gs = g_const ? 0 : hv;
-            const float g0 = 2 * tid < L ? fmaxf(gp[(2 * tid) * gs], kGFloor) : 0.f;
-            const float g1 = 2 * tid + 1 < L ? fmaxf(gp[(2 * tid + 1) * gs], kGFloor) : 0.f;
+            const float g0 = 2 * tid < L ? floored(gp[(2 * tid) * gs]) : 0.f;
+            const float g1 = 2 * tid + 1 < L ? floored(gp[(2 * tid + 1) * gs]) : 0.f;
             double s = double(g0) + double(g1);
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {

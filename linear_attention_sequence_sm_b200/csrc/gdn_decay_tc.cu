@@ -342,7 +342,7 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                 const uint32_t mm = m + uint32_t(n);
                 const int p = w.seg.pos + w.chunk_at(n);  // the chunk's start in the sequence
                 if (kDots && a.ckpt && !a.zsum && mine && p > 0 && p % a.sched.hdr->ick == 0) {
-                    float *ck = a.ckpt + (size_t(w.seg.ck + p / a.sched.hdr->ick) * hv + w.h) * 16384;
+                    float *ck = a.ckpt + (size_t((w.seg.start + w.chunk_at(n)) / a.sched.hdr->ick) * hv + w.h) * 16384;
 #pragma unroll
                     for (int j = 0; j < 64; ++j) ck[(c0 + j) * 128 + row] = S[j];
                 }
@@ -416,7 +416,7 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                                     if (c0 + j < dy) dot = fmaf(a.s_first[sbase + size_t(c0 + j) * dz + row], S[j], dot);
                             }
                         } else {
-                            const float *cp = a.ckpt + slot * 16384;
+                            const float *cp = a.ckpt + (size_t((w.seg.start + w.chunk_at(n)) / a.sched.hdr->ick) * hv + w.h) * 16384;
 #pragma unroll
                             for (int j = 0; j < 64; ++j) dot = fmaf(cp[(c0 + j) * 128 + row], S[j], dot);
                         }
@@ -792,7 +792,7 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                 for (int n = 0; n < w.nch; ++n) {
                     const uint32_t mm = m + uint32_t(n);
                     float *vec = vecs(mm);
-                    const float a0 = fmaxf(g0, kGFloor), a1 = fmaxf(g1, kGFloor);
+                    const float a0 = floored(g0), a1 = floored(g1);
                     if (n + 1 < w.nch) load_g(n + 1);
                     float pre = a0 + a1, suf = a0 + a1;
 #pragma unroll

@@ -283,9 +283,10 @@ cudaError_t launch_backward_tc(const PrefillArgs &a, const void *dO, const float
                                const BwdTcLayout &L, cudaStream_t stream, int num_sms);
 
 // The output side as its own pass over o, in place (for the CUDA-core prefill,
-// whose blocks each own a slice of d_v).
+// whose blocks each own a slice of d_v).  With `status` (device memory), rows
+// are left alone where it is not GDN_OK.
 cudaError_t launch_output_side(void *o, int32_t tokens, int32_t hv, int32_t dv, int32_t dtype, const OutSide &os,
-                               cudaStream_t stream);
+                               cudaStream_t stream, const int32_t *status = nullptr);
 
 // Kimi Delta Attention: prefill (token order, CUDA cores) and decode.
 cudaError_t launch_kda_prefill(const PrefillArgs &a, cudaStream_t stream);

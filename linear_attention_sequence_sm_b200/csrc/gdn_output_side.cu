@@ -16,7 +16,9 @@ constexpr int kOutWarps = 8;
 
 template <typename T>
 __global__ void __launch_bounds__(kOutWarps * 32)
-output_side_kernel(T *__restrict__ o, int64_t rows, int32_t hv, int32_t dv, const OutSide os) {
+output_side_kernel(T *__restrict__ o, int64_t rows, int32_t hv, int32_t dv, const OutSide os,
+                   const int32_t *__restrict__ status) {
+    if (status && *status != GDN_OK) return;  // the call was rejected on the device: o stays as it was
     const int lane = threadIdx.x & 31;
     const int64_t row = int64_t(blockIdx.x) * kOutWarps + (threadIdx.x >> 5);
     if (row >= rows) return;
@@ -44,7 +46,7 @@ output_side_kernel(T *__restrict__ o, int64_t rows, int32_t hv, int32_t dv, cons
 }
 
 cudaError_t launch_output_side(void *o, int32_t tokens, int32_t hv, int32_t dv, int32_t dtype, const OutSide &os,
-                               cudaStream_t stream) {
+                               cudaStream_t stream, const int32_t *status) {
     const int64_t rows = int64_t(tokens) * hv;
     if (rows <= 0) return cudaSuccess;
     if (dv > 128) return cudaErrorInvalidValue;
@@ -52,10 +54,10 @@ cudaError_t launch_output_side(void *o, int32_t tokens, int32_t hv, int32_t dv, 
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     if (dtype == GDN_DTYPE_BF16)
         output_side_kernel<__nv_bfloat16><<<unsigned(blocks), kOutWarps * 32, 0, stream>>>(
-            static_cast<__nv_bfloat16 *>(o), rows, hv, dv, os);
+            static_cast<__nv_bfloat16 *>(o), rows, hv, dv, os, status);
     else
         output_side_kernel<float><<<unsigned(blocks), kOutWarps * 32, 0, stream>>>(static_cast<float *>(o), rows,
-                                                                                   hv, dv, os);
+                                                                                   hv, dv, os, status);
     count_launch();
     return cudaGetLastError();
 }

@@ -703,6 +703,18 @@ def _raw_stream(stream, dev):
     return _stream_handle(stream, dev).value
 
 
+def _room(workspace, nbytes, dev, stream):
+    """``workspace`` where it is large enough, else a new one that belongs to
+    the call's stream: freed on return, its memory goes to that stream's later
+    work only, which runs after the call's kernels."""
+    if workspace is not None and workspace.numel() >= nbytes:
+        return workspace
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -756,9 +768,7 @@ def decay_forward(q, k, v, g, initial_state=None, cu_seqlens=None, output_final_
         out = torch.empty(v.shape, dtype=dt, device=dev)
     if final_state is None and output_final_state:
         final_state = torch.empty((n_seqs, hv, dv, dk), dtype=torch.float32, device=dev)
-    nbytes = decay_workspace_size(shape)
-    if workspace is None or workspace.numel() < nbytes:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    workspace = _room(workspace, decay_workspace_size(shape), dev, stream)
     osc = output_norm.c_struct(out) if output_norm is not None else None
     with _on(dev):  # the library launches on the current device
         _check(LIB.gdn_decay_forward(ctypes.byref(shape), _addr(q), _addr(k), _addr(v), _addr(g), layout,
@@ -808,9 +818,7 @@ def decay_backward(q, k, v, g, d_o, d_final_state=None, initial_state=None, cu_s
         _need(t, n, torch.float32, dev)
     _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
     shape = make_shape(q, v, cu_seqlens, 64, force_simt)
-    nbytes = decay_workspace_size(shape, backward=True)
-    if workspace is None or workspace.numel() < nbytes:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    workspace = _room(workspace, decay_workspace_size(shape, backward=True), dev, stream)
     out = {"dq": torch.empty(q.shape, dtype=dt, device=dev), "dk": torch.empty(k.shape, dtype=dt, device=dev),
            "dv": torch.empty(v.shape, dtype=dt, device=dev),
            "dg": torch.empty(g.shape, dtype=torch.float32, device=dev) if want_dg else None,
@@ -926,9 +934,7 @@ def block_norm_backward(x, residual, norm: BlockNorm, gate=None, d_h=None, d_y=N
     if d_y is not None and not norm.pre_norm:
         raise ValueError("d_y needs pre_norm")
     rows, width, rt = _block_norm_inputs(x, residual, norm, gate, ((d_h, "d_h", True), (d_y, "d_y", False)))
-    nbytes = block_norm_workspace_size(rows, width)
-    if workspace is None or workspace.numel() < nbytes:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    workspace = _room(workspace, block_norm_workspace_size(rows, width), x.device, stream)
     like = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
     out = {"dx": torch.empty_like(x), "d_residual": like(residual), "d_gate": like(gate),
            "d_post_weight": like(norm.post_weight), "d_scale": like(norm.scale), "d_pre_weight": like(norm.pre_weight)}

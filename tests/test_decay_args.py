@@ -103,7 +103,8 @@ def test_c_shape_refusals(gdn, call):
                      (dict(seq_len=-1), inv), (dict(flags=1 << 9), inv), (dict(flags=gdn.GDN_FLAG_QK_L2NORM), uns),
                      (dict(flags=gdn.GDN_FLAG_GATE_LOGITS), uns), (dict(flags=gdn.GDN_FLAG_SPLIT), uns),
                      (dict(chunk_size=32), uns), (dict(head_dim_v=129), uns),
-                     (dict(num_qk_heads=1, num_v_heads=70000), uns)):
+                     (dict(num_qk_heads=1, num_v_heads=70000), uns),
+                     (dict(batch=1, num_seqs=1, seq_len=2 ** 31 - 2048, num_v_heads=2, head_dim_k=8, head_dim_v=8), uns)):
         assert call(gdn, shape(gdn, **kw)) == want, kw
     assert call(gdn, shape(gdn), layout=2) == inv
     assert call(gdn, shape(gdn), cu=P) == inv  # batch 2 with cu_seqlens
@@ -133,6 +134,20 @@ def test_c_decode_refusals(gdn):
         assert call(**kw) == uns, kw
     assert call(state=P + 8) == gdn.GDN_ERR_MISALIGNED
     assert call(n=0, q=0) == gdn.GDN_OK
+
+
+def test_c_decode_output_side_refused_before_the_state_moves(gdn):
+    side = gdn.OutputSideC(0, 0, 1e-6, 0)
+    assert gdn.LIB.gdn_decay_decode_step(1, 1, 1, 16, 129, 1, P, P, P, P, 0, P, ctypes.byref(side), P,
+                                         None) == gdn.GDN_ERR_UNSUPPORTED
+
+
+def test_workspace_of_many_short_sequences(gdn):
+    """No state is kept for a sequence's first position: 4096 sequences of 16 tokens need little more than one of
+    65,536."""
+    many = gdn.decay_workspace_size(shape(gdn, batch=4096, num_seqs=4096, seq_len=16, num_v_heads=32), backward=True)
+    one = gdn.decay_workspace_size(shape(gdn, batch=1, num_seqs=1, seq_len=65536, num_v_heads=32), backward=True)
+    assert many < 1.1 * one
 
 
 def test_workspace_grows_with_the_problem(gdn):
@@ -180,6 +195,11 @@ def test_block_norm_refusals(gdn):
     assert bwd(norm_struct(gdn, pre), w=P) == inv
     assert bwd(ok, ws=0) == inv and bwd(ok, nbytes=16) == gdn.GDN_ERR_WORKSPACE_TOO_SMALL
     assert fwd(ok, rows=0, x=0, h=0, y=0) == gdn.GDN_OK
+
+
+def test_block_norm_outputs_are_two_buffers(gdn):
+    n = norm_struct(gdn, gdn.GDN_BLOCK_PRE_NORM)
+    assert gdn.LIB.gdn_block_norm_forward(2, 64, 1, 1, P, P, 0, ctypes.byref(n), P, P, None) == gdn.GDN_ERR_INVALID_ARGUMENT
 
 
 def test_block_norm_binding_refusals(gdn):

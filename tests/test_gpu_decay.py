@@ -318,3 +318,84 @@ def test_captured_and_replayed():
         want = step()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@dtypes
+@pytest.mark.parametrize("simt", [False, True])
+def test_nan_decay_stays_in_its_head_and_after_its_token(simt, dtype):
+    """A NaN log-decay is not taken for the floor: its head is NaN from that token on, all else as without it."""
+    d = R.make(37, 1, 2, 128, 128, dtype, lens=[100, 140, 30])
+    o, sf = run_forward(d, force_simt=simt)
+    d["g"][170, 1] = float("nan")  # sequence 1, its second chunk
+    on, sn = run_forward(d, force_simt=simt)
+    hit = torch.zeros(270, 2, dtype=torch.bool)
+    hit[170:240, 1] = True
+    on, o = on.cpu(), o.cpu()
+    assert bool(on[hit].isnan().all()) and torch.equal(on[~hit], o[~hit])
+    assert bool(sn[1, 1].isnan().all()) and torch.equal(sn[1, 0], sf[1, 0]) and torch.equal(sn[::2], sf[::2])
+    from linear_attention_sequence_sm_b200 import gdn
+    c = R.cuda(d)
+    one = {k: c[k][169:171].clone() for k in ("q", "k", "v", "g")}
+    t = gdn.decay_decode_step(one["q"], one["k"], one["v"], one["g"], c["s0"][:2].clone())
+    assert bool(t[1, 1].isnan().all()) and not bool(t[0].isnan().any()) and not bool(t[1, 0].isnan().any())
+
+
+@dtypes
+@pytest.mark.parametrize("simt", [False, True])
+def test_values_of_other_sequences_do_not_leak(simt, dtype):
+    """Infinities and NaN in a sequence stay in it, with ends inside chunks on both sides."""
+    d = R.make(39, 1, 2, 128, 128, dtype, lens=[70, 50, 90])
+    o, sf = run_forward(d, force_simt=simt)
+    base = grads(d, force_simt=simt)
+    bad = {k: (t.clone() if t is not None else None) for k, t in d.items()}
+    for k, x in (("q", float("nan")), ("k", float("inf")), ("v", float("-inf")), ("do", float("nan"))):
+        bad[k][70:120] = x
+    on, sn = run_forward(bad, force_simt=simt)
+    got = grads(bad, force_simt=simt)
+    keep = torch.ones(210, dtype=torch.bool)
+    keep[70:120] = False
+    assert torch.equal(on.cpu()[keep], o.cpu()[keep]) and torch.equal(sn[::2], sf[::2])
+    for k in ("dq", "dk", "dv", "dg"):
+        assert torch.equal(got[k].cpu()[keep], base[k].cpu()[keep]), k
+    assert torch.equal(got["d_initial_state"][::2], base["d_initial_state"][::2])
+
+
+def test_output_side_leaves_rejected_calls_alone():
+    from linear_attention_sequence_sm_b200 import gdn
+    d = R.make(31, 1, 2, 128, 128, torch.bfloat16, lens=[40, 60])
+    c = R.cuda(d)
+    cu = torch.tensor([0, 60, 40], dtype=torch.int32, device="cuda")
+    o = torch.full_like(c["v"], 7.0)
+    gdn.decay_forward(c["q"], c["k"], c["v"], c["g"], cu_seqlens=cu, out=o, output_norm=gdn.OutputNorm(eps=1e-6))
+    torch.cuda.synchronize()
+    assert bool((o == 7).all())
+
+
+def test_workspaces_belong_to_the_calls_stream():
+    """A call queued on a side stream behind other work: memory that later work on the current stream takes and
+    fills must not be the call's workspace."""
+    from linear_attention_sequence_sm_b200 import gdn
+    d = R.make(41, 1, 2, 128, 128, torch.bfloat16, lens=[700, 64])
+    want, wf = grads(d), run_forward(d)
+    c = R.cuda(d)
+    sizes = [gdn.decay_workspace_size(gdn.make_shape(c["q"], c["v"], c["cu"], 64), backward=b) for b in (True, False)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # about ten milliseconds
+    got = gdn.decay_backward(c["q"], c["k"], c["v"], c["g"], c["do"], d_final_state=c["dsf"], initial_state=c["s0"],
+                             cu_seqlens=c["cu"], stream=side)
+    o, sf = gdn.decay_forward(c["q"], c["k"], c["v"], c["g"], initial_state=c["s0"], cu_seqlens=c["cu"], stream=side)
+    for n in sizes * 2:
+        torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255)
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[k], want[k]) for k in want)
+    assert torch.equal(o, wf[0]) and torch.equal(sf, wf[1])
+
+
+@dtypes
+def test_many_sequences_and_checkpoints(dtype):
+    """Gradients where cuts, checkpoints and sequence ends fall into one another: one long sequence among short ones."""
+    d = R.make(43, 1, 2, 64, 64, dtype, lens=[1, 30, 1300, 2, 64, 257, 1])
+    check_backward(d, grads(d))
