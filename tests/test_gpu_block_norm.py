@@ -184,3 +184,33 @@ def test_same_bits_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(u, v) for u, v in zip(outs, run()))
+
+
+@pytest.mark.parametrize("types", TYPES, ids=["bf16", "bf16_wide", "f32"])
+@pytest.mark.parametrize("size", [(1301, 4096), (2503, 2048), (2601, 1032), (9477, 264), (10003, 24)], ids=str)
+def test_many_rows(size, types):
+    """Rows enough for several groups a block, the last ones short; each part of the gradients wanted or not."""
+    from linear_attention_sequence_sm_b200 import gdn
+    names = dict(x="dx", residual="d_residual", gate="d_gate", w1="d_post_weight", scale="d_scale", w2="d_pre_weight")
+    full = dict(rho=0.75, branch=0.5, zero_centred=True)
+    for gate, use, kw in ((True, {}, full), (False, dict(use_dh=False), dict(activation="sigmoid")),
+                          (True, {}, dict(activation="sigmoid", post=False)), (True, dict(use_dy=False), dict(pre=False)),
+                          (False, {}, dict()), (False, {}, dict(post=False)), (True, {}, dict(post=False)),
+                          (True, {}, dict(activation="sigmoid"))):
+        d = make(57, *size, *types, gate=gate)
+        for k, on in (("w1", kw.get("post", True)), ("w2", kw.get("pre", True))):
+            if not on:
+                d[k] = None
+        c = R.cuda(d)
+        up = {k: c[k] for k, flag in (("d_h", "use_dh"), ("d_y", "use_dy")) if use.get(flag, True)}
+        got = gdn.block_norm_backward(c["x"], c["residual"], norm_of(c, **kw), gate=c["gate"], **up)
+        torch.cuda.synchronize()
+        ref = reference(d, True, **use, **kw)
+        for k, name in names.items():
+            if k not in ref:
+                assert got[name] is None
+                continue
+            # twice the forward's error, as in test_forward_and_backward; column sums of `rows` fp32 terms each: a
+            # chain of at most rows / 148 + 16 additions, (that + 296) u of terms that do not cancel in the norm
+            bars = 2 * bar(got[name]) + (size[0] / 148 + 312) * R.U32
+            assert rel(got[name], ref[k]) <= bars, (name, gate, kw)
