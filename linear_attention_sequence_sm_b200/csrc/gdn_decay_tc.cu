@@ -144,7 +144,7 @@ struct Maps {
 };
 
 // The units of this CTA, one after the other.
-struct UnitWalk {
+template <bool kRev> struct UnitWalk {
     const DecayPass &a;
     int64_t u, units;
     DecaySeg seg;
@@ -160,13 +160,13 @@ struct UnitWalk {
             seg = a.sched.segs[u / a.hv];
             h = int(u % a.hv);
             nch = (seg.len + kDecayChunk - 1) / kDecayChunk;
-            first = a.reverse ? seg.pos + seg.len == seg.seq_len : seg.pos == 0;
-            last = a.reverse ? seg.pos == 0 : seg.pos + seg.len == seg.seq_len;
+            first = kRev ? seg.pos + seg.len == seg.seq_len : seg.pos == 0;
+            last = kRev ? seg.pos == 0 : seg.pos + seg.len == seg.seq_len;
             if (!(state_only && (seg.slot < 0 || last))) return true;
         }
     }
     // first token of the n-th chunk in pass order, from the segment's start
-    __device__ int chunk_at(int n) const { return kDecayChunk * (a.reverse ? nch - 1 - n : n); }
+    __device__ int chunk_at(int n) const { return kDecayChunk * (kRev ? nch - 1 - n : n); }
 };
 
 // A bounded wait that leaves the issue slots to the others: the thread is
@@ -256,7 +256,7 @@ __device__ __forceinline__ void stmatrix_t(uint32_t addr, uint32_t a, uint32_t b
                  : "memory");
 }
 
-template <int kKind>
+template <int kKind, bool kRev, bool kF32>
 __global__ void __launch_bounds__(kThreads, 1)
 decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
     using K = Cfg<kKind>;
@@ -297,7 +297,7 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
     bool ok = a.sched.hdr->status == GDN_OK;
     const int hv = a.hv, dy = a.dy, dz = a.dz;
     const int ya = dy > 64 ? 2 : 1;  // 64-column halves of y and of the state
-    UnitWalk w(a, !ok);
+    UnitWalk<kRev> w(a, !ok);
     const bool dead = !ok;
     uint32_t m = 0;  // chunks this CTA has processed
 
@@ -571,7 +571,7 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                                     red[quarter * 64 + 16 * p + 8 * (lane >> 4) + tp + ((lane >> 3) & 1)] = d[0];
                             }
                         }
-                        if (!a.out_f32) {
+                        if (!kF32) {
                             // bf16 token pairs, transposed into rows of 64 bytes (four 16-byte pieces, swizzled) per token
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
@@ -607,7 +607,7 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(kBVecFree + int(mm & 3u)));
-                    if (!a.out_f32) {
+                    if (!kF32) {
                         __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.out) + at;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -758,8 +758,8 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
                                 const int c = c0 + j;
-                                const bool in = a.reverse ? (c >= r && c < L) : c <= r;
-                                const float d = a.reverse ? gc[j] - Gr : Gr - gc[j];
+                                const bool in = kRev ? (c >= r && c < L) : c <= r;
+                                const float d = kRev ? gc[j] - Gr : Gr - gc[j];
                                 float e;
                                 asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(d));
                                 x[j] = in ? v[8 * q + j] * e : 0.f;
@@ -811,8 +811,8 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                     if (mm >= 4) ok = warp_wait(bar(kBVecFree + int(mm & 3u)), ((mm >> 2) - 1) & 1u);
                     if (!ok) break;
                     *reinterpret_cast<float2 *>(vec + kVecG + 2 * lane) = make_float2(G0 * kLog2e, G1 * kLog2e);
-                    *reinterpret_cast<float2 *>(vec + kVecIn + 2 * lane) = a.reverse ? make_float2(f0, f1) : make_float2(e0, e1);
-                    *reinterpret_cast<float2 *>(vec + kVecSt + 2 * lane) = a.reverse ? make_float2(e0, e1) : make_float2(f0, f1);
+                    *reinterpret_cast<float2 *>(vec + kVecIn + 2 * lane) = kRev ? make_float2(f0, f1) : make_float2(e0, e1);
+                    *reinterpret_cast<float2 *>(vec + kVecSt + 2 * lane) = kRev ? make_float2(e0, e1) : make_float2(f0, f1);
                     if (lane == 0) vec[kVecGamma] = et;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(kBVec + int(mm & 3u)));
@@ -971,14 +971,14 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
     if (warp == 0) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int kKind>
+template <int kKind, bool kRev, bool kF32>
 cudaError_t launch_as(const Maps &tm, const DecayPass &p, int64_t max_units, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(decay_pass_tc_kernel<kKind>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(decay_pass_tc_kernel<kKind, kRev, kF32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          int(Cfg<kKind>::kSmem));
     if (e != cudaSuccess) return e;
     static const int regs = [] {
         cudaFuncAttributes fa;
-        return cudaFuncGetAttributes(&fa, decay_pass_tc_kernel<kKind>) == cudaSuccess ? fa.numRegs : -1;
+        return cudaFuncGetAttributes(&fa, decay_pass_tc_kernel<kKind, kRev, kF32>) == cudaSuccess ? fa.numRegs : -1;
     }();
     if (regs != kRegsLaunch) return cudaErrorInvalidKernelImage;  // the roles' registers are dealt out of these
     const int sms = device_sm_count(nullptr);
@@ -993,10 +993,19 @@ cudaError_t launch_as(const Maps &tm, const DecayPass &p, int64_t max_units, cud
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, decay_pass_tc_kernel<kKind>, tm, p);
+    e = cudaLaunchKernelEx(&cfg, decay_pass_tc_kernel<kKind, kRev, kF32>, tm, p);
     count_launch();
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
+}
+
+template <int kKind>
+cudaError_t launch_out(const Maps &tm, const DecayPass &p, int64_t max_units, cudaStream_t stream) {
+    if (p.reverse)
+        return p.out_f32 ? launch_as<kKind, true, true>(tm, p, max_units, stream)
+                         : launch_as<kKind, true, false>(tm, p, max_units, stream);
+    return p.out_f32 ? launch_as<kKind, false, true>(tm, p, max_units, stream)
+                     : launch_as<kKind, false, false>(tm, p, max_units, stream);
 }
 
 }  // namespace
@@ -1015,9 +1024,10 @@ cudaError_t launch_decay_pass_tc(const DecayPass &p, int64_t max_units, cudaStre
          !make_head_map(&tm.y, p.y, p.hy, p.dy, p.tokens) || !make_head_map(&tm.z, p.z, p.hz, p.dz, p.tokens) ||
          (p.aux && !make_head_map(&tm.aux, p.aux, p.haux, p.dz, p.tokens))))
         return cudaErrorInvalidValue;
-    if (p.state_only) return launch_as<kStateOnly>(tm, p, max_units, stream);
-    if (p.dot) return launch_as<kDot>(tm, p, max_units, stream);
-    return launch_as<kPlain>(tm, p, max_units, stream);
+    if (p.state_only)
+        return p.reverse ? launch_as<kStateOnly, true, false>(tm, p, max_units, stream)
+                         : launch_as<kStateOnly, false, false>(tm, p, max_units, stream);
+    return p.dot ? launch_out<kDot>(tm, p, max_units, stream) : launch_out<kPlain>(tm, p, max_units, stream);
 }
 
 }  // namespace gdn
