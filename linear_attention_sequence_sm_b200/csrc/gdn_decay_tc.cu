@@ -229,8 +229,13 @@ __device__ __forceinline__ void tmem_st_frag(uint32_t taddr, uint32_t a, uint32_
 }
 // x minus the two bf16 values of w (exact where w is x rounded).
 __device__ __forceinline__ f32x2 sub_bf16x2(f32x2 x, uint32_t w) { return fma2(from_bf16x2(w), both(-1.f), x); }
-// 8 consecutive 32-bit columns of this thread's lane, written (raw bits).
-__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&r)[8]) {
+// Consecutive 32-bit columns of this thread's lane, written (raw bits).
+__device__ __forceinline__ void tmem_st_words(uint32_t taddr, const uint32_t (&r)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st_words(uint32_t taddr, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
@@ -353,24 +358,25 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
                     tc_fence_after();
                     if (mine) {
                         const uint32_t ca = trow + K::kColC + uint32_t(c0 / 2);
+constexpr int kW = K::kCopies == 1 ? 8 : 4;  // words of a slice (fewer where its terms take registers too)
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {  // 16 columns
-                            uint32_t pk[8];
-                            f32x2 r[8];
+                        for (int q = 0; q < 32 / kW; ++q) {
+                            uint32_t pk[kW];
+                            f32x2 r[kW];
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                r[j] = pair(S[16 * q + 2 * j], S[16 * q + 2 * j + 1]);
+                            for (int j = 0; j < kW; ++j) {
+                                r[j] = pair(S[2 * (kW * q + j)], S[2 * (kW * q + j) + 1]);
                                 pk[j] = to_bf16x2(r[j]);
                             }
-                            tmem_st8u(ca + 8 * q, pk);
+                            tmem_st_words(ca + kW * q, pk);
 #pragma unroll
                             for (int t = 1; t < K::kCopies; ++t) {
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) {
+                                for (int j = 0; j < kW; ++j) {
                                     r[j] = sub_bf16x2(r[j], pk[j]);
                                     pk[j] = to_bf16x2(r[j]);
                                 }
-                                tmem_st8u(ca + 64 * t + 8 * q, pk);
+                                tmem_st_words(ca + 64 * t + kW * q, pk);
                             }
                         }
                         tmem_wait_st();
