@@ -1005,8 +1005,10 @@ template <typename K>
 cudaError_t staged_launch(K kern, int stages, const BlockNormArgs &a, const Stages &sg, int grid, dim3 block,
                           cudaStream_t stream) {
     const size_t bytes = 64 + size_t(stages) * sg.stage_bytes;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
-    if (e != cudaSuccess) return e;
+    if (bytes > 40 * 1024) {  // (a kernel may have 48 KB in all without asking)
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+        if (e != cudaSuccess) return e;
+    }
     kern<<<unsigned(grid), block, bytes, stream>>>(a, sg);
     count_launch();
     return cudaGetLastError();

@@ -205,11 +205,24 @@ def _need(t, name, dtype=None, device=None):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
+def _ready(dev, dtype, *tensors):
+    """Whether _need(t, ..., dtype, dev) would accept every tensor (None: not
+    given): the common case in one pass; a caller that gets False asks _need
+    one by one, for its message."""
+    index = dev.index
+    if index is None:  # (not a CUDA device)
+        return False
+    for t in tensors:
+        if t is not None and (t.dtype is not dtype or t.get_device() != index or not t.is_contiguous()):
+            return False
+    return True
+
+
 def _expect(t, name, shape):
     """``t`` (if given) must have exactly ``shape``: the library takes bare
     pointers and derives every extent from q and v, so a tensor of another
     shape would be read or written out of bounds on the device."""
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if t is not None and t.shape != (shape if isinstance(shape, tuple) else tuple(shape)):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -758,16 +771,18 @@ def decay_forward(q, k, v, g, initial_state=None, cu_seqlens=None, output_final_
     _expect(out, "out", v.shape)
     _expect(final_state, "final_state", (n_seqs, hv, dv, dk))
     dev, dt = q.device, q.dtype
-    for t, n in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
-        _need(t, n, dt, dev)
-    for t, n in ((g, "g"), (initial_state, "initial_state"), (final_state, "final_state")):
-        _need(t, n, torch.float32, dev)
+    if not (_ready(dev, dt, q, k, v, out) and _ready(dev, torch.float32, g, initial_state, final_state)):
+        for t, n in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
+            _need(t, n, dt, dev)
+        for t, n in ((g, "g"), (initial_state, "initial_state"), (final_state, "final_state")):
+            _need(t, n, torch.float32, dev)
     _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
     shape = make_shape(q, v, cu_seqlens, 64, force_simt)
     if out is None:
-        out = torch.empty(v.shape, dtype=dt, device=dev)
+        out = torch.empty_like(v)
     if final_state is None and output_final_state:
-        final_state = torch.empty((n_seqs, hv, dv, dk), dtype=torch.float32, device=dev)
+        final_state = torch.empty_like(initial_state) if initial_state is not None else \
+            torch.empty((n_seqs, hv, dv, dk), dtype=torch.float32, device=dev)
     workspace = _room(workspace, decay_workspace_size(shape), dev, stream)
     osc = output_norm.c_struct(out) if output_norm is not None else None
     with _on(dev):  # the library launches on the current device
@@ -786,12 +801,13 @@ def decay_decode_step(q, k, v, g, state, out=None, stream=None, output_norm: Out
     layout = _decay_layout(g, tuple(v.shape[:-1]))
     _expect(out, "out", v.shape)
     dev, dt = q.device, q.dtype
-    for t, n in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
-        _need(t, n, dt, dev)
-    _need(g, "g", torch.float32, dev)
-    _need(state, "state", torch.float32, dev)
+    if not (_ready(dev, dt, q, k, v, out) and _ready(dev, torch.float32, g, state)):
+        for t, n in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
+            _need(t, n, dt, dev)
+        _need(g, "g", torch.float32, dev)
+        _need(state, "state", torch.float32, dev)
     if out is None:
-        out = torch.empty(v.shape, dtype=dt, device=dev)
+        out = torch.empty_like(v)
     N, hk, dk = q.shape
     hv, dv = v.shape[1], v.shape[2]
     osc = output_norm.c_struct(out) if output_norm is not None else None
@@ -812,16 +828,16 @@ def decay_backward(q, k, v, g, d_o, d_final_state=None, initial_state=None, cu_s
     _expect(d_o, "d_o", v.shape)
     _expect(d_final_state, "d_final_state", (n_seqs, hv, dv, dk))
     dev, dt = q.device, q.dtype
-    for t, n in ((q, "q"), (k, "k"), (v, "v"), (d_o, "d_o")):
-        _need(t, n, dt, dev)
-    for t, n in ((g, "g"), (initial_state, "initial_state"), (d_final_state, "d_final_state")):
-        _need(t, n, torch.float32, dev)
+    if not (_ready(dev, dt, q, k, v, d_o) and _ready(dev, torch.float32, g, initial_state, d_final_state)):
+        for t, n in ((q, "q"), (k, "k"), (v, "v"), (d_o, "d_o")):
+            _need(t, n, dt, dev)
+        for t, n in ((g, "g"), (initial_state, "initial_state"), (d_final_state, "d_final_state")):
+            _need(t, n, torch.float32, dev)
     _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
     shape = make_shape(q, v, cu_seqlens, 64, force_simt)
     workspace = _room(workspace, decay_workspace_size(shape, backward=True), dev, stream)
-    out = {"dq": torch.empty(q.shape, dtype=dt, device=dev), "dk": torch.empty(k.shape, dtype=dt, device=dev),
-           "dv": torch.empty(v.shape, dtype=dt, device=dev),
-           "dg": torch.empty(g.shape, dtype=torch.float32, device=dev) if want_dg else None,
+    out = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
+           "dg": torch.empty_like(g) if want_dg else None,
            "d_initial_state": torch.empty((n_seqs, hv, dv, dk), dtype=torch.float32, device=dev)
            if want_d_initial_state else None}
     with _on(dev):  # the library launches on the current device
@@ -862,8 +878,9 @@ class BlockNorm:
 
     def c_struct(self, x: torch.Tensor, gate) -> BlockNormC:
         dev = x.device
-        for w, n in ((self.post_weight, "post_weight"), (self.scale, "scale"), (self.pre_weight, "pre_weight")):
-            _need(w, n, torch.float32, dev)  # (their shapes: _block_norm_inputs)
+        if not _ready(dev, torch.float32, self.post_weight, self.scale, self.pre_weight):
+            for w, n in ((self.post_weight, "post_weight"), (self.scale, "scale"), (self.pre_weight, "pre_weight")):
+                _need(w, n, torch.float32, dev)  # (their shapes: _block_norm_inputs)
         flags = ((GDN_BLOCK_POST_NORM if self.post_norm else 0) | (GDN_BLOCK_PRE_NORM if self.pre_norm else 0) |
                  (GDN_BLOCK_ZERO_CENTRED if self.zero_centred else 0))
         if gate is not None:
@@ -877,22 +894,25 @@ def _block_norm_inputs(x, residual, norm, gate, more):
     name, type) of x's shape.  Returns (rows, width, residual type)."""
     if x.dim() < 1:
         raise ValueError("x must be [..., width]")
-    rt = x.dtype if residual is None else residual.dtype
-    _expect(residual, "residual", x.shape)
-    _expect(gate, "gate", x.shape)
+    dt, shape, dev = x.dtype, x.shape, x.device
+    rt = dt if residual is None else residual.dtype
+    _expect(residual, "residual", shape)
+    _expect(gate, "gate", shape)
     for t, n, _ in more:
-        _expect(t, n, x.shape)
+        _expect(t, n, shape)
+    row = shape[-1:]
     for w, n in ((norm.post_weight, "post_weight"), (norm.scale, "scale"), (norm.pre_weight, "pre_weight")):
-        _expect(w, n, x.shape[-1:])
-    if rt not in (x.dtype, torch.float32):
-        raise TypeError(f"residual must be {x.dtype} or torch.float32, got {rt}")
-    dev = x.device
-    _need(x, "x", x.dtype, dev)
-    _need(residual, "residual", rt, dev)
-    _need(gate, "gate", x.dtype, dev)
-    for t, n, wide in more:
-        _need(t, n, rt if wide else x.dtype, dev)
-    width = x.shape[-1]
+        _expect(w, n, row)
+    if rt is not dt and rt is not torch.float32:
+        raise TypeError(f"residual must be {dt} or torch.float32, got {rt}")
+    wide = [t for t, _, w in more if w]
+    if not (_ready(dev, dt, x, gate, *(t for t, _, w in more if not w)) and _ready(dev, rt, residual, *wide)):
+        _need(x, "x", dt, dev)
+        _need(residual, "residual", rt, dev)
+        _need(gate, "gate", dt, dev)
+        for t, n, w in more:
+            _need(t, n, rt if w else dt, dev)
+    width = shape[-1]
     return (x.numel() // width if width else 0), width, rt
 
 
@@ -906,7 +926,7 @@ def block_norm_forward(x, residual, norm: BlockNorm, gate=None, h=None, y=None, 
         raise ValueError("y needs pre_norm")
     rows, width, rt = _block_norm_inputs(x, residual, norm, gate, ((h, "h", True), (y, "y", False)))
     if h is None:
-        h = torch.empty(x.shape, dtype=rt, device=x.device)
+        h = torch.empty_like(x if residual is None else residual)
     if y is None and norm.pre_norm:
         y = torch.empty_like(x)
     c = norm.c_struct(x, gate)
