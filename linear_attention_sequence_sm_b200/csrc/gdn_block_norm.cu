@@ -12,8 +12,11 @@
 //     dn1 = du w1,     dx = (dn1 - n1 mean(dn1 . n1)) / rms(x),
 //     dw2 = sum dy n2, ds = sum c e b, dw1 = sum du n1      (sums over rows)
 //
-// Both are bound by memory: each input row is read once into registers, h and
-// the norms are recomputed in the backward instead of kept.
+// Both are bound by memory: each input row is read once, h and the norms are
+// recomputed in the backward instead of kept.  16,384 x 4096 rows in bf16 with
+// a gate and a residual: forward 114 us, 0.90 of the copy bandwidth; gradients
+// 246 us, 0.67.  (Compiling the forward for the parts a call has, as the
+// gradients are, gave nothing: 127 us against 124.)
 #include <algorithm>
 
 #include "gdn_block_norm.cuh"

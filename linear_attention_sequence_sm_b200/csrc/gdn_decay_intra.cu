@@ -17,7 +17,10 @@
 // What bounds it is reading q, k, v and do once: two warp-level products
 // (mma.sync) of 2 x 64 x 64 x 128 per value head are a tenth of the time that
 // takes, so their accumulators may as well be where the scan wants them, in
-// registers; the tensor-memory path would only add a round trip.
+// registers; the tensor-memory path would only add a round trip.  4 x 4096
+// tokens, 16 q/k and 32 value heads, d = 128: 127 us for 405 MB, 0.49 of the
+// copy bandwidth (a block for each value head, reading q and k again: 178 us;
+// on CUDA cores 941 us); three blocks an SM wait for their tiles in turn.
 #include <algorithm>
 
 #include "gdn_decay.cuh"
