@@ -399,3 +399,11 @@ def test_many_sequences_and_checkpoints(dtype):
     """Gradients where cuts, checkpoints and sequence ends fall into one another: one long sequence among short ones."""
     d = R.make(43, 1, 2, 64, 64, dtype, lens=[1, 30, 1300, 2, 64, 257, 1])
     check_backward(d, grads(d))
+
+
+@dtypes
+@pytest.mark.parametrize("shape", [(1, 3, 33, 17), (2, 4, 7, 5), (1, 2, 12, 20)], ids=str)
+@pytest.mark.parametrize("per_token", [True, False])
+def test_backward_grouped_heads_of_odd_sizes(per_token, shape, dtype):
+    d = R.make(45, *shape, dtype, lens=[70, 0, 33], per_token=per_token)
+    check_backward(d, grads(d))
