@@ -9,7 +9,7 @@
 // flight; a row's dot product takes one shuffle tree, interleaved over the
 // rows.  d_k not a multiple of 4 takes a scalar form of the same walk.  256
 // sequences x 32 heads x 128 x 128: 168 us, 0.98 of the copy bandwidth; one
-// sequence is the host's time for a call (13 us).
+// sequence is the host's time for a call (11 us).
 #include <algorithm>
 
 #include "gdn_decay.cuh"

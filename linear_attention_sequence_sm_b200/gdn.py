@@ -744,7 +744,15 @@ def _decay_layout(g, per_token):
 
 def _decay_prefill_shapes(q, k, v, g, initial_state, cu_seqlens):
     """Shape checks of the decayed linear attention's prefill and backward:
-    _prefill_shapes, with g [..., Hv] or [Hv] and no beta."""
+    _prefill_shapes, with g [..., Hv] or [Hv] and no beta.  Returns (N, Hv,
+    d_v, d_k, the decays' layout)."""
+    qs, vs, gs = q.shape, v.shape, g.shape
+    if cu_seqlens is None and len(qs) == 4 and len(vs) == 4 and k.shape == qs and vs[:2] == qs[:2]:
+        # (the usual call in few steps; whatever it does not settle goes on to the checks with their messages)
+        n, hv, dv, dk = qs[0], vs[2], vs[3], qs[3]
+        layout = GDN_DECAY_PER_TOKEN if gs == vs[:3] else GDN_DECAY_PER_HEAD if gs == (hv,) else None
+        if layout is not None and (initial_state is None or initial_state.shape == (n, hv, dv, dk)):
+            return n, hv, dv, dk, layout
     per_token = g if g.dim() == v.dim() - 1 else None
     n_seqs, hv, dv, dk = _prefill_shapes(q, k, v, per_token, None, initial_state, cu_seqlens)
     return n_seqs, hv, dv, dk, _decay_layout(g, tuple(v.shape[:-1]))
@@ -768,8 +776,10 @@ def decay_forward(q, k, v, g, initial_state=None, cu_seqlens=None, output_final_
     ([B, T, Hv]) or per head ([Hv]).  The other arguments are as for
     chunk_forward; nothing is normalised inside."""
     n_seqs, hv, dv, dk, layout = _decay_prefill_shapes(q, k, v, g, initial_state, cu_seqlens)
-    _expect(out, "out", v.shape)
-    _expect(final_state, "final_state", (n_seqs, hv, dv, dk))
+    if out is not None:
+        _expect(out, "out", v.shape)
+    if final_state is not None:
+        _expect(final_state, "final_state", (n_seqs, hv, dv, dk))
     dev, dt = q.device, q.dtype
     if not (_ready(dev, dt, q, k, v, out) and _ready(dev, torch.float32, g, initial_state, final_state)):
         for t, n in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
@@ -797,9 +807,16 @@ def decay_decode_step(q, k, v, g, state, out=None, stream=None, output_norm: Out
     """One token per sequence of the decayed linear attention: q, k
     [N, Hk, d_k], v [N, Hv, d_v], g [N, Hv] or [Hv] fp32; ``state``
     [N, Hv, d_v, d_k] fp32 is updated in place.  Returns o [N, Hv, d_v]."""
-    _decode_shapes(q, k, v, None, None, state)
-    layout = _decay_layout(g, tuple(v.shape[:-1]))
-    _expect(out, "out", v.shape)
+    qs, vs = q.shape, v.shape
+    layout = None
+    if len(qs) == 3 and len(vs) == 3 and k.shape == qs and vs[0] == qs[0] and state.shape == (*vs, qs[2]):
+        gs = g.shape
+        layout = GDN_DECAY_PER_TOKEN if gs == vs[:2] else GDN_DECAY_PER_HEAD if gs == vs[1:2] else None
+    if layout is None:  # the same checks one by one, with their messages
+        _decode_shapes(q, k, v, None, None, state)
+        layout = _decay_layout(g, tuple(v.shape[:-1]))
+    if out is not None:
+        _expect(out, "out", vs)
     dev, dt = q.device, q.dtype
     if not (_ready(dev, dt, q, k, v, out) and _ready(dev, torch.float32, g, state)):
         for t, n in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
@@ -808,8 +825,8 @@ def decay_decode_step(q, k, v, g, state, out=None, stream=None, output_norm: Out
         _need(state, "state", torch.float32, dev)
     if out is None:
         out = torch.empty_like(v)
-    N, hk, dk = q.shape
-    hv, dv = v.shape[1], v.shape[2]
+    N, hk, dk = qs
+    hv, dv = vs[1], vs[2]
     osc = output_norm.c_struct(out) if output_norm is not None else None
     with _on(dev):  # the library launches on the current device
         _check(LIB.gdn_decay_decode_step(N, hk, hv, dk, dv, _dtype_code(q), _addr(q), _addr(k), _addr(v), _addr(g),
@@ -902,11 +919,12 @@ def _block_norm_inputs(x, residual, norm, gate, more):
         _expect(t, n, shape)
     row = shape[-1:]
     for w, n in ((norm.post_weight, "post_weight"), (norm.scale, "scale"), (norm.pre_weight, "pre_weight")):
-        _expect(w, n, row)
+        if w is not None:
+            _expect(w, n, row)
     if rt is not dt and rt is not torch.float32:
         raise TypeError(f"residual must be {dt} or torch.float32, got {rt}")
-    wide = [t for t, _, w in more if w]
-    if not (_ready(dev, dt, x, gate, *(t for t, _, w in more if not w)) and _ready(dev, rt, residual, *wide)):
+    narrow, wide = ([t for t, _, w in more if not w], [t for t, _, w in more if w]) if more else ((), ())
+    if not (_ready(dev, dt, x, gate, *narrow) and _ready(dev, rt, residual, *wide)):
         _need(x, "x", dt, dev)
         _need(residual, "residual", rt, dev)
         _need(gate, "gate", dt, dev)
@@ -924,7 +942,8 @@ def block_norm_forward(x, residual, norm: BlockNorm, gate=None, h=None, y=None, 
     ``x`` (in place).  Returns (h, y or None without pre_norm)."""
     if y is not None and not norm.pre_norm:
         raise ValueError("y needs pre_norm")
-    rows, width, rt = _block_norm_inputs(x, residual, norm, gate, ((h, "h", True), (y, "y", False)))
+    more = () if h is None and y is None else ((h, "h", True), (y, "y", False))
+    rows, width, rt = _block_norm_inputs(x, residual, norm, gate, more)
     if h is None:
         h = torch.empty_like(x if residual is None else residual)
     if y is None and norm.pre_norm:
@@ -932,8 +951,9 @@ def block_norm_forward(x, residual, norm: BlockNorm, gate=None, h=None, y=None, 
     c = norm.c_struct(x, gate)
     dev = x.device
     with _on(dev):  # the library launches on the current device
-        _check(LIB.gdn_block_norm_forward(rows, width, _dtype_code(x), _dtype_code(h), _addr(x), _addr(residual),
-                                          _addr(gate), ctypes.byref(c), _addr(h), _addr(y), _raw_stream(stream, dev)))
+        _check(LIB.gdn_block_norm_forward(rows, width, _dtype_code(x), _dtype_code(h), x.data_ptr(), _addr(residual),
+                                          _addr(gate), ctypes.byref(c), h.data_ptr(), _addr(y),
+                                          _raw_stream(stream, dev)))
     return h, y
 
 
