@@ -407,3 +407,25 @@ def test_many_sequences_and_checkpoints(dtype):
 def test_backward_grouped_heads_of_odd_sizes(per_token, shape, dtype):
     d = R.make(45, *shape, dtype, lens=[70, 0, 33], per_token=per_token)
     check_backward(d, grads(d))
+
+
+def test_two_calls_at_once():
+    """Prefills and gradients on two streams side by side, each with its own workspace."""
+    from linear_attention_sequence_sm_b200 import gdn
+    ds = [R.make(s, 2, 4, 128, 128, torch.bfloat16, lens=ls) for s, ls in ((47, [900, 130, 64]), (48, [65] * 9))]
+    want = [(run_forward(d), grads(d)) for d in ds]
+    cs = [R.cuda(d) for d in ds]
+    streams = [torch.cuda.Stream() for _ in ds]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(3):
+        for i, (c, s) in enumerate(zip(cs, streams)):
+            f = gdn.decay_forward(c["q"], c["k"], c["v"], c["g"], initial_state=c["s0"], cu_seqlens=c["cu"], stream=s)
+            b = gdn.decay_backward(c["q"], c["k"], c["v"], c["g"], c["do"], d_final_state=c["dsf"],
+                                   initial_state=c["s0"], cu_seqlens=c["cu"], stream=s)
+            got[i].append((f, b))
+    torch.cuda.synchronize()
+    for (wf, wb), runs in zip(want, got):
+        for f, b in runs:
+            assert torch.equal(f[0], wf[0]) and torch.equal(f[1], wf[1])
+            assert all(torch.equal(b[k], wb[k]) for k in wb)
