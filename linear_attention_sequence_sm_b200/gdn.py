@@ -717,10 +717,14 @@ def _raw_stream(stream, dev):
 
 
 def _room(workspace, nbytes, dev, stream):
-    """``workspace`` where it is large enough, else a new one that belongs to
-    the call's stream: freed on return, its memory goes to that stream's later
-    work only, which runs after the call's kernels."""
-    if workspace is not None and workspace.numel() >= nbytes:
+    """The caller's ``workspace`` (uint8 on the tensors' device, at least
+    ``nbytes``: the library writes through its bare pointer), or a new one that
+    belongs to the call's stream: freed on return, its memory goes to that
+    stream's later work only, which runs after the call's kernels."""
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8, dev)
+        if workspace.numel() < nbytes:
+            raise ValueError(f"workspace has {workspace.numel()} bytes, the call needs {nbytes}")
         return workspace
     if stream is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=dev)
@@ -773,8 +777,9 @@ def decay_forward(q, k, v, g, initial_state=None, cu_seqlens=None, output_final_
     S_t = e^{g_t} S_{t-1} + v_t k_t^T, o_t = S_t q_t.  Returns (o,
     final_state or None).  q, k [B, T, Hk, d_k], v [B, T, Hv, d_v] (or packed
     [T, ...] with ``cu_seqlens``); g fp32, one log-decay per token and head
-    ([B, T, Hv]) or per head ([Hv]).  The other arguments are as for
-    chunk_forward; nothing is normalised inside."""
+    ([B, T, Hv]) or per head ([Hv]).  ``workspace`` is uint8, of at least
+    decay_workspace_size bytes; the other arguments are as for chunk_forward.
+    Nothing is normalised inside."""
     n_seqs, hv, dv, dk, layout = _decay_prefill_shapes(q, k, v, g, initial_state, cu_seqlens)
     if out is not None:
         _expect(out, "out", v.shape)

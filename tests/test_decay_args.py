@@ -225,3 +225,34 @@ def test_block_norm_binding_refusals(gdn):
     for kw in (dict(activation="relu"), dict(post_norm=False, post_weight=x), dict(pre_norm=False, pre_weight=x)):
         with pytest.raises(ValueError):
             gdn.BlockNorm(**kw)
+
+
+def refused_workspaces(gdn, nbytes):
+    return [(torch.zeros(2 * nbytes, dtype=torch.uint8), "CUDA tensor"),
+            (torch.zeros(1, dtype=torch.uint8).expand(2 * nbytes), "CUDA tensor|contiguous"),
+            (torch.zeros(2 * nbytes, dtype=torch.uint8, device="meta"), "CUDA tensor")]
+
+
+@pytest.mark.parametrize("name", ["decay_forward", "decay_backward", "block_norm_backward"])
+def test_workspace_of_another_place(gdn, monkeypatch, name):
+    """A workspace is checked like every tensor: the library would write its header through the bare pointer.  (The
+    checks of the other tensors are left out, so that CPU tensors get as far as the workspace.)"""
+    need = gdn._need
+    monkeypatch.setattr(gdn, "_ready", lambda *a: True)
+    monkeypatch.setattr(gdn, "_need", lambda t, n, *a: need(t, n, *a) if n == "workspace" else None)
+    x = torch.zeros(4, 32)
+    call = dict(decay_forward=lambda ws: gdn.decay_forward(*args(), workspace=ws),
+                decay_backward=lambda ws: gdn.decay_backward(*args(), torch.zeros(B, T, HV, DV), workspace=ws),
+                block_norm_backward=lambda ws: gdn.block_norm_backward(x, x, gdn.BlockNorm(), d_h=x, workspace=ws))[name]
+    for ws, what in refused_workspaces(gdn, 1 << 22):
+        with pytest.raises(ValueError, match=what):
+            call(ws)
+
+
+def test_small_workspace_is_refused_not_replaced(gdn, monkeypatch):
+    """A workspace that the call does not use would hold no status of it."""
+    monkeypatch.setattr(gdn, "_need", lambda *a: None)
+    with pytest.raises(ValueError, match="workspace has 255 bytes, the call needs 256"):
+        gdn._room(torch.zeros(255, dtype=torch.uint8), 256, torch.device("cpu"), None)
+    ws = torch.zeros(256, dtype=torch.uint8)
+    assert gdn._room(ws, 256, torch.device("cpu"), None) is ws
