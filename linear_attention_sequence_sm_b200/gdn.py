@@ -376,6 +376,7 @@ def chunk_forward(q, k, v, g, beta, initial_state=None, cu_seqlens=None, chunk_s
                                   dtype=torch.float32, device=dev)
     _need(final_state, "final_state", torch.float32, dev)
     nbytes = workspace_size(shape)
+    _need(workspace, "workspace", None, dev)  # (the library writes through its bare pointer)
     if workspace is None or workspace.numel() < nbytes:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     if output_norm is not None:
@@ -507,6 +508,7 @@ def kda_forward(q, k, v, g, beta, initial_state=None, cu_seqlens=None, output_fi
                                   dtype=torch.float32, device=dev)
     _need(final_state, "final_state", torch.float32, dev)
     nbytes = kda_workspace_size(shape)
+    _need(workspace, "workspace", None, dev)  # (the library writes through its bare pointer)
     if workspace is None or workspace.numel() < nbytes:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     osc = output_norm.c_struct(out) if output_norm is not None else None
@@ -624,6 +626,7 @@ def chunk_backward(q, k, v, g, beta, d_o, d_final_state=None, initial_state=None
     shape = make_shape(q, v, cu_seqlens, 32, force_simt=force_simt)
     n = ctypes.c_size_t(0)
     _check(LIB.gdn_chunk_backward_workspace_size(ctypes.byref(shape), ctypes.byref(n)))
+    _need(workspace, "workspace", None, dev)  # (the library writes through its bare pointer)
     if workspace is None or workspace.numel() < n.value:
         workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
     f32 = dict(dtype=torch.float32, device=dev)

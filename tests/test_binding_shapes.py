@@ -178,3 +178,20 @@ def test_stream_of_another_device_is_rejected():
         gdn._stream_handle(other, torch.device("cuda", 0))
     same = types.SimpleNamespace(device=torch.device("cuda", 0), cuda_stream=1234)
     assert gdn._stream_handle(same, torch.device("cuda", 0)).value == 1234
+
+
+@pytest.mark.parametrize("name", ["chunk_forward", "kda_forward", "chunk_backward"])
+def test_workspace_of_another_place(monkeypatch, name):
+    """A workspace on another device, or one whose elements share memory, is
+    refused like any tensor: the library would write its header through the
+    bare pointer.  (The checks of the other tensors are left out, so that CPU
+    tensors get as far as the workspace.)"""
+    from linear_attention_sequence_sm_b200 import gdn
+    need = gdn._need
+    monkeypatch.setattr(gdn, "_need", lambda t, n, *a: need(t, n, *a) if n == "workspace" else None)
+    x = prefill(g=torch.zeros(B, T, HV, DK)) if name == "kda_forward" else prefill()
+    more = (torch.zeros(B, T, HV, DV),) if name == "chunk_backward" else ()
+    for ws in (torch.zeros(1 << 22, dtype=torch.uint8), torch.zeros(1, dtype=torch.uint8).expand(1 << 22),
+               torch.zeros(1 << 22, dtype=torch.uint8, device="meta")):
+        with pytest.raises(ValueError, match="workspace must be"):
+            getattr(gdn, name)(x["q"], x["k"], x["v"], x["g"], x["beta"], *more, workspace=ws)
