@@ -39,10 +39,15 @@ struct SimtVec {
     float pad[3];
 };
 static_assert(sizeof(SimtVec) % 16 == 0, "tiles are 16-byte aligned");
-inline size_t simt_smem(int dy, int dz, bool state_only) {
+constexpr size_t simt_smem(int dy, int dz, bool state_only) {
     const size_t tiles = size_t(state_only ? 1 : 2) * C * pitch(dy) + size_t(C) * pitch(dz) + size_t(padded(dz)) * pitch(dy);
     return sizeof(SimtVec) + 4 * (tiles + (state_only ? 0 : C * LP));
 }
+// The most that any call asks for.  A kernel's limit is one value for all host
+// threads: set to a call's own size, another thread could lower it before this
+// call's launch, which would then be refused.
+constexpr size_t kSimtMaxSmem = simt_smem(128, 128, false);
+static_assert(kSimtMaxSmem <= 232448, "shared memory over the sm_100 per-block limit");
 
 // rows [0, L) of a [tokens, heads, d] tensor's head into a tile, the rest of
 // the 64 rows and of the columns up to a multiple of 8 zero
@@ -473,7 +478,7 @@ cudaError_t launch_decay_pass_simt(const DecayPass &p, const DecayPass *also, in
                                                : reinterpret_cast<const void *>(decay_pass_simt_kernel<float>);
     const size_t bytes = std::max(simt_smem(p.dy, p.dz, p.state_only),
                                   also ? simt_smem(also->dy, also->dz, also->state_only) : 0);
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSimtMaxSmem));
     if (e != cudaSuccess) return e;
     const dim3 grid(unsigned(std::min<int64_t>(max_units, kDecayPlanSms * 8)), also ? 2 : 1);
     if (dtype == GDN_DTYPE_BF16) decay_pass_simt_kernel<__nv_bfloat16><<<grid, kThreads, bytes, stream>>>(p, also ? *also : p);
