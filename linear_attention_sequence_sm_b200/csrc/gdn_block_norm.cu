@@ -1004,12 +1004,18 @@ Stages stages_of(const void *const *src, const int *size, int count, int width, 
     return s;
 }
 
+// Rows whose bytes are multiples of 16 (8 columns), and kFwdStages or
+// kBwdStages stages of which fit in shared memory, are staged.
+constexpr size_t kStageRoom = 220 * 1024;
+
 template <typename K>
 cudaError_t staged_launch(K kern, int stages, const BlockNormArgs &a, const Stages &sg, int grid, dim3 block,
                           cudaStream_t stream) {
     const size_t bytes = 64 + size_t(stages) * sg.stage_bytes;
     if (bytes > 40 * 1024) {  // (a kernel may have 48 KB in all without asking)
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+        // The limit is one value for all host threads: the most that any call asks for, never this call's own size,
+        // which another thread could lower before the launch.
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(64 + kStageRoom));
         if (e != cudaSuccess) return e;
     }
     kern<<<unsigned(grid), block, bytes, stream>>>(a, sg);
@@ -1017,9 +1023,6 @@ cudaError_t staged_launch(K kern, int stages, const BlockNormArgs &a, const Stag
     return cudaGetLastError();
 }
 
-// Rows whose bytes are multiples of 16 (8 columns), and two stages of which
-// fit in shared memory, are staged.
-constexpr size_t kStageRoom = 220 * 1024;
 bool aligned_rows(const BlockNormArgs &a) { return a.width % 8 == 0; }
 
 template <typename T, typename R>

@@ -76,3 +76,29 @@ def decay_call(shape, backward, dtype=torch.float32):
 @pytest.mark.parametrize("backward", [False, True])
 def test_decay_of_two_head_sizes(backward):
     run_together(decay_call((1, 1, 128, 128), backward), decay_call((1, 1, 33, 17), backward))
+
+
+def norm_call(rows, width, gate, backward):
+    from linear_attention_sequence_sm_b200 import gdn
+    gen = torch.Generator(device="cuda").manual_seed(72)
+    x, r, z, dh, dy = (torch.randn(rows, width, generator=gen, device="cuda") for _ in range(5))
+    z = z if gate else None
+    n = gdn.BlockNorm().c_struct(x, z)
+    nbytes = gdn.block_norm_workspace_size(rows, width)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    f32 = gdn.GDN_DTYPE_F32
+
+    def call(stream):
+        outs = [torch.empty_like(x), torch.empty_like(x)]
+        ins = [rows, width, f32, f32, p(x), p(r), p(z), ctypes.byref(n)]
+        if backward:
+            return gdn.LIB.gdn_block_norm_backward, [*ins, p(dh), p(dy), *map(p, outs), None, None, None, None, p(ws),
+                                                     nbytes, ctypes.c_void_p(stream)], outs
+        return gdn.LIB.gdn_block_norm_forward, [*ins, *map(p, outs), ctypes.c_void_p(stream)], outs
+    call.keep = (x, r, z, dh, dy, n)
+    return call
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_block_norms_of_two_widths(backward):
+    run_together(norm_call(3, 2048, True, backward), norm_call(3, 1800, False, backward))
