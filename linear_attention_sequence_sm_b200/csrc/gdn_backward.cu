@@ -608,6 +608,14 @@ size_t backward_ckpt_bytes(int32_t tokens, int32_t num_seqs, int32_t hv, int32_t
     return states + slots * size_t(hv) * n_slices * bwd_keep_floats(dk) * sizeof(float);
 }
 
+// The kernel's shared-memory limit, one value for all host threads: the most
+// that any call asks for, never a call's own size, which another thread could
+// lower before this call's launch.
+static int bwd_limit(bool tc) {
+    // (the padded row strides make no smaller head larger than 128)
+    return int(bwd_smem(128, tc).total * sizeof(float));
+}
+
 cudaError_t launch_chunk_backward(const PrefillArgs &a, const void *dO, const float *dSf, float *dq, float *dk,
                                   float *dv, float *dg, float *dbeta, float *dS0, float *ckpt, cudaStream_t stream) {
     const int n_slices = (a.dv + kBwdRows - 1) / kBwdRows;
@@ -621,13 +629,13 @@ cudaError_t launch_chunk_backward(const PrefillArgs &a, const void *dO, const fl
     cudaError_t e;
     if (a.dtype == GDN_DTYPE_BF16) {
         e = cudaFuncSetAttribute(chunk_backward_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 int(bytes));
+                                 bwd_limit(true));
         if (e != cudaSuccess) return e;
         chunk_backward_kernel<__nv_bfloat16><<<unsigned(blocks), kBwdThreads, bytes, stream>>>(
             a, dO, dSf, dq, dk, dv, dg, dbeta, dS0, ckpt, keep, n_slices);
     } else {
         e = cudaFuncSetAttribute(chunk_backward_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 int(bytes));
+                                 bwd_limit(false));
         if (e != cudaSuccess) return e;
         chunk_backward_kernel<float><<<unsigned(blocks), kBwdThreads, bytes, stream>>>(a, dO, dSf, dq, dk, dv, dg,
                                                                                       dbeta, dS0, ckpt, keep,

@@ -232,6 +232,11 @@ chunk_simt_kernel(PrefillArgs a, int n_slices) {
     }
 }
 
+// The kernel's shared-memory limit, one value for all host threads: the most
+// that any call asks for, never a call's own size, which another thread could
+// lower before this call's launch.
+static int simt_limit() { return int(simt_smem(64, 128).total_floats * sizeof(float)); }
+
 cudaError_t launch_chunk_simt(const PrefillArgs &a, cudaStream_t stream, int num_sms) {
     const SimtSmem L = simt_smem(a.chunk, a.dk);
     const size_t bytes = L.total_floats * sizeof(float);
@@ -240,9 +245,9 @@ cudaError_t launch_chunk_simt(const PrefillArgs &a, cudaStream_t stream, int num
     cudaError_t e;
     if (a.dtype == GDN_DTYPE_BF16)
         e = cudaFuncSetAttribute(chunk_simt_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 int(bytes));
+                                 simt_limit());
     else
-        e = cudaFuncSetAttribute(chunk_simt_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+        e = cudaFuncSetAttribute(chunk_simt_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, simt_limit());
     if (e != cudaSuccess) return e;
     const int per_sm = bytes > 110 * 1024 ? 1 : (bytes > 72 * 1024 ? 2 : 4);
     const int64_t grid = units < int64_t(num_sms) * per_sm ? units : int64_t(num_sms) * per_sm;

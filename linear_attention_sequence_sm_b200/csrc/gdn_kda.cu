@@ -367,7 +367,10 @@ template <typename T, uint32_t F>
 static void launch_kda_as(const PrefillArgs &a, int n_slices, unsigned grid, cudaStream_t stream) {
     if (a.dk % 8 == 0 && a.dv % 8 == 0) {
         const int bytes = 2 * KdaStageLayout<T>(a.dk).bytes;
-        cudaFuncSetAttribute(kda_prefill_staged_kernel<T, F>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        // The limit is one value for all host threads: the most that any call asks for (the widest heads), never this
+        // call's own size, which another thread could lower before the launch.
+        cudaFuncSetAttribute(kda_prefill_staged_kernel<T, F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             2 * KdaStageLayout<T>(kKdaMaxE * 32).bytes);
         kda_prefill_staged_kernel<T, F><<<grid, kKdaWarps * 32, bytes, stream>>>(a, n_slices);
     } else {
         kda_prefill_kernel<T, F><<<grid, kKdaWarps * 32, 0, stream>>>(a, n_slices);

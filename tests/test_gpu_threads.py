@@ -16,9 +16,9 @@ pytestmark = pytest.mark.gpu
 CALLS = 20_000
 
 
-def run_together(*calls):
+def run_together(*calls, bar=0.0):
     """Each call (stream -> (entry point, its arguments, outputs)) CALLS times in a thread of its own: refused by
-    none, and the outputs at the end what the call alone gives.  The arguments are made before, so that the threads
+    none, and the outputs at the end what the call alone gives (to ``bar``, in the 2-norm).  The arguments are made before, so that the threads
     spend their time inside the library."""
     from linear_attention_sequence_sm_b200 import gdn
     jobs = []
@@ -47,7 +47,7 @@ def run_together(*calls):
     torch.cuda.synchronize()
     assert not refused, refused
     for _, _, outs, want in jobs:
-        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+        assert all(float((a - b).norm()) <= bar * float(b.norm()) for a, b in zip(outs, want))
 
 
 def p(t):
@@ -102,3 +102,36 @@ def norm_call(rows, width, gate, backward):
 @pytest.mark.parametrize("backward", [False, True])
 def test_block_norms_of_two_widths(backward):
     run_together(norm_call(3, 2048, True, backward), norm_call(3, 1800, False, backward))
+
+
+def delta_call(kind, d, chunk=64):
+    from linear_attention_sequence_sm_b200 import gdn
+    gen = torch.Generator(device="cuda").manual_seed(73)
+    r = lambda *s: 0.3 * torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    q, k, v, do = (r(1, 3, 1, d) for _ in range(4))
+    g, beta = -r(1, 3, 1, d if kind == "kda" else 1).abs().reshape(1, 3, 1, -1), r(1, 3, 1).sigmoid()
+    sh = gdn.make_shape(q, v, None, 32 if kind == "backward" else chunk, force_simt=True)
+    size, fn = dict(chunk=(gdn.LIB.gdn_chunk_forward_workspace_size, gdn.LIB.gdn_chunk_forward),
+                    kda=(gdn.LIB.gdn_kda_forward_workspace_size, gdn.LIB.gdn_kda_forward),
+                    backward=(gdn.LIB.gdn_chunk_backward_workspace_size, gdn.LIB.gdn_chunk_backward))[kind]
+    nbytes = ctypes.c_size_t(0)
+    assert size(ctypes.byref(sh), ctypes.byref(nbytes)) == gdn.GDN_OK
+    ws = torch.empty(nbytes.value, dtype=torch.uint8, device="cuda")
+
+    def call(stream):
+        ins = [ctypes.byref(sh), p(q), p(k), p(v), p(g), p(beta), None, None]
+        tail = [p(ws), nbytes, ctypes.c_void_p(stream)]
+        if kind == "backward":
+            outs = [torch.empty_like(t) for t in (q, k, v, g, beta)]
+            return fn, [*ins, p(do), None, *map(p, outs), None, *tail], outs
+        outs = [torch.empty_like(v)]
+        return fn, [*ins, *([None] if kind == "kda" else []), p(outs[0]), None, *tail], outs
+    call.keep = (q, k, v, do, g, beta, sh, ws)
+    return call
+
+
+@pytest.mark.parametrize("kind", ["chunk", "kda", "backward"])
+def test_delta_rule_of_two_head_sizes(kind):
+    # (the delta rule's gradients add slices of the state by atomics, in any order: fp32 sums of a few hundred terms)
+    run_together(delta_call(kind, 128), delta_call(kind, 32, 16 if kind == "chunk" else 64),
+                 bar=256 * R.U32 if kind == "backward" else 0.0)
