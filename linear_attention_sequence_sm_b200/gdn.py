@@ -735,6 +735,22 @@ def _room(workspace, nbytes, dev, stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=dev)
 
 
+def _new(stream, dev, make, *args, **kw):
+    """``make(*args, **kw)``, a tensor for the call to write, in memory of the
+    call's stream: what the current stream's work was given may still be in
+    use there, and what the call's stream still uses must not be given to the
+    current one.  The current stream may read it behind the call, so the
+    memory also waits for that stream's work when the tensor is dropped."""
+    if stream is None:
+        return make(*args, **kw)
+    _stream_handle(stream, dev)  # (refuses another device's stream)
+    here = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        t = make(*args, **kw)
+    t.record_stream(here)
+    return t
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -797,10 +813,10 @@ def decay_forward(q, k, v, g, initial_state=None, cu_seqlens=None, output_final_
     _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
     shape = make_shape(q, v, cu_seqlens, 64, force_simt)
     if out is None:
-        out = torch.empty_like(v)
+        out = _new(stream, dev, torch.empty_like, v)
     if final_state is None and output_final_state:
-        final_state = torch.empty_like(initial_state) if initial_state is not None else \
-            torch.empty((n_seqs, hv, dv, dk), dtype=torch.float32, device=dev)
+        final_state = _new(stream, dev, torch.empty_like, initial_state) if initial_state is not None else \
+            _new(stream, dev, torch.empty, (n_seqs, hv, dv, dk), dtype=torch.float32, device=dev)
     workspace = _room(workspace, decay_workspace_size(shape), dev, stream)
     osc = output_norm.c_struct(out) if output_norm is not None else None
     with _on(dev):  # the library launches on the current device
@@ -832,7 +848,7 @@ def decay_decode_step(q, k, v, g, state, out=None, stream=None, output_norm: Out
         _need(g, "g", torch.float32, dev)
         _need(state, "state", torch.float32, dev)
     if out is None:
-        out = torch.empty_like(v)
+        out = _new(stream, dev, torch.empty_like, v)
     N, hk, dk = qs
     hv, dv = vs[1], vs[2]
     osc = output_norm.c_struct(out) if output_norm is not None else None
@@ -861,9 +877,9 @@ def decay_backward(q, k, v, g, d_o, d_final_state=None, initial_state=None, cu_s
     _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
     shape = make_shape(q, v, cu_seqlens, 64, force_simt)
     workspace = _room(workspace, decay_workspace_size(shape, backward=True), dev, stream)
-    out = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
-           "dg": torch.empty_like(g) if want_dg else None,
-           "d_initial_state": torch.empty((n_seqs, hv, dv, dk), dtype=torch.float32, device=dev)
+    like = lambda t: _new(stream, dev, torch.empty_like, t)  # noqa: E731
+    out = {"dq": like(q), "dk": like(k), "dv": like(v), "dg": like(g) if want_dg else None,
+           "d_initial_state": _new(stream, dev, torch.empty, (n_seqs, hv, dv, dk), dtype=torch.float32, device=dev)
            if want_d_initial_state else None}
     with _on(dev):  # the library launches on the current device
         _check(LIB.gdn_decay_backward(ctypes.byref(shape), _addr(q), _addr(k), _addr(v), _addr(g), layout,
@@ -952,12 +968,12 @@ def block_norm_forward(x, residual, norm: BlockNorm, gate=None, h=None, y=None, 
         raise ValueError("y needs pre_norm")
     more = () if h is None and y is None else ((h, "h", True), (y, "y", False))
     rows, width, rt = _block_norm_inputs(x, residual, norm, gate, more)
-    if h is None:
-        h = torch.empty_like(x if residual is None else residual)
-    if y is None and norm.pre_norm:
-        y = torch.empty_like(x)
-    c = norm.c_struct(x, gate)
     dev = x.device
+    if h is None:
+        h = _new(stream, dev, torch.empty_like, x if residual is None else residual)
+    if y is None and norm.pre_norm:
+        y = _new(stream, dev, torch.empty_like, x)
+    c = norm.c_struct(x, gate)
     with _on(dev):  # the library launches on the current device
         _check(LIB.gdn_block_norm_forward(rows, width, _dtype_code(x), _dtype_code(h), x.data_ptr(), _addr(residual),
                                           _addr(gate), ctypes.byref(c), h.data_ptr(), _addr(y),
@@ -982,13 +998,13 @@ def block_norm_backward(x, residual, norm: BlockNorm, gate=None, d_h=None, d_y=N
     if d_y is not None and not norm.pre_norm:
         raise ValueError("d_y needs pre_norm")
     rows, width, rt = _block_norm_inputs(x, residual, norm, gate, ((d_h, "d_h", True), (d_y, "d_y", False)))
-    workspace = _room(workspace, block_norm_workspace_size(rows, width), x.device, stream)
-    like = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
-    out = {"dx": torch.empty_like(x), "d_residual": like(residual), "d_gate": like(gate),
+    dev = x.device
+    workspace = _room(workspace, block_norm_workspace_size(rows, width), dev, stream)
+    like = lambda t: None if t is None else _new(stream, dev, torch.empty_like, t)  # noqa: E731
+    out = {"dx": like(x), "d_residual": like(residual), "d_gate": like(gate),
            "d_post_weight": like(norm.post_weight), "d_scale": like(norm.scale), "d_pre_weight": like(norm.pre_weight)}
     c = norm.c_struct(x, gate)
     code = GDN_DTYPE_F32 if rt == torch.float32 else GDN_DTYPE_BF16
-    dev = x.device
     with _on(dev):  # the library launches on the current device
         _check(LIB.gdn_block_norm_backward(rows, width, _dtype_code(x), code, _addr(x), _addr(residual), _addr(gate),
                                            ctypes.byref(c), _addr(d_h), _addr(d_y), _addr(out["dx"]),

@@ -12,6 +12,7 @@ import pytest
 import torch
 
 import decay_ref as R
+import streams
 
 pytestmark = pytest.mark.gpu
 
@@ -429,3 +430,28 @@ def test_two_calls_at_once():
         for f, b in runs:
             assert torch.equal(f[0], wf[0]) and torch.equal(f[1], wf[1])
             assert all(torch.equal(b[k], wb[k]) for k in wb)
+
+
+def test_outputs_belong_to_the_calls_stream():
+    from linear_attention_sequence_sm_b200 import gdn
+    d = R.make(51, 1, 2, 128, 128, torch.bfloat16, lens=[300, 64])
+    c = R.cuda(d)
+    rows = c["v"].reshape(-1, 256).contiguous()
+    one = {k: c[k][:2].contiguous() for k in ("q", "k", "v", "g")}
+    norm, state = gdn.BlockNorm(), c["s0"].clone()
+
+    def decode(s):
+        with torch.cuda.stream(s):
+            state.copy_(c["s0"])
+        return [gdn.decay_decode_step(one["q"], one["k"], one["v"], one["g"], state, stream=s)]
+
+    calls = [
+        lambda s: gdn.decay_forward(c["q"], c["k"], c["v"], c["g"], initial_state=c["s0"], cu_seqlens=c["cu"], stream=s),
+        decode,
+        lambda s: list(gdn.decay_backward(c["q"], c["k"], c["v"], c["g"], c["do"], d_final_state=c["dsf"],
+                                          initial_state=c["s0"], cu_seqlens=c["cu"], stream=s).values()),
+        lambda s: gdn.block_norm_forward(rows, rows, norm, stream=s),
+        lambda s: [t for t in gdn.block_norm_backward(rows, rows, norm, d_h=rows, d_y=rows, stream=s).values()
+                   if t is not None],
+    ]
+    streams.check_outputs_belong_to_the_calls_stream(calls)
