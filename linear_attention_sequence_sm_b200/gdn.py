@@ -369,16 +369,15 @@ def chunk_forward(q, k, v, g, beta, initial_state=None, cu_seqlens=None, chunk_s
     shape = make_shape(q, v, cu_seqlens, chunk_size, force_simt, input_flags(qk_l2norm, gate_logits), one_kernel,
                        split)
     if out is None:
-        out = torch.empty(v.shape, dtype=dt, device=dev)
+        out = _new(stream, dev, torch.empty, v.shape, dtype=dt, device=dev)
     _need(out, "out", dt, dev)
     if final_state is None and output_final_state:
-        final_state = torch.empty((shape.num_seqs, shape.num_v_heads, shape.head_dim_v, shape.head_dim_k),
-                                  dtype=torch.float32, device=dev)
+        final_state = _new(stream, dev, torch.empty, (n_seqs, hv, dv, dk), dtype=torch.float32, device=dev)
     _need(final_state, "final_state", torch.float32, dev)
     nbytes = workspace_size(shape)
     _need(workspace, "workspace", None, dev)  # (the library writes through its bare pointer)
     if workspace is None or workspace.numel() < nbytes:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        workspace = _room(None, nbytes, dev, stream)
     if output_norm is not None:
         osc = output_norm.c_struct(out)
         with torch.cuda.device(dev):  # the library launches on the current device
@@ -415,11 +414,10 @@ def chunk_forward_noalloc(q, k, v, g, beta, initial_state=None, cu_seqlens=None,
     _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
     shape = make_shape(q, v, cu_seqlens, chunk_size, force_simt, input_flags(qk_l2norm, gate_logits))
     if out is None:
-        out = torch.empty(v.shape, dtype=dt, device=dev)
+        out = _new(stream, dev, torch.empty, v.shape, dtype=dt, device=dev)
     _need(out, "out", dt, dev)
     if final_state is None and output_final_state:
-        final_state = torch.empty((shape.num_seqs, shape.num_v_heads, shape.head_dim_v, shape.head_dim_k),
-                                  dtype=torch.float32, device=dev)
+        final_state = _new(stream, dev, torch.empty, (n_seqs, hv, dv, dk), dtype=torch.float32, device=dev)
     _need(final_state, "final_state", torch.float32, dev)
     with torch.cuda.device(dev):  # the library launches on the current device
         _check(LIB.gdn_chunk_forward_noalloc(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
@@ -462,7 +460,7 @@ def decode_step(q, k, v, g, beta, state, out=None, stream=None, qk_l2norm=False,
     _need(beta, "beta", torch.float32, dev)
     _need(state, "state", torch.float32, dev)
     if out is None:
-        out = torch.empty(v.shape, dtype=dt, device=dev)
+        out = _new(stream, dev, torch.empty, v.shape, dtype=dt, device=dev)
     _need(out, "out", dt, dev)
     N, hk, dk = q.shape
     hv, dv = v.shape[1], v.shape[2]
@@ -501,16 +499,15 @@ def kda_forward(q, k, v, g, beta, initial_state=None, cu_seqlens=None, output_fi
     _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
     shape = make_shape(q, v, cu_seqlens, chunk_size, force_simt, input_flags(qk_l2norm, gate_logits))
     if out is None:
-        out = torch.empty(v.shape, dtype=dt, device=dev)
+        out = _new(stream, dev, torch.empty, v.shape, dtype=dt, device=dev)
     _need(out, "out", dt, dev)
     if final_state is None and output_final_state:
-        final_state = torch.empty((shape.num_seqs, shape.num_v_heads, shape.head_dim_v, shape.head_dim_k),
-                                  dtype=torch.float32, device=dev)
+        final_state = _new(stream, dev, torch.empty, (n_seqs, hv, dv, dk), dtype=torch.float32, device=dev)
     _need(final_state, "final_state", torch.float32, dev)
     nbytes = kda_workspace_size(shape)
     _need(workspace, "workspace", None, dev)  # (the library writes through its bare pointer)
     if workspace is None or workspace.numel() < nbytes:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        workspace = _room(None, nbytes, dev, stream)
     osc = output_norm.c_struct(out) if output_norm is not None else None
     with torch.cuda.device(dev):  # the library launches on the current device
         _check(LIB.gdn_kda_forward(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
@@ -535,7 +532,7 @@ def kda_decode_step(q, k, v, g, beta, state, out=None, stream=None, qk_l2norm=Fa
     N, hk, dk = q.shape
     hv, dv = v.shape[1], v.shape[2]
     if out is None:
-        out = torch.empty(v.shape, dtype=dt, device=dev)
+        out = _new(stream, dev, torch.empty, v.shape, dtype=dt, device=dev)
     _need(out, "out", dt, dev)
     osc = output_norm.c_struct(out) if output_norm is not None else None
     with torch.cuda.device(dev):  # the library launches on the current device
@@ -571,9 +568,9 @@ def decode_multi(q, k, v, g, beta, state, out=None, snapshots=None, stream=None,
     N, K, hk, dk = q.shape
     hv, dv = v.shape[2], v.shape[3]
     if out is None:
-        out = torch.empty(v.shape, dtype=dt, device=dev)
+        out = _new(stream, dev, torch.empty, v.shape, dtype=dt, device=dev)
     if snapshots is None:
-        snapshots = torch.empty((N, K, hv, dv, dk), dtype=torch.float32, device=dev)
+        snapshots = _new(stream, dev, torch.empty, (N, K, hv, dv, dk), dtype=torch.float32, device=dev)
     _need(out, "out", dt, dev)
     _need(snapshots, "snapshots", torch.float32, dev)
     with torch.cuda.device(dev):  # the library launches on the current device
@@ -628,12 +625,10 @@ def chunk_backward(q, k, v, g, beta, d_o, d_final_state=None, initial_state=None
     _check(LIB.gdn_chunk_backward_workspace_size(ctypes.byref(shape), ctypes.byref(n)))
     _need(workspace, "workspace", None, dev)  # (the library writes through its bare pointer)
     if workspace is None or workspace.numel() < n.value:
-        workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
-    f32 = dict(dtype=torch.float32, device=dev)
-    out = {"dq": torch.empty(q.shape, **f32), "dk": torch.empty(k.shape, **f32), "dv": torch.empty(v.shape, **f32),
-           "dg": torch.empty(g.shape, **f32), "dbeta": torch.empty(beta.shape, **f32),
-           "d_initial_state": torch.empty((shape.num_seqs, shape.num_v_heads, shape.head_dim_v, shape.head_dim_k),
-                                          **f32) if want_d_initial_state else None}
+        workspace = _room(None, n.value, dev, stream)
+    f32 = lambda shape: _new(stream, dev, torch.empty, shape, dtype=torch.float32, device=dev)  # noqa: E731
+    out = {"dq": f32(q.shape), "dk": f32(k.shape), "dv": f32(v.shape), "dg": f32(g.shape), "dbeta": f32(beta.shape),
+           "d_initial_state": f32((n_seqs, hv, dv, dk)) if want_d_initial_state else None}
     with torch.cuda.device(dev):  # the library launches on the current device
         _check(LIB.gdn_chunk_backward(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
                                       _ptr(initial_state), _ptr(cu_seqlens), _ptr(d_o), _ptr(d_final_state),
@@ -678,10 +673,10 @@ def short_conv(x, weight, cu_seqlens=None, state=None, silu=True, out=None, stat
     _need(state, "state", torch.float32, dev)
     _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
     if out is None:
-        out = torch.empty_like(x)
+        out = _new(stream, dev, torch.empty_like, x)
     _need(out, "out", dt, dev)
     if state_out is None and want_state:
-        state_out = torch.empty((n_seqs, *ch, width - 1), dtype=torch.float32, device=dev)
+        state_out = _new(stream, dev, torch.empty, (n_seqs, *ch, width - 1), dtype=torch.float32, device=dev)
     _need(state_out, "state_out", torch.float32, dev)
     channels = 1
     for c in ch:
