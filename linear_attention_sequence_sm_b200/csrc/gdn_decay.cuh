@@ -26,13 +26,15 @@
 // (do_i . v_j) of all pairs j < t <= i.  Inside t's chunk they are summed
 // directly; pairs with one end in the chunk are q_i . dq_i's and k_j . dk_j's
 // parts that come from the chunk's start and end states (`dot` below), and
-// pairs that span the chunk follow from <dS, S> at its start, known exactly
-// at checkpoints every `ick` tokens and carried from chunk to chunk by taking
-// off and adding the one-ended sums.  (The shorter dg_t = dg_{t+1} + q_t .
-// dq_t - k_t . dk_t over the whole sequence loses digits where decays are
-// strong: its terms hold the undecayed q_t . k_t, and cancel.  So would
-// <dS, S> at a chunk's end: at the last one it holds the undecayed pairs of
-// the last token and the final state's gradient.)
+// the pairs that span the chunk are e^{G_last} <dS at its end, S at its start>:
+// the pass forward in time keeps each chunk's start state, the one backward in
+// time multiplies it with dS.  Every part is a sum of decayed terms and none is
+// taken off, so a token whose decay is far stronger than its neighbours' keeps
+// the digits of its small gradient.  (dg_t = dg_{t+1} + q_t . dq_t - k_t . dk_t
+// over the sequence cancels there, and so does carrying the pairs across a
+// chunk's start from one chunk to the next: with g = -15 among -0.01, dg = 2.5e-5
+// is what remains of some 80 in fp32.  The states cost 64 KB a chunk and head,
+// written once and read once.)
 #pragma once
 
 #include "gdn_internal.cuh"
@@ -41,7 +43,7 @@ namespace gdn {
 
 constexpr int kDecayChunk = 64;      // tokens of a chunk
 constexpr int kDecayMinSeg = 256;    // shortest segment a split sequence is cut into
-constexpr int kDecayMaxIck = 1024;   // checkpoint spacing of the decays' gradient (tokens)
+constexpr int kDecayMaxTokens = INT32_MAX - 2048;  // (positions past a sequence's end stay in 32 bits)
 constexpr int kDecayPlanSms = 148;   // SMs the split aims to fill (B200)
 
 // A log-decay as the recurrence uses it.  A NaN stays one (fmaxf would make it
@@ -58,15 +60,15 @@ struct DecaySeg {
     int32_t start, len;     // first token (of all tokens) and token count
     int32_t pos, seq_len;   // offset in the sequence, the sequence's length
     int32_t seq, slot;      // sequence; slot of its start state, -1 for an uncut sequence
-    int32_t ck;             // first checkpoint slot of the sequence
+    int32_t chunk;          // chunks before the sequence
     int32_t pad;
 };
 
 // Header of the workspace (shares its status word with the other operators').
 struct DecayHeader {
     int32_t status, bad_index;
-    int32_t num_segs, num_split, ick, seg_len, num_cks, total_chunks;
-    int32_t pad[56];
+    int32_t num_segs, num_split, seg_len, total_chunks;
+    int32_t pad[58];
 };
 static_assert(sizeof(DecayHeader) == 256, "header must be 256 bytes");
 
@@ -75,18 +77,17 @@ struct DecaySched {
     DecaySeg *segs;         // [max_segs], longest sequences first
     int32_t *split;         // [max_split] first segment of each cut sequence
     int32_t *chunk_base;    // [N + 1] chunks before each sequence
-    int32_t *ck_base;       // [N + 1] checkpoint slots before each sequence
 };
 
 // Workspace (offsets 256-byte aligned).  Every bound is a function of the
 // shape alone; see decay_layout for the arithmetic.
 struct DecayLayout {
-    size_t segs_off, split_off, cbase_off, ckbase_off, order_off;
+    size_t segs_off, split_off, cbase_off, order_off;
     size_t state_off[2];    // start states of cut sequences, [slots][Hv][128][128] fp32 (backward: two directions)
     size_t segdec_off[2];   // [slots][Hv] decay across each segment (each direction writes its own)
-    size_t ckpt_off, zsum_off, dot_off[2], intra_off, part_off[2], dgtok_off;
+    size_t start_off, span_off, dot_off[2], intra_off, part_off[2], dgtok_off;
     size_t total;
-    int64_t max_segs, max_split, max_slots, max_cks, max_ckpt, max_chunks;
+    int64_t max_segs, max_split, max_slots, max_starts, max_chunks;
 };
 DecayLayout decay_layout(const gdn_shape_t &s, bool backward);
 
@@ -108,12 +109,12 @@ struct DecayPass {
     void *out;                    // [tokens, hv, dz]
     int32_t out_f32;              // 32-bit out whatever the inputs' type
     float *dot;                   // [hv][tokens], or NULL
-    // States at positions p > 0 that are multiples of `ick`, or NULL: [tokens / ick + 1][hv][128 * 128], at slot
-    // (token / ick).  Two of them are at least ick tokens apart, whatever the sequences, so no slot is used twice;
-    // the state at p = 0 is s_first.
-    float *ckpt;
-    float *zsum;                  // backward in time: <Sigma, checkpoint>, [cks][hv][8 parts]; NULL: write checkpoints
-    const float *s_first;         // the checkpoint at a sequence's start, stored as s_in, or NULL for zeros
+    // Start states of the chunks behind a sequence's first, or NULL: [tokens / 64 + 1][hv][a state], at slot
+    // (first token / 64), in an order of the pass's own.  Two of them are at least 64 tokens apart, whatever the sequences, so no slot is used twice;
+    // a sequence's first is s_first.
+    float *starts;
+    float *span;                  // backward in time: e^G <Sigma, start state>, [chunks][hv][8 parts]; NULL: write starts
+    const float *s_first;         // a sequence's first start state, stored as s_in, or NULL for zeros
     DecaySched sched;
 };
 
@@ -145,7 +146,7 @@ cudaError_t launch_decay_intra(const gdn_shape_t &s, const int32_t *cu, const De
 
 // dg from its parts, and the sums over grouped value heads.
 cudaError_t launch_decay_dg(const gdn_shape_t &s, const int32_t *cu, const DecayLayout &L, const DecaySched &sc, const float *dot_q,
-                            const float *dot_k, const float *intra, const float *zsum, const float *g, bool g_const,
+                            const float *dot_k, const float *intra, const float *span, const float *g, bool g_const,
                             float *dg_tok, float *dg, cudaStream_t stream);
 cudaError_t launch_decay_group_sum(const DecayHeader *hdr, const float *part, void *out, int64_t tokens, int32_t hk,
                                    int32_t hv, int32_t d, int32_t dtype, cudaStream_t stream);

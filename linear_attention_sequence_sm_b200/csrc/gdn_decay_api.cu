@@ -21,8 +21,8 @@ gdn_status_t check_decay_shape(const gdn_shape_t *s, const int32_t *cu_seqlens, 
         return fail(GDN_ERR_UNSUPPORTED, "the decayed linear attention uses chunks of %d tokens (got %d)", kDecayChunk,
                     s->chunk_size);
     if (s->num_v_heads > 65535) return fail(GDN_ERR_UNSUPPORTED, "more than 65535 value heads");
-    if (int64_t(s->batch) * s->seq_len > INT32_MAX - 2 * kDecayMaxIck)  // (positions past a sequence's end stay in 32 bits)
-        return fail(GDN_ERR_UNSUPPORTED, "more than 2^31 - %d tokens", 2 * kDecayMaxIck + 1);
+    if (int64_t(s->batch) * s->seq_len > kDecayMaxTokens)
+        return fail(GDN_ERR_UNSUPPORTED, "more than %d tokens", kDecayMaxTokens);
     if (s->num_seqs > (1 << 24)) return fail(GDN_ERR_UNSUPPORTED, "more than 2^24 sequences");
     if (layout_known) {
         if (cu_seqlens) {
@@ -270,11 +270,11 @@ gdn_status_t gdn_decay_backward(const gdn_shape_t *s, const void *q, const void 
     pk.s_out = d_initial_state;
     if (dg) {
         pq.aux = q; pq.haux = hk; pq.dot = at(L.dot_off[0]);
-        pq.ckpt = at(L.ckpt_off);
+        pq.starts = at(L.start_off);
         pk.s_first = initial_state;
         pk.aux = k; pk.haux = hk; pk.dot = at(L.dot_off[1]);
-        pk.ckpt = at(L.ckpt_off);
-        pk.zsum = at(L.zsum_off);
+        pk.starts = at(L.start_off);
+        pk.span = at(L.span_off);
     }
     // dv: out_t = dS_t k_t, backward in time
     DecayPass pv = base;
@@ -288,7 +288,7 @@ gdn_status_t gdn_decay_backward(const gdn_shape_t *s, const void *q, const void 
     pv.seg_state = at(L.state_off[1]);
     pv.seg_trans = 1;
     pv.out = dv;
-    // (dk's decay sums read the checkpoints that dq's pass writes)
+    // (dk's pass reads the start states that dq's pass writes)
     if ((e = run_pass(pq, *s, units, stream, &pv)) != cudaSuccess || (e = run_pass(pk, *s, units, stream)) != cudaSuccess)
         return cuda_fail(e, "backward launch");
     if (tokens == 0) return GDN_OK;
@@ -297,7 +297,7 @@ gdn_status_t gdn_decay_backward(const gdn_shape_t *s, const void *q, const void 
                 ? launch_decay_intra(*s, cu_seqlens, L, sc, q, k, v, d_o, g, base.g_const, at(L.intra_off), stream)
                 : launch_decay_intra_simt(*s, cu_seqlens, L, sc, q, k, v, d_o, g, base.g_const, at(L.intra_off), stream);
         if (e == cudaSuccess)
-            e = launch_decay_dg(*s, cu_seqlens, L, sc, pq.dot, pk.dot, at(L.intra_off), pk.zsum, g, base.g_const,
+            e = launch_decay_dg(*s, cu_seqlens, L, sc, pq.dot, pk.dot, at(L.intra_off), pk.span, g, base.g_const,
                                 at(L.dgtok_off), dg, stream);
         if (e != cudaSuccess) return cuda_fail(e, "decay gradient launch");
     }

@@ -77,7 +77,7 @@ __device__ void block_scan(int (&v)[kN], int (&totals)[kN], int *part) {
 // ceil(longest / floor(longest / B)) tokens, rounded up, whose start states come from a
 // first sweep over all segments but one end's (k and v are then read twice, a
 // third of the prefill's traffic; the uncut chain would take at least twice as
-// long).  At 1 x 65,536 tokens and 48 heads: 3 segments of 22,528 tokens.
+// long).  At 1 x 65,536 tokens and 48 heads: 3 segments of 21,888 tokens.
 __global__ void __launch_bounds__(kSchedThreads)
 decay_schedule_kernel(int32_t num_seqs, int32_t tokens, int32_t batched_len, int32_t hv, DecayPlan plan,
                       const int32_t *__restrict__ cu, DecaySched sc, int32_t *order) {
@@ -90,8 +90,7 @@ decay_schedule_kernel(int32_t num_seqs, int32_t tokens, int32_t batched_len, int
         longest = 0;
         hdr->status = GDN_OK;
         hdr->bad_index = -1;
-        hdr->num_segs = hdr->num_split = hdr->num_cks = hdr->total_chunks = 0;
-        hdr->ick = kDecayMaxIck;
+        hdr->num_segs = hdr->num_split = hdr->total_chunks = 0;
         hdr->seg_len = 0;
     }
     __syncthreads();
@@ -116,18 +115,15 @@ decay_schedule_kernel(int32_t num_seqs, int32_t tokens, int32_t batched_len, int
         }
         return;
     }
-    // segment length and checkpoint spacing
-    int seg_len = INT32_MAX, ick = kDecayMaxIck;
+    // segment length: whole chunks
+    int seg_len = INT32_MAX;
     {
         const int64_t balanced = balanced_tokens(tokens, hv, plan.ways);
         const int64_t k = balanced > 0 ? longest / balanced : 1;
         if (k >= 2 && longest > plan.min_seg) {
             int64_t L = (longest + k - 1) / k;
-            // cuts fall on checkpoints: one a segment up to 1024 tokens, then every 1024
-            const int64_t unit = L <= kDecayMaxIck ? kDecayChunk : kDecayMaxIck;
-            L = max(int64_t(plan.min_seg), (L + unit - 1) / unit * unit);
+            L = max(int64_t(plan.min_seg), (L + kDecayChunk - 1) / kDecayChunk * kDecayChunk);
             seg_len = int(L);
-            ick = min(seg_len, kDecayMaxIck);
         }
     }
     // longest first, ties by index
@@ -144,23 +140,18 @@ decay_schedule_kernel(int32_t num_seqs, int32_t tokens, int32_t batched_len, int
         }
         order[r] = n;
     }
-    // chunks and checkpoint slots before each sequence: each thread takes a run of sequences
+    // chunks before each sequence: each thread takes a run of sequences
     const int per = (num_seqs + kSchedThreads - 1) / kSchedThreads;
     const int n0 = min(num_seqs, int(threadIdx.x) * per), n1 = min(num_seqs, n0 + per);
-    int two[2] = {0, 0}, total2[2];
-    for (int n = n0; n < n1; ++n) {
-        two[0] += (len_of(n) + kDecayChunk - 1) / kDecayChunk;
-        two[1] += (len_of(n) + ick - 1) / ick;
-    }
-    block_scan(two, total2, part);
-    int chunks = two[0], cks = two[1];
+    int one[1] = {0}, total1[1];
+    for (int n = n0; n < n1; ++n) one[0] += (len_of(n) + kDecayChunk - 1) / kDecayChunk;
+    block_scan(one, total1, part);
+    int chunks = one[0];
     for (int n = n0; n < n1; ++n) {
         sc.chunk_base[n] = chunks;
-        sc.ck_base[n] = cks;
         chunks += (len_of(n) + kDecayChunk - 1) / kDecayChunk;
-        cks += (len_of(n) + ick - 1) / ick;
     }
-    __syncthreads();  // order, ck_base
+    __syncthreads();  // order, chunk_base
     // segments, sequences by rank
     auto segs_of = [&](int n) { return len_of(n) <= seg_len ? 1 : (len_of(n) + seg_len - 1) / seg_len; };
     int three[3] = {0, 0, 0}, total3[3];
@@ -183,20 +174,17 @@ decay_schedule_kernel(int32_t num_seqs, int32_t tokens, int32_t batched_len, int
             g.seq_len = len;
             g.seq = n;
             g.slot = c > 1 ? slots++ : -1;
-            g.ck = sc.ck_base[n];
+            g.chunk = sc.chunk_base[n];
             g.pad = 0;
             sc.segs[segs++] = g;
         }
     }
     if (threadIdx.x == 0) {
-        sc.chunk_base[num_seqs] = total2[0];
-        sc.ck_base[num_seqs] = total2[1];
+        sc.chunk_base[num_seqs] = total1[0];
         hdr->num_segs = total3[0];
         hdr->num_split = total3[1];
-        hdr->ick = ick;
         hdr->seg_len = seg_len;
-        hdr->num_cks = total2[1];
-        hdr->total_chunks = total2[0];
+        hdr->total_chunks = total1[0];
     }
 }
 
@@ -247,68 +235,47 @@ decay_combine_kernel(DecaySched sc, float *__restrict__ states, const float *__r
     }
 }
 
-// The decays' gradient: one warp per (checkpoint interval, head), its chunks
-// first to last (the three values a token needs are read a chunk ahead; 4 x
-// 4096 tokens x 32 heads: 28 us, 16 dependent chunks a warp).  For token t of a chunk with both-outside weight Y:
-//   dg_t = intra_t + sum_{i >= t} dot_q_i + sum_{j < t} dot_k_j + Y,
-// Y = (pairs across the chunk's start) - sum dot_q, and the pairs across its
-// end are Y + sum dot_k.  At an interval's start the pairs across are zsum.
+// The decays' gradient: one warp per (chunk, head), two tokens a lane.  For
+// token t of the chunk
+//   dg_t = intra_t + sum_{i >= t} dot_q_i + sum_{j < t} dot_k_j + span.
 __global__ void __launch_bounds__(128)
 decay_dg_kernel(int num_seqs, int hv, int tokens, const int32_t *__restrict__ cu, int batched_len, DecaySched sc,
                 const float *__restrict__ dot_q, const float *__restrict__ dot_k, const float *__restrict__ intra,
-                const float *__restrict__ zsum, const float *__restrict__ g, int g_const, float *__restrict__ dg_tok,
+                const float *__restrict__ span, const float *__restrict__ g, int g_const, float *__restrict__ dg_tok,
                 float *__restrict__ dg) {
     if (sc.hdr->status != GDN_OK) return;
     const int lane = threadIdx.x & 31;
-    const int ick = sc.hdr->ick;
-    const int64_t units = int64_t(sc.hdr->num_cks) * hv;
+    const int64_t units = int64_t(sc.hdr->total_chunks) * hv;
     for (int64_t u = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5); u < units; u += int64_t(gridDim.x) * 4) {
-        const int ck = int(u / hv), h = int(u % hv);
-        const int n = chunk_sequence(sc.ck_base, num_seqs, ck);
+        const int gc = int(u / hv), h = int(u % hv);
+        const int n = chunk_sequence(sc.chunk_base, num_seqs, gc);
         const int start = cu ? cu[n] : n * batched_len, len = cu ? cu[n + 1] - cu[n] : batched_len;
-        const int p0 = (ck - sc.ck_base[n]) * ick, p1 = min(len, p0 + ick);
-        const float *dq = dot_q + size_t(h) * tokens + start, *dk = dot_k + size_t(h) * tokens + start;
-        const float *in = intra + size_t(h) * tokens + start;
-        float across = 0.f;
-        for (int e = 0; e < 8; ++e) across += zsum[(size_t(ck) * hv + h) * 8 + e];
-        float2 nq, nk, ni;  // this lane's two tokens of the next chunk
-        auto fetch = [&](int b) {
-            const int t = b + 2 * lane;
-            const bool v0 = t < p1, v1 = t + 1 < p1;
-            nq = make_float2(v0 ? dq[t] : 0.f, v1 ? dq[t + 1] : 0.f);
-            nk = make_float2(v0 ? dk[t] : 0.f, v1 ? dk[t + 1] : 0.f);
-            ni = make_float2(v0 ? in[t] : 0.f, v1 ? in[t + 1] : 0.f);
-        };
-        fetch(p0);
-        for (int b = p0; b < p1; b += kDecayChunk) {
-            const int t0 = b + 2 * lane;
-            const float q0 = nq.x, q1 = nq.y, k0 = nk.x, k1 = nk.y;
-            const float2 ii = ni;
-            fetch(b + kDecayChunk);
-            float qs = q0 + q1, ks = k0 + k1;  // inclusive: qs from the end, ks from the start
+        const int t0 = (gc - sc.chunk_base[n]) * kDecayChunk + 2 * lane;
+        const size_t at = size_t(start) + t0, of = size_t(h) * tokens + at;
+        const bool v0 = t0 < len, v1 = t0 + 1 < len;
+        const float q0 = v0 ? dot_q[of] : 0.f, q1 = v1 ? dot_q[of + 1] : 0.f;
+        const float k0 = v0 ? dot_k[of] : 0.f, k1 = v1 ? dot_k[of + 1] : 0.f;
+        const float i0 = v0 ? intra[of] : 0.f, i1 = v1 ? intra[of + 1] : 0.f;
+        const float *sp = span + (size_t(gc) * hv + h) * 8;
+        const float outside = ((sp[0] + sp[1]) + (sp[2] + sp[3])) + ((sp[4] + sp[5]) + (sp[6] + sp[7]));
+        float qs = q0 + q1, ks = k0 + k1;  // inclusive: qs from the end, ks from the start
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const float a = __shfl_down_sync(0xffffffffu, qs, d), e = __shfl_up_sync(0xffffffffu, ks, d);
-                if (lane + d < 32) qs += a;
-                if (lane >= d) ks += e;
-            }
-            const float qsum = __shfl_sync(0xffffffffu, qs, 0), ksum = __shfl_sync(0xffffffffu, ks, 31);
-            const float outside = across - qsum;
-            float q_after = __shfl_down_sync(0xffffffffu, qs, 1), k_before = __shfl_up_sync(0xffffffffu, ks, 1);
-            if (lane == 31) q_after = 0.f;  // sums of the lanes after and before this one
-            if (lane == 0) k_before = 0.f;
+        for (int d = 1; d < 32; d <<= 1) {
+            const float a = __shfl_down_sync(0xffffffffu, qs, d), e = __shfl_up_sync(0xffffffffu, ks, d);
+            if (lane + d < 32) qs += a;
+            if (lane >= d) ks += e;
+        }
+        float q_after = __shfl_down_sync(0xffffffffu, qs, 1), k_before = __shfl_up_sync(0xffffffffu, ks, 1);
+        if (lane == 31) q_after = 0.f;  // sums of the lanes after and before this one
+        if (lane == 0) k_before = 0.f;
+        float val[2] = {i0 + qs + k_before + outside, i1 + (q1 + q_after) + (k_before + k0) + outside};
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int t = t0 + e;
-                if (t >= p1) continue;
-                const float r = e ? q1 + q_after : qs, f = e ? k_before + k0 : k_before;
-                float val = (e ? ii.y : ii.x) + r + f + outside;
-                const size_t at = size_t(start + t) * hv + h;
-                if ((g_const ? g[h] : g[at]) < kGFloor) val = 0.f;
-                if (g_const) dg_tok[size_t(h) * tokens + start + t] = val;
-                else dg[at] = val;
-            }
-            across = outside + ksum;
+        for (int e = 0; e < 2; ++e) {
+            if (!(e ? v1 : v0)) continue;
+            const size_t to = (at + e) * hv + h;
+            if ((g_const ? g[h] : g[to]) < kGFloor) val[e] = 0.f;
+            if (g_const) dg_tok[of + e] = val[e];
+            else dg[to] = val[e];
         }
     }
 }
@@ -383,10 +350,7 @@ DecayLayout decay_layout(const gdn_shape_t &s, bool backward) {
     L.max_split = may_split(s) ? tokens / shortest + 1 : 0;
     L.max_segs = N + L.max_slots;
     L.max_chunks = (tokens + 63 * N) / kDecayChunk;
-    // checkpoints are `ick` apart, 1024 unless segments are shorter
-    const int64_t ick = balanced >= kDecayMaxIck || !may_split(s) ? kDecayMaxIck : plan.min_seg;
-    L.max_cks = tokens / ick + N;
-    L.max_ckpt = tokens / ick + 1;  // (a sequence's first needs no room: it is the initial state)
+    L.max_starts = tokens / kDecayChunk + 1;  // (a sequence's first needs no room: it is the initial state)
     size_t off = 256;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -397,14 +361,16 @@ DecayLayout decay_layout(const gdn_shape_t &s, bool backward) {
     L.split_off = take(size_t(L.max_split) * 4);
     L.order_off = take(size_t(N) * 4);
     L.cbase_off = take(size_t(N + 1) * 4);
-    L.ckbase_off = take(size_t(N + 1) * 4);
     L.segdec_off[0] = take(size_t(L.max_slots) * hv * 4);
     L.state_off[0] = take(size_t(L.max_slots) * hv * 65536);
     if (backward) {
         L.segdec_off[1] = take(size_t(L.max_slots) * hv * 4);
         L.state_off[1] = take(size_t(L.max_slots) * hv * 65536);
-        L.ckpt_off = take(size_t(L.max_ckpt) * hv * 65536);
-        L.zsum_off = take(size_t(L.max_cks) * hv * 32);
+        // (the tensor-core pass keeps 128 rows and 64 or 128 columns whatever the head sizes)
+        const size_t state = decay_tc_supported(s) ? (s.head_dim_v > 64 ? 16384 : 8192)
+                                                   : size_t(s.head_dim_k) * s.head_dim_v;
+        L.start_off = take(size_t(L.max_starts) * hv * state * 4);
+        L.span_off = take(size_t(L.max_chunks) * hv * 32);
         for (int i = 0; i < 2; ++i) L.dot_off[i] = take(size_t(tokens) * hv * 4);
         L.intra_off = take(size_t(tokens) * hv * 4);
         L.dgtok_off = take(size_t(tokens) * hv * 4);
@@ -421,7 +387,6 @@ DecaySched decay_sched(char *ws, const DecayLayout &L) {
     sc.segs = reinterpret_cast<DecaySeg *>(ws + L.segs_off);
     sc.split = reinterpret_cast<int32_t *>(ws + L.split_off);
     sc.chunk_base = reinterpret_cast<int32_t *>(ws + L.cbase_off);
-    sc.ck_base = reinterpret_cast<int32_t *>(ws + L.ckbase_off);
     return sc;
 }
 
@@ -447,13 +412,13 @@ cudaError_t launch_decay_combine(const gdn_shape_t &s, const DecayLayout &L, con
 }
 
 cudaError_t launch_decay_dg(const gdn_shape_t &s, const int32_t *cu, const DecayLayout &L, const DecaySched &sc,
-                            const float *dot_q, const float *dot_k, const float *intra, const float *zsum,
+                            const float *dot_q, const float *dot_k, const float *intra, const float *span,
                             const float *g, bool g_const, float *dg_tok, float *dg, cudaStream_t stream) {
-    const int64_t tokens = int64_t(s.batch) * s.seq_len, units = L.max_cks * s.num_v_heads;
+    const int64_t tokens = int64_t(s.batch) * s.seq_len, units = L.max_chunks * s.num_v_heads;
     const unsigned grid = unsigned(std::min<int64_t>((units + 3) / 4, 148 * 16));
     if (grid > 0) {
         decay_dg_kernel<<<grid, 128, 0, stream>>>(s.num_seqs, s.num_v_heads, int(tokens), cu, s.seq_len, sc, dot_q,
-                                                  dot_k, intra, zsum, g, g_const, dg_tok, dg);
+                                                  dot_k, intra, span, g, g_const, dg_tok, dg);
         count_launch();
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;

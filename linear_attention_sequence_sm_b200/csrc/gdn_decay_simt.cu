@@ -215,9 +215,33 @@ decay_pass_simt_kernel(const __grid_constant__ DecayPass a0, const __grid_consta
             load_gates(sm, g + size_t(t0) * gs, gs, L, a.reverse);
             __syncthreads();
             seg_sum += float(sm.G[C - 1]);
-            if (a.ckpt && !a.zsum && seg.pos + t0 > 0 && (seg.pos + t0) % hdr->ick == 0) {
-                float *dst = a.ckpt + (size_t((seg.start + t0) / hdr->ick) * hv + h) * 16384;
-                for (int q = tid; q < dz * dy; q += kThreads) dst[q] = tS[(q / dy) * ly + q % dy];
+            if (a.starts) {
+                const bool start = seg.pos + t0 == 0;
+                float *at = a.starts + (size_t((seg.start + t0) / C) * hv + h) * dz * dy;
+                if (!a.span) {
+                    if (!start)
+                        for (int q = tid; q < dz * dy; q += kThreads) at[q] = tS[(q / dy) * ly + q % dy];
+                } else {
+                    // <Sigma at the chunk's end, the state at its start>
+                    const float *cp = !start ? at : a.s_first ? a.s_first + (size_t(seg.seq) * hv + h) * dz * dy : nullptr;
+                    float s = 0.f;
+                    if (cp) {
+                        const bool tr = start && a.s_trans;
+                        for (int q0 = tid; q0 < dz * dy; q0 += 8 * kThreads) {
+                            float v[8];
+#pragma unroll
+                            for (int b = 0; b < 8; ++b) v[b] = q0 + b * kThreads < dz * dy ? cp[q0 + b * kThreads] : 0.f;
+#pragma unroll
+                            for (int b = 0; b < 8; ++b) {
+                                const int q = q0 + b * kThreads;
+                                if (q < dz * dy) s = fmaf(v[b], tS[(tr ? q % dz : q / dy) * ly + (tr ? q / dz : q % dy)], s);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+                    if ((tid & 31) == 0) sm.red[tid >> 5] = s;
+                }
             }
             if (!a.state_only) {
                 {
@@ -234,6 +258,8 @@ decay_pass_simt_kernel(const __grid_constant__ DecayPass a0, const __grid_consta
                         }
                 }
                 __syncthreads();
+                if (a.span && tid < 8)
+                    a.span[(size_t(seg.chunk + (seg.pos + t0) / C) * hv + h) * 8 + tid] = sm.gamma * sm.red[tid];
                 // out rows 4 rg .. 4 rg + 3, columns cg + 16 q (the rows of Sigma a quarter-warp reads are then
                 // next to one another and fall into different banks)
                 float in[4][8], ex[4][8];
@@ -337,25 +363,6 @@ decay_pass_simt_kernel(const __grid_constant__ DecayPass a0, const __grid_consta
                     for (int p = 0; p < 4; ++p)
                         *reinterpret_cast<ulonglong2 *>(tS + (zb + p) * ly + yb) = make_ulonglong2(acc[p][0], acc[p][1]);
                 }
-            if (a.zsum && (seg.pos + t0) % hdr->ick == 0) {
-                // <Sigma, checkpoint> at the chunk's start
-                const int slot = seg.ck + (seg.pos + t0) / hdr->ick;
-                const bool start = seg.pos + t0 == 0;
-                const float *cp = start ? (a.s_first ? a.s_first + (size_t(seg.seq) * hv + h) * dz * dy : nullptr)
-                                        : a.ckpt + (size_t((seg.start + t0) / hdr->ick) * hv + h) * 16384;
-                __syncthreads();
-                float s = 0.f;
-                if (cp)
-                    for (int q = tid; q < dz * dy; q += kThreads) {
-                        const bool tr = start && a.s_trans;
-                        s = fmaf(cp[q], tS[(tr ? q % dz : q / dy) * ly + (tr ? q / dz : q % dy)], s);
-                    }
-#pragma unroll
-                for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-                if ((tid & 31) == 0) sm.red[tid >> 5] = s;
-                __syncthreads();
-                if (tid < 8) a.zsum[(size_t(slot) * hv + h) * 8 + tid] = sm.red[tid];
-            }
         }
         __syncthreads();
         if (a.state_only) {

@@ -14,7 +14,11 @@
 // operands in tensor memory: operands read from shared memory are what the
 // products wait for (12 products of 128 x 128 x 16 take 1450 cycles with both
 // operands there, 1040 with one), and what shared memory holds goes to a
-// third tile of x, y and z, loaded two chunks ahead.
+// third tile of x, y and z, loaded two chunks ahead -- or, in the dot pass
+// backward in time, to the chunk's start state (64 KB), which its state warps
+// multiply with dS while X1 runs (read from global memory by these warps: 358
+// us; by the out warps, with Sigma from its copies: 500; from shared memory:
+// 276).
 //
 // Sigma itself lives in the state warps' registers, so that L's products need
 // nothing from the chunk before: the chain from chunk to chunk is one
@@ -46,8 +50,9 @@
 // copies of Sigma) two.
 //
 // Measured on a B200, 4 x 4096 tokens, 32 heads, d = 128 (128 units, 64 chunks
-// each): 136 us plain, 247 us with dots and fp32 out; 65,536 x 48 heads: 386
-// us for the states at the cuts and 701 us for the outputs.  A plain chunk
+// each): 130 us plain, 232 us with dots and fp32 out (dq) and 276 us backward
+// in time (dk); 65,536 x 48 heads: 386 us for the states at the cuts and 701 us
+// for the outputs.  A plain chunk
 // takes about 3900 cycles, its products 2060 of them (tensor pipe 33 % busy
 // over all SMs, 40 % where 148 are used); DRAM traffic is what the operands
 // are.  So the bound is latency: hand-overs between roles, and issue slots
@@ -88,10 +93,14 @@ constexpr int kVecG = 0, kVecIn = 64, kVecSt = 128, kVecGamma = 192, kVecFloats 
 
 // kKind: what a pass leaves out or adds
 enum { kPlain = 0, kDot = 1, kStateOnly = 2 };
-constexpr int kRing = 3;  // tiles of x, y and z
 constexpr uint32_t kStage = 2304;  // an out warp's staging: 32 rows of 64 bytes, or 16 rows of 36 floats
 
-template <int kKind> struct Cfg {
+template <int kKind, bool kRev> struct Cfg {
+    // Dot passes also keep the start state of every chunk (forward in time) or multiply with it (backward, from a
+    // buffer that takes a tile of each ring; a dot pass's chunks are long enough for two).
+    static constexpr bool kKeepStarts = kKind == kDot && !kRev, kSpans = kKind == kDot && kRev;
+    static constexpr uint32_t kRing = kSpans ? 2 : 3;            // tiles of x, y and z
+    static constexpr uint32_t kAuxRing = kSpans ? 1 : 2;         // of aux
     static constexpr int kCopies = kKind == kDot ? 3 : 1;        // bf16 terms of Sigma's copy
     static constexpr int kBufs = kKind == kDot ? 1 : 2;          // of X2 and QK
     static constexpr int kQuarters = kKind == kDot ? 2 : 4;      // of w z
@@ -99,13 +108,14 @@ template <int kKind> struct Cfg {
     static constexpr uint32_t kOffX = 0;
     static constexpr uint32_t kOffZ = kOffX + kRing * kTile;
     static constexpr uint32_t kOffY = kOffZ + kRing * kTile;
-    static constexpr uint32_t kOffAux = kOffY + kRing * kTile;                     // [2], kDot only
-    static constexpr uint32_t kOffP = kOffAux + (kKind == kDot ? 2 * kTile : 0);   // [2]
+    static constexpr uint32_t kOffAux = kOffY + kRing * kTile;                     // kDot only
+    static constexpr uint32_t kOffStart = kOffAux + (kKind == kDot ? kAuxRing * kTile : 0);  // kSpans only
+    static constexpr uint32_t kOffP = kOffStart + (kSpans ? 4 * kTile : 0);        // [2]
     static constexpr uint32_t kOffOut = kOffP + 2 * kPTile;                        // kStage bytes an out warp
     static constexpr uint32_t kOffVec = kOffOut + 8 * kStage;                           // [4]
     static constexpr uint32_t kOffRed = kOffVec + 4 * kVecFloats * 4;              // [4 warps][64]
     static constexpr uint32_t kOffBar = kOffRed + 1024;
-    static constexpr uint32_t kSmem = kOffBar + 448 + 1024;
+    static constexpr uint32_t kSmem = kOffBar + 464 + 1024;
     static_assert(kSmem <= 232448, "shared memory over the sm_100 per-block limit");
     // tensor memory columns
     // L (two for the state alone); quarters of w z (8 columns a term); the copies of Sigma (64 columns a term);
@@ -117,6 +127,8 @@ template <int kKind> struct Cfg {
     static __device__ __forceinline__ uint32_t buf(uint32_t m) { return kBufs == 2 ? (m & 1u) : 0u; }
     static __device__ __forceinline__ uint32_t phase(uint32_t m) { return (kBufs == 2 ? m >> 1 : m) & 1u; }
     static __device__ __forceinline__ uint32_t col_x2(uint32_t m) { return kColX2 + 64u * buf(m); }
+    static __device__ __forceinline__ uint32_t aux(uint32_t m) { return m % kAuxRing; }
+    static __device__ __forceinline__ uint32_t aux_turn(uint32_t m) { return m / kAuxRing; }
     // quarter q of chunk m: its buffer, and which use of it this is
     static __device__ __forceinline__ uint32_t qbuf(uint32_t q) { return kQuarters == 4 ? q : q & 1u; }
     static __device__ __forceinline__ uint32_t qturn(uint32_t m, uint32_t q) { return kQuarters == 4 ? m : 2 * m + (q >> 1); }
@@ -127,7 +139,7 @@ template <int kKind> struct Cfg {
 
 // mbarriers
 enum {
-    kBX = 0,        // [3] x landed
+    kBX = 0,        // [3] x landed (one barrier a tile of the ring)
     kBZ = 3,        // [3] z
     kBY = 6,        // [3] y
     kBA = 9,        // [2] aux
@@ -150,7 +162,9 @@ enum {
     kBVecFree = 48, // [4] token vectors read (8 state warps, 8 out warps)
     kBX2Free = 52,  // X2 read (8 out warps; where QK needs its columns)
     kBDrain = 53,
-    kNumBars = 54
+    kBStart = 54,     // the chunk's start state landed
+    kBStartFree = 55, // and multiplied (8 state warps)
+    kNumBars = 56
 };
 
 struct Maps {
@@ -182,6 +196,13 @@ template <bool kRev> struct UnitWalk {
     // first token of the n-th chunk in pass order, from the segment's start
     __device__ int chunk_at(int n) const { return kDecayChunk * (kRev ? nch - 1 - n : n); }
 };
+
+// The start state of the chunk that begins at token t, as the state warps hold
+// it: 64 columns a thread as 16 pieces of 16 bytes, the threads' first pieces
+// one after the other, then their second, and so on.
+__device__ __forceinline__ float *start_slot(const DecayPass &a, int t, int h, int ya) {
+    return a.starts + (size_t(t / kDecayChunk) * a.hv + h) * size_t(8192 * ya);
+}
 
 // A bounded wait that leaves the issue slots to the others: the thread is
 // suspended until the phase completes or kIdleNs pass.
@@ -278,8 +299,10 @@ __device__ __forceinline__ void stmatrix_t(uint32_t addr, uint32_t a, uint32_t b
 template <int kKind, bool kRev, bool kF32>
 __global__ void __launch_bounds__(kThreads, 1)
 decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
-    using K = Cfg<kKind>;
+    using K = Cfg<kKind, kRev>;
+    constexpr uint32_t kRing = K::kRing;
     constexpr bool kDots = kKind == kDot, kSt = kKind == kStateOnly;
+    constexpr bool kKeepStarts = K::kKeepStarts, kSpans = K::kSpans;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sb = smem_u32(smem);
@@ -293,11 +316,11 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
             int n = 1;
             if ((i >= kBW && i < kBW + 4) || i == kBP || i == kBP + 1) n = 4;
             if (i == kBSt || i == kBLFree || i == kBLFree + 1 || i == kBOutFree || i == kBX2Free || i == kBAFree ||
-                i == kBAFree + 1)
+                i == kBAFree + 1 || i == kBStartFree)
                 n = 8;
             if (i == kBOut || i == kBKV || i == kBKV + 1) n = 2;
-            if (i >= kBZFree && i < kBZFree + kRing) n = kSt ? 16 : 9;  // (each split warp once a chunk)
-            if (i >= kBYFree && i < kBYFree + kRing) n = kSt ? 1 : 2;
+            if (i >= kBZFree && i < kBZFree + int(kRing)) n = kSt ? 16 : 9;  // (each split warp once a chunk)
+            if (i >= kBYFree && i < kBYFree + int(kRing)) n = kSt ? 1 : 2;
             if (i == kBDrain) n = 2;
             if (i >= kBVecFree && i < kBVecFree + 4) n = kSt ? 8 : 16;
             mbar_init(bar(i), uint32_t(n));
@@ -359,12 +382,6 @@ decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
             float dec = 1.f;
             for (int n = 0; n < w.nch; ++n) {
                 const uint32_t mm = m + uint32_t(n);
-                const int p = w.seg.pos + w.chunk_at(n);  // the chunk's start in the sequence
-                if (kDots && a.ckpt && !a.zsum && mine && p > 0 && p % a.sched.hdr->ick == 0) {
-                    float *ck = a.ckpt + (size_t((w.seg.start + w.chunk_at(n)) / a.sched.hdr->ick) * hv + w.h) * 16384;
-#pragma unroll
-                    for (int j = 0; j < 64; ++j) ck[(c0 + j) * 128 + row] = S[j];
-                }
                 if constexpr (!kSt) {
                     // the copies of Sigma, once the previous X1 has read its own
                     if (mm > 0) ok = warp_wait(bar(kBX1), (mm - 1) & 1u);
@@ -399,6 +416,31 @@ constexpr int kW = K::kCopies == 1 ? 8 : 4;  // words of a slice (fewer where it
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(kBSt));
                 }
+                if (kKeepStarts && mine && w.seg.pos + w.chunk_at(n) > 0) {
+                    float4 *st = reinterpret_cast<float4 *>(start_slot(a, w.seg.start + w.chunk_at(n), w.h, ya)) + tid;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        st[j * 128 * ya] = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
+                }
+                float span = 0.f;  // <Sigma at the chunk's end, the state at its start>, while X1 runs
+                if constexpr (kSpans) {
+                    ok = warp_wait(bar(kBStart), mm & 1u);
+                    if (!ok) break;
+                    if (mine && w.seg.pos + w.chunk_at(n) > 0) {
+                        const float4 *st = reinterpret_cast<const float4 *>(smem + K::kOffStart) + tid;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float4 x = st[j * 128 * ya];
+                            span = fmaf(x.x, S[4 * j], fmaf(x.y, S[4 * j + 1], fmaf(x.z, S[4 * j + 2], fmaf(x.w, S[4 * j + 3], span))));
+                        }
+                    } else if (mine && a.s_first && zin) {  // the initial state, stored [y][z] (s_trans)
+#pragma unroll
+                        for (int j = 0; j < 64; ++j)
+                            if (c0 + j < dy) span = fmaf(a.s_first[sbase + size_t(c0 + j) * dz + row], S[j], span);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kBStartFree));
+                }
                 ok = warp_wait(bar(kBKV + int(K::lbuf(mm))), K::lphase(mm));
                 if (!ok) break;
                 tc_fence_after();
@@ -424,26 +466,11 @@ constexpr int kW = K::kCopies == 1 ? 8 : 4;  // words of a slice (fewer where it
                     mbar_arrive(bar(kBLFree + int(K::lbuf(mm))));
                     mbar_arrive(bar(kBVecFree + int(mm & 3u)));
                 }
-                if (kDots && a.zsum && p % a.sched.hdr->ick == 0) {
-                    // <Sigma, checkpoint> at the chunk's start
-                    const size_t slot = size_t(w.seg.ck + p / a.sched.hdr->ick) * hv + w.h;
-                    float dot = 0.f;
-                    if (mine && zin) {
-                        if (p == 0) {  // stored [y][z] (s_trans)
-                            if (a.s_first) {
+                if (kSpans) {
 #pragma unroll
-                                for (int j = 0; j < 64; ++j)
-                                    if (c0 + j < dy) dot = fmaf(a.s_first[sbase + size_t(c0 + j) * dz + row], S[j], dot);
-                            }
-                        } else {
-                            const float *cp = a.ckpt + (size_t((w.seg.start + w.chunk_at(n)) / a.sched.hdr->ick) * hv + w.h) * 16384;
-#pragma unroll
-                            for (int j = 0; j < 64; ++j) dot = fmaf(cp[(c0 + j) * 128 + row], S[j], dot);
-                        }
-                    }
-#pragma unroll
-                    for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
-                    if (lane == 0) a.zsum[slot * 8 + warp] = dot;
+                    for (int s = 16; s > 0; s >>= 1) span += __shfl_xor_sync(0xffffffffu, span, s);
+                    if (lane == 0)
+                        a.span[(size_t(w.seg.chunk + (w.seg.pos + w.chunk_at(n)) / kDecayChunk) * hv + w.h) * 8 + warp] = gamma * span;
                 }
             }
             if (!ok) break;
@@ -491,7 +518,7 @@ constexpr int kW = K::kCopies == 1 ? 8 : 4;  // words of a slice (fewer where it
                     const int t0 = w.chunk_at(n), L = min(kDecayChunk, w.seg.len - t0);
                     ok = warp_wait(bar(kBOut), mm & 1u);
                     if (kDots && a.aux) {
-                        if (ok) ok = warp_wait(bar(kBA + int(mm & 1u)), (mm >> 1) & 1u);
+                        if (ok) ok = warp_wait(bar(kBA + int(K::aux(mm))), K::aux_turn(mm) & 1u);
                         ok = !named_sync_or(kBarOut + part, 128, !ok);  // the four warps stay together (and `red` was read)
                     }
                     if (!ok) break;
@@ -558,7 +585,7 @@ constexpr int kW = K::kCopies == 1 ? 8 : 4;  // words of a slice (fewer where it
                         if constexpr (kDots) {
                             if (a.aux) {
                                 float d[4];  // dots of this thread's 4 tokens over its 4 rows
-                                const uint32_t aux = sb + K::kOffAux + (mm & 1u) * kTile + uint32_t(quarter >> 1) * kAtom;
+                                const uint32_t aux = sb + K::kOffAux + K::aux(mm) * kTile + uint32_t(quarter >> 1) * kAtom;
 #pragma unroll
                                 for (int j = 0; j < 2; ++j) {
                                     // tiles: tokens 8 j .. 8 j + 7, z 8 i .. 8 i + 7 of this quarter, i = lane / 8
@@ -641,7 +668,7 @@ constexpr int kW = K::kCopies == 1 ? 8 : 4;  // words of a slice (fewer where it
                     }
                     if (kDots && a.aux) {
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(kBAFree + int(mm & 1u)));
+                        if (lane == 0) mbar_arrive(bar(kBAFree + int(K::aux(mm))));
                         named_sync(kBarOut + part, 128);
                         const int tk = 32 * part + ot;
                         if (ot < 32 && tk < L)
@@ -848,7 +875,7 @@ constexpr int kW = K::kCopies == 1 ? 8 : 4;  // words of a slice (fewer where it
                     const uint32_t mm = m + uint32_t(n);
                     const int tok = w.seg.start + w.chunk_at(n);
                     const uint32_t s = mm % kRing, freed = (mm / kRing - 1) & 1u;
-                    const bool wait = mm >= uint32_t(kRing);
+                    const bool wait = mm >= kRing;
                     {
                         const uint32_t dst = sb + K::kOffY + s * kTile, b = bar(kBY + int(s));
                         if (wait) ok = mbar_wait(bar(kBYFree + int(s)), freed);
@@ -873,9 +900,19 @@ constexpr int kW = K::kCopies == 1 ? 8 : 4;  // words of a slice (fewer where it
                         tma_load_3d(dst, &tm.z, 0, hz, tok, b);
                         tma_load_3d(dst + kAtom, &tm.z, 64, hz, tok, b);
                     }
+                    if constexpr (kSpans) {
+                        if (mm > 0) ok = mbar_wait(bar(kBStartFree), (mm - 1) & 1u);
+                        if (!ok) break;
+                        if (w.seg.pos + w.chunk_at(n) > 0) {
+                            mbar_arrive_expect_tx(bar(kBStart), 32768u * uint32_t(ya));
+                            bulk_load(sb + K::kOffStart, start_slot(a, tok, w.h, ya), 32768u * uint32_t(ya), bar(kBStart));
+                        } else {
+                            mbar_arrive(bar(kBStart));  // (the initial state is read where it is)
+                        }
+                    }
                     if (kDots && a.aux) {
-                        const uint32_t i = mm & 1u, dst = sb + K::kOffAux + i * kTile, b = bar(kBA + int(i));
-                        if (mm >= 2) ok = mbar_wait(bar(kBAFree + int(i)), ((mm >> 1) - 1) & 1u);
+                        const uint32_t i = K::aux(mm), dst = sb + K::kOffAux + i * kTile, b = bar(kBA + int(i));
+                        if (mm >= K::kAuxRing) ok = mbar_wait(bar(kBAFree + int(i)), (K::aux_turn(mm) - 1) & 1u);
                         if (!ok) break;
                         mbar_arrive_expect_tx(b, kTile);
                         tma_load_3d(dst, &tm.aux, 0, ha, tok, b);
@@ -994,7 +1031,7 @@ constexpr int kW = K::kCopies == 1 ? 8 : 4;  // words of a slice (fewer where it
 template <int kKind, bool kRev, bool kF32>
 cudaError_t launch_as(const Maps &tm, const DecayPass &p, int64_t max_units, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(decay_pass_tc_kernel<kKind, kRev, kF32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         int(Cfg<kKind>::kSmem));
+                                         int(Cfg<kKind, kRev>::kSmem));
     if (e != cudaSuccess) return e;
     static const int regs = [] {
         cudaFuncAttributes fa;
@@ -1006,7 +1043,7 @@ cudaError_t launch_as(const Maps &tm, const DecayPass &p, int64_t max_units, cud
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(std::min<int64_t>(max_units, sms)));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Cfg<kKind>::kSmem;
+    cfg.dynamicSmemBytes = Cfg<kKind, kRev>::kSmem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

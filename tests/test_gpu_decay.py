@@ -455,3 +455,43 @@ def test_outputs_belong_to_the_calls_stream():
                    if t is not None],
     ]
     streams.check_outputs_belong_to_the_calls_stream(calls)
+
+
+def dg_sizes(d):
+    """a_t |dS_t| |S_(t-1)| (2-norms) per token and head, in 64 bits: what dg_t = a_t <dS_t, S_(t-1)> is a product of."""
+    lens = R.lens_of(d["q"], d["cu"])
+    q, k, v, do = (d[n].reshape(-1, *d[n].shape[-2:]).double() for n in ("q", "k", "v", "do"))
+    hv = v.shape[1]
+    head = torch.arange(hv) // (hv // q.shape[1])
+    a = d["g"].double().reshape(-1, hv).clamp(min=R.FLOOR).exp()
+    left, right, start = torch.zeros_like(a), torch.zeros_like(a), 0
+    for n, ln in enumerate(lens):
+        S, D = d["s0"][n].double(), d["dsf"][n].double()
+        for t in range(start, start + ln):
+            left[t] = S.flatten(1).norm(dim=-1)
+            S = a[t][:, None, None] * S + v[t][:, :, None] * k[t, head][:, None, :]
+        for t in reversed(range(start, start + ln)):
+            D = D + do[t][:, :, None] * q[t, head][:, None, :]
+            right[t] = D.flatten(1).norm(dim=-1)
+            D = a[t][:, None, None] * D
+        start += ln
+    return a * left * right
+
+
+@dtypes
+@pytest.mark.parametrize("simt", [False, True])
+def test_backward_lone_strong_decays_among_slow_ones(simt, dtype):
+    """A token whose decay nearly ends what came before it: its dg is tiny beside its neighbours' and still right.
+    dg_t is a product of the two states, put together from four parts (pairs inside the chunk, pairs with one end in
+    it on either side, pairs across it), each within 256 u of the product of the norms it is made of; the parts of
+    tokens drawn independently have norms of at most about the whole's, twice that for the bar."""
+    d = R.make(49, 2, 4, 64, 64, dtype, lens=[1100, 130])
+    d["g"].fill_(-0.01)
+    for h, x in enumerate((-8.0, -12.0, -15.0, -19.0)):
+        for t in (0, 1, 640, 700, 767, 1090, 1150):
+            d["g"][t, h] = x
+    got = grads(d, force_simt=simt)
+    ref = R.backward(d["q"], d["k"], d["v"], d["g"], d["do"], d["dsf"], d["s0"], d["cu"])
+    err = (got["dg"].double().cpu() - ref["dg"]).abs()
+    assert float((err / dg_sizes(d)).max()) <= 8 * 256 * R.U32
+    check_backward(d, got)
