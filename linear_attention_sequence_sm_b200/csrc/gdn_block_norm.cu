@@ -12,11 +12,12 @@
 //     dn1 = du w1,     dx = (dn1 - n1 mean(dn1 . n1)) / rms(x),
 //     dw2 = sum dy n2, ds = sum c e b, dw1 = sum du n1      (sums over rows)
 //
-// Both are bound by memory: each input row is read once, h and the norms are
-// recomputed in the backward instead of kept.  16,384 x 4096 rows in bf16 with
-// a gate and a residual: forward 114 us, 0.90 of the copy bandwidth; gradients
-// 246 us, 0.67.  (Compiling the forward for the parts a call has, as the
-// gradients are, gave nothing: 127 us against 124.)
+// Each input row is read once; h and the norms are recomputed in the backward
+// instead of kept.  The forward is bound by memory: 16,384 x 4096 rows in bf16
+// with a gate and a residual take 116 us, 0.88 of the copy bandwidth.  The
+// gradients of the same take 246 us, 0.67: a row is a chain of sums over the
+// block and of what follows from them, and one block of 16 warps an SM leaves
+// about half of the issue slots empty while it waits for them.
 #include <algorithm>
 
 #include "gdn_block_norm.cuh"
@@ -112,53 +113,72 @@ template <typename T> __device__ __forceinline__ void store_pairs(T *p, const f3
     }
 }
 
-// The staged rows: a block takes blockDim.y consecutive rows at a time, which
-// are one run of bytes of each tensor; kStages groups are in flight as bulk
-// copies counted on an mbarrier each.
-constexpr int kMaxTensors = 5;
+// The staged rows: a block takes the same number of consecutive rows at a time,
+// and kStages groups of them are in flight.  A thread copies the bytes that it
+// will read itself (a warp, where 32 bytes a thread are copied as two runs of
+// 16 bytes a lane), so it waits for its own copies only: no barrier of the block
+// stands between a copy, its readers and the next copy, and there is no wait
+// that could run out.  (Bulk copies by one thread, counted on mbarriers, were 2
+// to 10 % slower forward, 2 % faster for the gradients of 4096 bf16 columns and
+// 3 to 9 % for fp32 ones up to 2048, and a copy that did not arrive in time
+// left its rows out without a word.)
+constexpr int kMaxTensors = 5;  // x, gate, residual, d_y, d_h
 struct Stages {
     const unsigned char *src[kMaxTensors];  // NULL: not wanted
     uint32_t row_bytes[kMaxTensors], off[kMaxTensors];  // a row's bytes; where its group starts in a stage
     uint32_t stage_bytes;
 };
-template <int kStages> struct Pipe {
-    uint32_t bars, buf, stage, phase;  // the stage being read and its barrier's phase
-    int rows, per, next;               // the first row of the next group to fetch
-    __device__ void init(unsigned char *smem, int rows_, int per_) {
-        bars = smem_u32(smem);
-        buf = bars + 64;
-        rows = rows_;
-        per = per_;
-        stage = phase = 0;
-        next = int(blockIdx.x) * per;
-        if (threadIdx.x == 0 && threadIdx.y == 0) {
-            for (int i = 0; i < kStages; ++i) mbar_init(bars + 8 * i, 1);
-            fence_mbarrier_init();
-        }
-        __syncthreads();
-    }
-    // one thread: the copies of this block's next group, into stage `st`
-    __device__ void fetch(const Stages &s, uint32_t st) {
-        if (next >= rows) return;
-        const uint32_t live = uint32_t(min(rows - next, per)), bar = bars + 8 * st, dst = buf + st * s.stage_bytes;
-        uint32_t bytes = 0;
+__device__ __forceinline__ void copy16(uint32_t dst, const unsigned char *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// kRows consecutive rows a thread.
+template <typename T, typename R, int kStages, int kGroups, int kRows> struct Pipe {
+    static constexpr bool kShared = sizeof(T) == 4 || sizeof(R) == 4;  // lanes copy for one another
+    uint32_t buf, stage;
+    int rows, stride, next;  // this thread's first row of the next group to fetch
+    __device__ Pipe(const unsigned char *smem, int rows_)
+        : buf(smem_u32(smem)), stage(0), rows(rows_), stride(int(gridDim.x * blockDim.y) * kRows),
+          next((int(blockIdx.x * blockDim.y) + int(threadIdx.y)) * kRows) {}
+    // the copies of this thread's next rows, into stage `st` (a group of copies, possibly of none)
+    __device__ __forceinline__ void fetch(const Stages &s, uint32_t st, int width) {
+        const uint32_t dst = buf + st * s.stage_bytes;
+        if constexpr (kShared) __syncwarp();
 #pragma unroll
-        for (int i = 0; i < kMaxTensors; ++i)
-            if (s.src[i]) bytes += live * s.row_bytes[i];
-        mbar_arrive_expect_tx(bar, bytes);
+        for (int i = 0; i < kMaxTensors; ++i) {
+            if (!s.src[i]) continue;
+            constexpr int kT = sizeof(T), kR = sizeof(R);
+            const int size = i == 2 || i == 4 ? kR : kT;
 #pragma unroll
-        for (int i = 0; i < kMaxTensors; ++i)
-            if (s.src[i]) bulk_load(dst + s.off[i], s.src[i] + int64_t(next) * s.row_bytes[i], live * s.row_bytes[i], bar);
-        next = next > rows - int(gridDim.x) * per ? rows : next + int(gridDim.x) * per;
-    }
-    // every thread; false: the copy did not arrive in time
-    __device__ bool wait() const { return mbar_wait(bars + 8 * stage, phase); }
-    __device__ void advance() {
-        if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
+            for (int k = 0; k < kRows; ++k) {
+                if (next + k >= rows) continue;
+                const unsigned char *row = s.src[i] + int64_t(next + k) * s.row_bytes[i];
+                const uint32_t to = dst + s.off[i] + (threadIdx.y * kRows + k) * s.row_bytes[i];
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    const int mine = 8 * (g * int(blockDim.x) + int(threadIdx.x));
+                    if (size == 2) {
+                        if (mine < width) copy16(to + 2 * mine, row + 2 * mine);
+                    } else {
+                        const int c = mine - 4 * int(threadIdx.x & 31);
+                        if (c < width) copy16(to + 4 * c, row + 4 * c);
+                        if (c + 128 < width) copy16(to + 4 * c + 512, row + 4 * c + 512);
+                    }
+                }
+            }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        next = next > rows - stride ? rows : next + stride;
     }
+    __device__ __forceinline__ void start(const Stages &s, int width) {
+#pragma unroll
+        for (uint32_t i = 0; i < kStages; ++i) fetch(s, i, width);
+    }
+    // all copies are here but those of the last kLeft fetches
+    template <int kLeft> __device__ __forceinline__ void wait() const {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+        if constexpr (kShared) __syncwarp();
+    }
+    __device__ __forceinline__ void advance() { stage = stage + 1 == kStages ? 0 : stage + 1; }
 };
 
 // Sums of kN values over the n threads of a row (n a multiple of 32, at most
@@ -284,16 +304,13 @@ block_norm_forward_kernel(const BlockNormArgs a, const Stages sg) {
     clear_red(red_all);
     constexpr bool kKeep = kGroups <= 2;
     const int n = blockDim.x, t = threadIdx.x, width = a.width;
-    const bool leader = threadIdx.x == 0 && threadIdx.y == 0;
     float *red = red_all + kWarps * threadIdx.y;
-    Pipe<kFwdStages> pipe;
-    pipe.init(smem, int(a.rows), blockDim.y);
+    Pipe<T, R, kFwdStages, kGroups, 1> pipe(smem, int(a.rows));
     const bool post = a.flags & GDN_BLOCK_POST_NORM, pre = a.flags & GDN_BLOCK_PRE_NORM;
     const bool silu = a.flags & GDN_BLOCK_GATE_SILU, gated = sg.src[1] != nullptr, res = sg.src[2] != nullptr;
     const float inv_width = 1.f / float(width);
     const int rows = int(a.rows), stride = int(gridDim.x * blockDim.y);
-    if (leader)
-        for (uint32_t i = 0; i < kFwdStages; ++i) pipe.fetch(sg, i);
+    pipe.start(sg, width);
     f32x2 w1s[kKeep ? kGroups : 1][4], w2[kKeep ? kGroups : 1][4];  // w1 branch_scale s, w2
     auto weights = [&](int i, f32x2 (&u)[4], f32x2 (&v)[4]) {
         Weights w;
@@ -310,8 +327,9 @@ block_norm_forward_kernel(const BlockNormArgs a, const Stages sg) {
     for (int first = int(blockIdx.x * blockDim.y), left = 1; left > 0; first += stride) {
         left = rows - first - stride;  // (rows < 2^31, and so is first: `left` > 0 while another group follows)
         const int row = first + int(threadIdx.y);
-        const bool live = row < rows && pipe.wait();
-        const unsigned char *st = smem + 64 + pipe.stage * sg.stage_bytes;
+        const bool live = row < rows;
+        pipe.template wait<kFwdStages - 1>();
+        const unsigned char *st = smem + pipe.stage * sg.stage_bytes;
         auto at = [&](int i) { return st + sg.off[i] + threadIdx.y * sg.row_bytes[i]; };
         const int64_t base = int64_t(row) * width + 8 * t;
         const int lw = live ? width : 0;
@@ -352,8 +370,7 @@ block_norm_forward_kernel(const BlockNormArgs a, const Stages sg) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) ss = fma2(xv[i][e], xv[i][e], ss);  // h
         }
-        __syncthreads();  // the stage has been read
-        if (leader) pipe.fetch(sg, pipe.stage);
+        pipe.fetch(sg, pipe.stage, width);  // (the stage has been read)
         pipe.advance();
         if (live && a.h)
 #pragma unroll
@@ -454,17 +471,14 @@ block_norm_backward_kernel(const BlockNormArgs a, const Stages sg) {
     clear_red(red_all);
     constexpr bool kKeep = kGroups == 1;
     const int n = blockDim.x, t = threadIdx.x, width = a.width;
-    const bool leader = threadIdx.x == 0 && threadIdx.y == 0;
     float *red = red_all + 32 * threadIdx.y;
-    Pipe<kBwdStages> pipe;
-    pipe.init(smem, int(a.rows), blockDim.y);
+    Pipe<T, R, kBwdStages, kGroups, 1> pipe(smem, int(a.rows));
     const bool post = a.flags & GDN_BLOCK_POST_NORM, pre = sg.src[3] != nullptr;
     const bool silu = a.flags & GDN_BLOCK_GATE_SILU, gated = sg.src[1] != nullptr, res = sg.src[2] != nullptr;
     const bool has_dh = sg.src[4] != nullptr;
     const float inv_width = 1.f / float(width);
     const int rows = int(a.rows), stride = int(gridDim.x * blockDim.y);
-    if (leader)
-        for (uint32_t i = 0; i < kBwdStages; ++i) pipe.fetch(sg, i);
+    pipe.start(sg, width);
     Weights w;
     if constexpr (kKeep) w.load(a, 0, t, n, width);
     f32x2 sw1[kGroups][4], sw2[kGroups][4], ssc[kGroups][4];
@@ -475,8 +489,9 @@ block_norm_backward_kernel(const BlockNormArgs a, const Stages sg) {
     for (int first = int(blockIdx.x * blockDim.y), left = 1; left > 0; first += stride) {
         left = rows - first - stride;  // (rows < 2^31, and so is first: `left` > 0 while another group follows)
         const int row = first + int(threadIdx.y);
-        const bool live = row < rows && pipe.wait();
-        const unsigned char *st = smem + 64 + pipe.stage * sg.stage_bytes;
+        const bool live = row < rows;
+        pipe.template wait<kBwdStages - 1>();
+        const unsigned char *st = smem + pipe.stage * sg.stage_bytes;
         auto at = [&](int i) { return st + sg.off[i] + threadIdx.y * sg.row_bytes[i]; };
         const int64_t base = int64_t(row) * width + 8 * t;
         const int lw = live ? width : 0;  // rows past the end read as zeros and add zeros
@@ -580,9 +595,6 @@ block_norm_backward_kernel(const BlockNormArgs a, const Stages sg) {
             }
             if (in && a.d_gate) store_pairs(static_cast<T *>(a.d_gate) + base + 8 * i * n, dv[i]);
         }
-        __syncthreads();  // the stage has been read
-        if (leader) pipe.fetch(sg, pipe.stage);
-        pipe.advance();
         if (post) {
             float s3[1] = {lo_of(sd) + hi_of(sd)};
             row_sum<1, 16>(s3, red, t, n);
@@ -597,6 +609,8 @@ block_norm_backward_kernel(const BlockNormArgs a, const Stages sg) {
 #pragma unroll
             for (int i = 0; i < kGroups; ++i)
                 if (8 * (i * n + t) < width) store_pairs(static_cast<T *>(a.dx) + base + 8 * i * n, hv[i]);
+        pipe.fetch(sg, pipe.stage, width);  // (the stage has been read; here fewer values are held than where it was)
+        pipe.advance();
     }
     float *out = a.partial + (int64_t(blockIdx.x) * blockDim.y + threadIdx.y) * 3 * width + 8 * t;
 #pragma unroll
@@ -615,11 +629,11 @@ block_norm_backward_kernel(const BlockNormArgs a, const Stages sg) {
 // a sum carries both rows' terms, and x^2 of the next two rows is summed with
 // dn1 . n1 of these (two sums for two rows, not six).  A row keeps its h and
 // the gate's sigmoid in registers; x, z and dy are read again from the stage.
-// What is left is instructions, so kParts says at compile time which parts
-// there are (with a residual and both upstream gradients; kAnyParts: looked
-// up).  16,384 x 4096 in bf16: 318 us in the form above, 345 us with two rows
-// and parts looked up at every use, 297 us with one row and parts known, 242
-// us with both (0.67 of the copy bandwidth).
+// kParts says at compile time which parts there are (with a residual and both
+// upstream gradients; kAnyParts: looked up), which takes instructions off the
+// chain.  16,384 x 4096 in bf16, each with bulk copies: 318 us in the form
+// above, 345 us with two rows and parts looked up at every use, 297 us with
+// one row and parts known, 242 us with both.
 enum { kPartPost = 1, kPartGate = 2, kPartSilu = 4, kAnyParts = 8 };
 template <typename T, typename R, int kParts>
 __global__ void __launch_bounds__(512, 1)
@@ -629,11 +643,9 @@ block_norm_backward_pair_kernel(const BlockNormArgs a, const Stages sg) {
     if (threadIdx.y == 0 && threadIdx.x < 8) zeros[threadIdx.x] = 0.f;
     clear_red(red_all);
     const int n = blockDim.x, t = threadIdx.x, width = a.width, c = 8 * t;
-    const bool leader = threadIdx.x == 0 && threadIdx.y == 0;
     float *red = red_all + 64 * threadIdx.y;
-    Pipe<kBwdStages> pipe;
+    Pipe<T, R, kBwdStages, 1, 2> pipe(smem, int(a.rows));
     const int per = 2 * blockDim.y;
-    pipe.init(smem, int(a.rows), per);
     constexpr bool kAny = kParts == kAnyParts;
     const bool post = kAny ? bool(a.flags & GDN_BLOCK_POST_NORM) : bool(kParts & kPartPost);
     const bool gated = kAny ? sg.src[1] != nullptr : bool(kParts & kPartGate);
@@ -641,8 +653,7 @@ block_norm_backward_pair_kernel(const BlockNormArgs a, const Stages sg) {
     const bool pre = !kAny || sg.src[3] != nullptr, res = !kAny || sg.src[2] != nullptr, has_dh = !kAny || sg.src[4] != nullptr;
     const float inv_width = 1.f / float(width);
     const int rows = int(a.rows), stride = int(gridDim.x) * per;
-    if (leader)
-        for (uint32_t i = 0; i < kBwdStages; ++i) pipe.fetch(sg, i);
+    pipe.start(sg, width);
     Weights w;
     w.load(a, 0, t, n, width);
     f32x2 sw1[4], sw2[4], ssc[4];
@@ -652,7 +663,7 @@ block_norm_backward_pair_kernel(const BlockNormArgs a, const Stages sg) {
     const int mine = 2 * int(threadIdx.y);
     // this thread's values of a row in a stage (of zeros, where it has none)
     auto at = [&](int i, int k, uint32_t stage, bool in) -> const unsigned char * {
-        return in ? smem + 64 + stage * sg.stage_bytes + sg.off[i] + (mine + k) * sg.row_bytes[i] +
+        return in ? smem + stage * sg.stage_bytes + sg.off[i] + (mine + k) * sg.row_bytes[i] +
                         t * 8 * (i == 2 || i == 4 ? int(sizeof(R)) : int(sizeof(T)))
                   : reinterpret_cast<const unsigned char *>(zeros);
     };
@@ -666,10 +677,10 @@ block_norm_backward_pair_kernel(const BlockNormArgs a, const Stages sg) {
     int first = int(blockIdx.x) * per;
     bool live[2];
     auto arrive = [&](bool more) {  // the group at `first`, if there is one
-        const bool here = more && first + mine < rows && pipe.wait();
-        live[0] = here && c < width;
+        live[0] = more && first + mine < rows && c < width;
         live[1] = live[0] && first + mine + 1 < rows;
     };
+    pipe.template wait<kBwdStages - 1>();
     arrive(first < rows);
     float s3[4] = {0.f, 0.f, 0.f, 0.f};  // dn1 . n1 of two rows, x^2 of the next two
     if (post) {
@@ -774,6 +785,7 @@ block_norm_backward_pair_kernel(const BlockNormArgs a, const Stages sg) {
         more = first < rows - stride;
         if (more) first += stride;
         pipe.advance();
+        pipe.template wait<kBwdStages - 2>();  // (this stage's next copies are not on their way yet)
         arrive(more);
         if (post) {
             s3[2] = squares(0, live[0]);
@@ -793,8 +805,7 @@ block_norm_backward_pair_kernel(const BlockNormArgs a, const Stages sg) {
             }
             if (in && a.dx) store_pairs(static_cast<T *>(a.dx) + base + int64_t(k) * width, hv[k]);
         }
-        __syncthreads();  // the stage has been read
-        if (leader) pipe.fetch(sg, stage);
+        pipe.fetch(sg, stage, width);  // (the stage has been read)
     }
     float *out = a.partial + (int64_t(blockIdx.x) * blockDim.y + threadIdx.y) * 3 * width + c;
     if (c >= width) return;
@@ -1011,11 +1022,11 @@ constexpr size_t kStageRoom = 220 * 1024;
 template <typename K>
 cudaError_t staged_launch(K kern, int stages, const BlockNormArgs &a, const Stages &sg, int grid, dim3 block,
                           cudaStream_t stream) {
-    const size_t bytes = 64 + size_t(stages) * sg.stage_bytes;
+    const size_t bytes = size_t(stages) * sg.stage_bytes;
     if (bytes > 40 * 1024) {  // (a kernel may have 48 KB in all without asking)
         // The limit is one value for all host threads: the most that any call asks for, never this call's own size,
         // which another thread could lower before the launch.
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(64 + kStageRoom));
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kStageRoom));
         if (e != cudaSuccess) return e;
     }
     kern<<<unsigned(grid), block, bytes, stream>>>(a, sg);

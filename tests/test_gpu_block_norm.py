@@ -214,3 +214,35 @@ def test_many_rows(size, types):
             # chain of at most rows / 148 + 16 additions, (that + 296) u of terms that do not cancel in the norm
             bars = 2 * bar(got[name]) + (size[0] / 148 + 312) * R.U32
             assert rel(got[name], ref[k]) <= bars, (name, gate, kw)
+
+
+@pytest.mark.parametrize("types", TYPES, ids=["bf16", "bf16_wide", "f32"])
+@pytest.mark.parametrize("size", [(14_001, 264), (3_553, 1032), (1_801, 2048), (1_801, 4096), (601, 5128), (601, 8192),
+                                  (453, 12_288)], ids=str)
+@pytest.mark.parametrize("gate", [True, False])
+def test_rows_enough_to_use_every_stage_again(gate, size, types):
+    """A block's stages of rows are filled, read and filled again several times over, the last groups short; the
+    forward and the gradients against their definition."""
+    from linear_attention_sequence_sm_b200 import gdn
+    kw = dict(rho=0.75, branch=0.5)
+    d = make(58, *size, *types, gate=gate)
+    c = R.cuda(d)
+    n = norm_of(c, **kw)
+    h, y = gdn.block_norm_forward(c["x"], c["residual"], n, gate=c["gate"])
+    got = gdn.block_norm_backward(c["x"], c["residual"], n, gate=c["gate"], d_h=c["d_h"], d_y=c["d_y"])
+    torch.cuda.synchronize()
+    rh, ry = reference(d, False, **kw)
+    ref = reference(d, True, **kw)
+    worst = lambda a, b: float(((a.double().cpu() - b).norm(dim=-1) / b.norm(dim=-1)).max())  # noqa: E731
+    # row by row, so that one row left out or taken twice shows
+    assert worst(h, rh.detach()) <= bar(h) and worst(y, ry.detach()) <= bar(y)
+    names = dict(x="dx", residual="d_residual", gate="d_gate", w1="d_post_weight", scale="d_scale", w2="d_pre_weight")
+    for k, name in names.items():
+        if k not in ref:
+            continue
+        # as in test_many_rows
+        bars = 2 * bar(got[name]) + (size[0] / 148 + 312) * R.U32
+        assert rel(got[name], ref[k]) <= bars, name
+        if k in ("x", "residual", "gate"):
+            # a row's gradients: three sums more than its values
+            assert worst(got[name], ref[k].detach()) <= 4 * bar(got[name]), name
