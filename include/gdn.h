@@ -476,7 +476,11 @@ GDN_API gdn_status_t gdn_short_conv(int32_t num_seqs, int32_t seq_len, const int
  * and the decay-masked chunk output).  Layouts, groups of value heads, the
  * floor on g and the states are gdn_chunk_forward's; there is no beta and no
  * normalisation of q and k.  (A NaN in g is not floored: the outputs of its
- * head from that token on are NaN.)  g has one of two layouts:
+ * head from that token on are NaN.)  An infinity or a NaN in q, k, v or an
+ * upstream gradient leaves every result finite that the recurrence does not
+ * make of it -- tokens before it, and in dk and dv those behind it, whatever
+ * chunk they share; the others are infinite or NaN (which, is not specified).
+ * g has one of two layouts:
  *   GDN_DECAY_PER_TOKEN   g [tokens, Hv] fp32 (decode: [N, Hv])
  *   GDN_DECAY_PER_HEAD    g [Hv] fp32, one decay a head for every token     */
 #define GDN_DECAY_PER_TOKEN 0

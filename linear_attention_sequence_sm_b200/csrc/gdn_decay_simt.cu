@@ -269,7 +269,10 @@ decay_pass_simt_kernel(const __grid_constant__ DecayPass a0, const __grid_consta
                     for (int p = 0; p < 4; ++p)
 #pragma unroll
                         for (int q = 0; q < 8; ++q) acc[p][q] = both(0.f);
-                    for (int c = 0; c < C; c += 4) {
+                    // Only pairs inside the mask are multiplied: a zero of P times an infinity or a NaN further on (back in
+                    // time, backward) would be NaN.  Tokens 4 rg .. are this thread's rows: whole groups of four before
+                    // (behind) them, and a triangle of their own.
+                    for (int c = a.reverse ? 4 * rg + 4 : 0; c < (a.reverse ? C : 4 * rg); c += 4) {
                         ulonglong2 pr[4];
 #pragma unroll
                         for (int p = 0; p < 4; ++p) pr[p] = ld4(tp + (4 * rg + p) * LP + c);
@@ -280,6 +283,18 @@ decay_pass_simt_kernel(const __grid_constant__ DecayPass a0, const __grid_consta
                             const ulonglong2 zv = make_ulonglong2(pair(zc[0], zc[lz]), pair(zc[2 * lz], zc[3 * lz]));
 #pragma unroll
                             for (int p = 0; p < 4; ++p) acc[p][q] = dot4(pr[p], zv, acc[p][q]);
+                        }
+                    }
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        if (16 * q >= dzp) break;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float zj = tz[(4 * rg + j) * lz + cg + 16 * q];
+#pragma unroll
+                            for (int p = 0; p < 4; ++p)
+                                if (a.reverse ? j >= p : j <= p)
+                                    acc[p][q] = fma2(pair(tp[(4 * rg + p) * LP + 4 * rg + j], 0.f), pair(zj, 0.f), acc[p][q]);
                         }
                     }
 #pragma unroll

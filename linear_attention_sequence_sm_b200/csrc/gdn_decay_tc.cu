@@ -29,7 +29,8 @@
 // `dot` passes, whose products with the start state feed the decays' fp32
 // gradient, Sigma's copy is split into three terms as well; otherwise X1 ends
 // in a bf16 output, and one bf16 copy costs it as much as the output's own
-// rounding.  P is one bf16 term for the same reason.
+// rounding.  P is one bf16 term for the same reason.  An infinity in z leaves
+// NaN in the state (its terms are inf and inf - inf).
 //
 // Roles (8 warpgroups; a role's warps are latency-bound, so the work is spread
 // until the products set the pace):
@@ -296,6 +297,58 @@ __device__ __forceinline__ void stmatrix_t(uint32_t addr, uint32_t a, uint32_t b
                  : "memory");
 }
 
+__device__ __forceinline__ float tmem_ld_1(uint32_t taddr) {
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
+    tmem_wait_ld();
+    return __uint_as_float(r);
+}
+
+// An out warp's 32 tokens (from 32 part) x 32 z columns (from z0) once more,
+// where X2 is not finite: a zero of P times an infinity or a NaN of z is NaN,
+// so z at one token reaches tokens before it (behind it, backward in time) that
+// it has nothing to do with.  Those are summed here over the pairs inside the
+// mask alone, x, y and z read from global memory, X1 from tensor memory (column
+// x1).  The other tokens keep what the products gave, which is not finite.
+// Kept short (nothing unrolled) and out of the way: it stands in the out warps'
+// loop, and unrolled it cost dq's pass 30 us without ever running.
+template <bool kRev, bool kF32>
+__device__ __forceinline__ void redo_tile(const DecayPass &a, const UnitWalk<kRev> &w, int t0, int L, int part, int z0, int lane,
+                                          uint32_t x1, const float *vec, uint32_t stage) {
+    const int hv = a.hv, zc = z0 + lane;
+    const size_t tok = size_t(w.seg.start) + t0;
+    auto rows = [&](const void *p, int heads, int d) {
+        return static_cast<const __nv_bfloat16 *>(p) + (tok * heads + w.h / (hv / heads)) * size_t(d);
+    };
+    const __nv_bfloat16 *x = rows(a.x, a.hx, a.dy), *y = rows(a.y, a.hy, a.dy), *z = rows(a.z, a.hz, a.dz) + zc;
+    const size_t xs = size_t(a.hx) * a.dy, ys = size_t(a.hy) * a.dy, zs = size_t(a.hz) * a.dz;
+    int edge = kRev ? -1 : kDecayChunk;  // the first (backward: last) token whose z is not finite
+    if (zc < a.dz)
+#pragma unroll 1
+        for (int c = 0; c < L; ++c)
+            if (!isfinite(to_f32(z[c * zs]))) edge = kRev ? c : min(edge, c);
+    const bool none = edge < 0 || edge == kDecayChunk;
+#pragma unroll 1
+    for (int r = 32 * part; r < min(L, 32 * part + 32); ++r) {
+        const bool mine = zc < a.dz && !none && (kRev ? r > edge : r < edge);
+        if (!__any_sync(0xffffffffu, mine)) continue;
+        float o = vec[kVecIn + r] * tmem_ld_1(x1 + uint32_t(r));
+#pragma unroll 1
+        for (int c = kRev ? r : 0; c < (kRev ? L : r + 1); ++c) {
+            float p = 0.f;
+#pragma unroll 1
+            for (int e = lane; e < a.dy; e += 32) p = fmaf(to_f32(x[r * xs + e]), to_f32(y[c * ys + e]), p);
+#pragma unroll 1
+            for (int m = 16; m > 0; m >>= 1) p += __shfl_xor_sync(0xffffffffu, p, m);
+            p *= exp2f(kRev ? vec[kVecG + c] - vec[kVecG + r] : vec[kVecG + r] - vec[kVecG + c]);
+            if (mine) o = fmaf(to_f32(__float2bfloat16_rn(p)), to_f32(z[c * zs]), o);  // (P as the products have it)
+        }
+        if (mine && kF32) static_cast<float *>(a.out)[((tok + r) * hv + w.h) * a.dz + zc] = o;
+        const uint32_t rr = uint32_t(r - 32 * part);
+        if (mine && !kF32) st_shared_b16(stage + rr * 64 + (((uint32_t(lane) >> 3) ^ ((rr >> 1) & 3)) << 4) + 2 * (lane & 7), o);
+    }
+}
+
 template <int kKind, bool kRev, bool kF32>
 __global__ void __launch_bounds__(kThreads, 1)
 decay_pass_tc_kernel(const __grid_constant__ Maps tm, const DecayPass a) {
@@ -528,6 +581,8 @@ constexpr int kW = K::kCopies == 1 ? 8 : 4;  // words of a slice (fewer where it
                     const size_t step = size_t(hv) * dz;
                     const size_t at = (tok * hv + w.h) * dz + 32 * quarter;
                     float y2[kDots ? 2 : 1][2][8];
+                    f32x2 all = both(0.f);  // the sum of X2's values: whether all of them are finite
+                    bool odd = false;
                     if constexpr (kDots) {
                         // X2 first: QK waits for its columns
 #pragma unroll
@@ -539,6 +594,13 @@ constexpr int kW = K::kCopies == 1 ? 8 : 4;  // words of a slice (fewer where it
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(kBX2Free));
+#pragma unroll
+                        for (int pp = 0; pp < 2; ++pp)
+#pragma unroll
+                            for (int l = 0; l < 2; ++l)
+#pragma unroll
+                                for (int e = 0; e < 8; e += 2) all = add2(all, pair(y2[pp][l][e], y2[pp][l][e + 1]));
+                        odd = __any_sync(0xffffffffu, !isfinite(lo_of(all) + hi_of(all)));
                     }
 #pragma unroll(kDots ? 2 : 1)
                     for (int pp = 0; pp < 2; ++pp) {  // 16 tokens (rolled: the roles share the instruction caches)
@@ -555,10 +617,19 @@ constexpr int kW = K::kCopies == 1 ? 8 : 4;  // words of a slice (fewer where it
                             }
                         }
                         tmem_wait_ld();
+                        if constexpr (!kDots) {
+#pragma unroll
+                            for (int l = 0; l < 2; ++l)
+#pragma unroll
+                                for (int e = 0; e < 8; e += 2) all = add2(all, pair(x2[l][e], x2[l][e + 1]));
+                        }
                         if (pp == 1) {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(bar(kBOutFree));
+                            if (!kDots) odd = __any_sync(0xffffffffu, !isfinite(lo_of(all) + hi_of(all)));
+                            if (__builtin_expect(!odd, 1)) {
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(bar(kBOutFree));
+                            }
                         }
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
@@ -653,6 +724,12 @@ constexpr int kW = K::kCopies == 1 ? 8 : 4;  // words of a slice (fewer where it
                         }
                     }
                     __syncwarp();
+                    if (__builtin_expect(odd, 0)) {
+                        redo_tile<kRev, kF32>(a, w, t0, L, part, 32 * quarter, lane, tq + K::kColX1, vecs(mm), stage_u);
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(kBOutFree));
+                    }
                     if (lane == 0) mbar_arrive(bar(kBVecFree + int(mm & 3u)));
                     if (!kF32) {
                         __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.out) + at;
