@@ -223,8 +223,6 @@ gdn_status_t gdn_decay_backward(const gdn_shape_t *s, const void *q, const void 
     const int hk = s->num_qk_heads, hv = s->num_v_heads, d_k = s->head_dim_k, d_v = s->head_dim_v;
     cudaError_t e = launch_decay_schedule(*s, cu_seqlens, ws, L, stream);
     if (e != cudaSuccess) return cuda_fail(e, "schedule kernel launch");
-    if (tokens == 0 && g_layout == GDN_DECAY_PER_HEAD && dg && (e = cudaMemsetAsync(dg, 0, 4 * size_t(hv), stream)) != cudaSuccess)
-        return cuda_fail(e, "clearing dg");
     auto at = [&](size_t off) { return reinterpret_cast<float *>(ws + off); };
     const bool grouped = hv != hk;
     const DecayPass base = pass_of(*s, sc, g, g_layout);
@@ -291,7 +289,12 @@ gdn_status_t gdn_decay_backward(const gdn_shape_t *s, const void *q, const void 
     // (dk's pass reads the start states that dq's pass writes)
     if ((e = run_pass(pq, *s, units, stream, &pv)) != cudaSuccess || (e = run_pass(pk, *s, units, stream)) != cudaSuccess)
         return cuda_fail(e, "backward launch");
-    if (tokens == 0) return GDN_OK;
+    if (tokens == 0) {  // (a rejected cu_seqlens leaves dg as it was: the kernel looks at the status)
+        e = dg && base.g_const ? launch_decay_dg(*s, cu_seqlens, L, sc, nullptr, nullptr, nullptr, nullptr, g, true,
+                                                 at(L.dgtok_off), dg, stream)
+                               : cudaSuccess;
+        return e == cudaSuccess ? GDN_OK : cuda_fail(e, "decay gradient launch");
+    }
     if (dg) {
         e = decay_tc_supported(*s)
                 ? launch_decay_intra(*s, cu_seqlens, L, sc, q, k, v, d_o, g, base.g_const, at(L.intra_off), stream)

@@ -526,3 +526,22 @@ def test_one_infinity_or_nan_reaches_what_it_must_and_no_more(form, x, where):
             else:
                 assert torch.equal(g[~hit], b[~hit]), (name, k)
             assert not bool(g[hit].isfinite().any()), (name, k)
+
+
+def test_no_tokens_and_a_rejected_cu_seqlens():
+    """Without tokens a fixed decay's gradient is zero, and as it was where cu_seqlens is rejected."""
+    import ctypes
+    from linear_attention_sequence_sm_b200 import gdn
+    q, v = torch.empty(0, 1, 64, dtype=torch.bfloat16, device="cuda"), torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    g = torch.full((2,), -0.5, device="cuda")
+    for cus, want in (([0, 0, 0], 0.0), ([0, 5, 0], 7.0), ([1, 0, 0], 7.0)):
+        cu = torch.tensor(cus, dtype=torch.int32, device="cuda")
+        sh = gdn.make_shape(q, v, cu, 64)
+        n = gdn.decay_workspace_size(sh, backward=True)
+        ws, dg = torch.empty(n, dtype=torch.uint8, device="cuda"), torch.full((2,), 7.0, device="cuda")
+        p = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+        st = gdn.LIB.gdn_decay_backward(ctypes.byref(sh), p(q), p(q), p(v), p(g), gdn.GDN_DECAY_PER_HEAD, None, p(cu),
+                                        p(v), None, p(q), p(q), p(v), p(dg), None, p(ws), n, None)
+        assert st == gdn.GDN_OK
+        assert gdn.read_device_status(ws) == (gdn.GDN_OK if want == 0 else gdn.GDN_ERR_DEVICE_CHECK)
+        assert dg.tolist() == [want, want]
