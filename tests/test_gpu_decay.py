@@ -545,3 +545,66 @@ def test_no_tokens_and_a_rejected_cu_seqlens():
         assert st == gdn.GDN_OK
         assert gdn.read_device_status(ws) == (gdn.GDN_OK if want == 0 else gdn.GDN_ERR_DEVICE_CHECK)
         assert dg.tolist() == [want, want]
+
+
+@pytest.mark.parametrize("form", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(2, 4, 128, 128), (1, 2, 24, 40)], ids=str)
+def test_more_units_than_blocks(shape, form):
+    """Blocks take several (sequence, head) pairs one after the other, of unequal lengths, some empty: 148 blocks on
+    the tensor cores, 1184 on the CUDA cores."""
+    gen = torch.Generator().manual_seed(55)
+    n = (2800 if form == "f32" else 400) // shape[1]
+    pool = torch.tensor([0, 1, 2, 63, 64, 65] if form == "bf16" else [0, 1, 2, 5])
+    lens = pool[torch.randint(len(pool), (n,), generator=gen)].tolist()
+    lens[3::50] = [130] * len(lens[3::50])
+    d = R.make(55, *shape, torch.float32 if form == "f32" else torch.bfloat16, lens=lens)
+    check_forward(d, *run_forward(d))
+    check_backward(d, grads(d))
+
+
+@pytest.mark.parametrize("per_token", [True, False])
+def test_more_cut_units_than_blocks(per_token):
+    """Units of cut sequences, more of them than blocks, with local states, joins and start states for each."""
+    d = R.make(56, 4, 12, 64, 64, torch.bfloat16, lens=[3900, 40, 1], per_token=per_token)
+    check_forward(d, *run_forward(d))
+    check_backward(d, grads(d))
+
+
+def two_terms(x):
+    """x as the sum of its two leading bf16 terms."""
+    a = x.bfloat16().float()
+    return a + (x - a).bfloat16().float()
+
+
+def worst_for_two_terms(values):
+    """The value whose two leading bf16 terms leave the most of it, and what they leave (relative)."""
+    left = (two_terms(values) / values - 1).abs()
+    i = int(left.argmax())
+    return values[i], float(left[i])
+
+
+def test_third_terms_are_there():
+    """States and the dots of the decays' gradient are sums of three bf16 terms.  Inputs that are all alike, so that
+    what a lost third term takes off adds up: about 2^-18, 64 half steps of fp32.  With sums of equal values, most of
+    them exact, the results must be within 16."""
+    bar = 16 * R.U32
+    # The state after 64 tokens, z = y = 1: 63 e^g + 1 with one decay at the end; e^g, the weight of all tokens but the
+    # last, is what is split (the exponential is within two units, four half steps, of the true one).
+    gs = -torch.rand(20000, generator=torch.Generator().manual_seed(57)) * 0.5
+    w, left = worst_for_two_terms(gs.exp())
+    assert left > 3.5 * bar
+    g = torch.zeros(1, 64, 1)
+    g[0, -1, 0] = gs[int((gs.exp() == w).nonzero()[0])]
+    one = torch.ones(1, 64, 1, 128, dtype=torch.bfloat16)
+    d = dict(q=one, k=one, v=one, g=g, s0=torch.zeros(1, 1, 128, 128), cu=None, do=one, dsf=None)
+    _, sf = run_forward(d)
+    _, rs = R.forward(d["q"], d["k"], d["v"], d["g"], d["s0"])
+    assert float((sf.double().cpu() / rs - 1).abs().max()) <= bar
+    # dg without decays, from an initial state of one value: the dot of q with S0^T do, S0's copy in three terms
+    s, left = worst_for_two_terms(1 + torch.rand(20000, generator=torch.Generator().manual_seed(58)))
+    assert left > 3.5 * bar
+    d.update(g=torch.zeros(1, 64, 1), v=torch.zeros_like(one), s0=torch.full((1, 1, 128, 128), float(s)))
+    got = grads(d)
+    ref = R.backward(d["q"], d["k"], d["v"], d["g"], d["do"], None, d["s0"])
+    rel = (got["dg"].double().cpu().reshape(ref["dg"].shape) / ref["dg"] - 1).abs()
+    assert float(rel.max()) <= bar
