@@ -746,6 +746,11 @@ def _new(stream, dev, make, *args, **kw):
     return t
 
 
+def _like(stream, dev):
+    """torch.empty_like by _new."""
+    return torch.empty_like if stream is None else lambda t: _new(stream, dev, torch.empty_like, t)
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -808,9 +813,9 @@ def decay_forward(q, k, v, g, initial_state=None, cu_seqlens=None, output_final_
     _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
     shape = make_shape(q, v, cu_seqlens, 64, force_simt)
     if out is None:
-        out = _new(stream, dev, torch.empty_like, v)
+        out = _like(stream, dev)(v)
     if final_state is None and output_final_state:
-        final_state = _new(stream, dev, torch.empty_like, initial_state) if initial_state is not None else \
+        final_state = _like(stream, dev)(initial_state) if initial_state is not None else \
             _new(stream, dev, torch.empty, (n_seqs, hv, dv, dk), dtype=torch.float32, device=dev)
     workspace = _room(workspace, decay_workspace_size(shape), dev, stream)
     osc = output_norm.c_struct(out) if output_norm is not None else None
@@ -843,7 +848,7 @@ def decay_decode_step(q, k, v, g, state, out=None, stream=None, output_norm: Out
         _need(g, "g", torch.float32, dev)
         _need(state, "state", torch.float32, dev)
     if out is None:
-        out = _new(stream, dev, torch.empty_like, v)
+        out = _like(stream, dev)(v)
     N, hk, dk = qs
     hv, dv = vs[1], vs[2]
     osc = output_norm.c_struct(out) if output_norm is not None else None
@@ -872,7 +877,7 @@ def decay_backward(q, k, v, g, d_o, d_final_state=None, initial_state=None, cu_s
     _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
     shape = make_shape(q, v, cu_seqlens, 64, force_simt)
     workspace = _room(workspace, decay_workspace_size(shape, backward=True), dev, stream)
-    like = lambda t: _new(stream, dev, torch.empty_like, t)  # noqa: E731
+    like = _like(stream, dev)
     out = {"dq": like(q), "dk": like(k), "dv": like(v), "dg": like(g) if want_dg else None,
            "d_initial_state": _new(stream, dev, torch.empty, (n_seqs, hv, dv, dk), dtype=torch.float32, device=dev)
            if want_d_initial_state else None}
@@ -965,9 +970,9 @@ def block_norm_forward(x, residual, norm: BlockNorm, gate=None, h=None, y=None, 
     rows, width, rt = _block_norm_inputs(x, residual, norm, gate, more)
     dev = x.device
     if h is None:
-        h = _new(stream, dev, torch.empty_like, x if residual is None else residual)
+        h = _like(stream, dev)(x if residual is None else residual)
     if y is None and norm.pre_norm:
-        y = _new(stream, dev, torch.empty_like, x)
+        y = _like(stream, dev)(x)
     c = norm.c_struct(x, gate)
     with _on(dev):  # the library launches on the current device
         _check(LIB.gdn_block_norm_forward(rows, width, _dtype_code(x), _dtype_code(h), x.data_ptr(), _addr(residual),
@@ -995,8 +1000,9 @@ def block_norm_backward(x, residual, norm: BlockNorm, gate=None, d_h=None, d_y=N
     rows, width, rt = _block_norm_inputs(x, residual, norm, gate, ((d_h, "d_h", True), (d_y, "d_y", False)))
     dev = x.device
     workspace = _room(workspace, block_norm_workspace_size(rows, width), dev, stream)
-    like = lambda t: None if t is None else _new(stream, dev, torch.empty_like, t)  # noqa: E731
-    out = {"dx": like(x), "d_residual": like(residual), "d_gate": like(gate),
+    new = _like(stream, dev)
+    like = lambda t: None if t is None else new(t)  # noqa: E731
+    out = {"dx": new(x), "d_residual": like(residual), "d_gate": like(gate),
            "d_post_weight": like(norm.post_weight), "d_scale": like(norm.scale), "d_pre_weight": like(norm.pre_weight)}
     c = norm.c_struct(x, gate)
     code = GDN_DTYPE_F32 if rt == torch.float32 else GDN_DTYPE_BF16
