@@ -983,8 +983,9 @@ block_norm_columns_kernel(const float *__restrict__ part, int lines, int width, 
 // Threads a row takes (a multiple of 32) with `groups` 8-value groups each.
 int row_threads(int width, int groups) { return ((width + 8 * groups - 1) / (8 * groups) + 31) / 32 * 32; }
 
-// Launch shape: threads per row and rows per block (256 threads at least, so
-// that short rows fill an SM), 8 columns a thread up to 4096 columns.
+// Launch shape: threads per row and rows per block (as many whole rows as 256
+// threads take, eight at most, or one row), 8 columns a thread up to 4096
+// columns.
 struct Shape {
     int groups, n, per;
 };

@@ -78,6 +78,8 @@ __device__ void block_scan(int (&v)[kN], int (&totals)[kN], int *part) {
 // first sweep over all segments but one end's (k and v are then read twice, a
 // third of the prefill's traffic; the uncut chain would take at least twice as
 // long).  At 1 x 65,536 tokens and 48 heads: 3 segments of 21,888 tokens.
+// Below 2 B nothing is cut, and units go to CTAs with a fixed stride: 160 equal
+// units on 148 SMs take two chains' time, 96 leave 52 SMs idle.
 __global__ void __launch_bounds__(kSchedThreads)
 decay_schedule_kernel(int32_t num_seqs, int32_t tokens, int32_t batched_len, int32_t hv, DecayPlan plan,
                       const int32_t *__restrict__ cu, DecaySched sc, int32_t *order) {

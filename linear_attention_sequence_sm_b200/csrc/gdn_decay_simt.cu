@@ -9,10 +9,14 @@
 // are 16 bytes; rows are padded by 4 floats so that a quarter-warp's rows fall
 // into different banks.
 //
-// What bounds it is the fp32 pipes and shared-memory reads: 5003 ragged tokens
-// of 8 heads, 64 x 96, take 157 us with their split (a chunk has 1.4 M
-// multiply-adds, 11,300 cycles of an SM's fp32 lanes).  Tiles sized by the heads instead of 128 wide, two blocks an SM:
-// 336 -> 246 us; paired arithmetic and loads in batches: 246 -> 158 us.
+// What bounds it is the chain of phases inside a chunk (loads, P, out, Sigma,
+// with barriers between them), which two blocks an SM overlap only in part:
+// 5003 ragged tokens of 8 heads, 64 x 96, take 154 us -- 95 for the pass, 36
+// for the sweep at the cuts, the rest for the join, the schedule and the
+// launches -- where the multiply-adds (1.4 M a chunk, 11,300 cycles of an SM's
+// fp32 lanes) would take 35.  Tiles sized by the heads instead of 128 wide, two
+// blocks an SM: 336 -> 246 us; paired arithmetic and loads in batches: 246 ->
+// 158 us.
 #include <algorithm>
 
 #include "gdn_decay.cuh"

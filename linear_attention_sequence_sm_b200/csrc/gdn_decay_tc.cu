@@ -51,8 +51,8 @@
 // copies of Sigma) two.
 //
 // Measured on a B200, 4 x 4096 tokens, 32 heads, d = 128 (128 units, 64 chunks
-// each): 130 us plain, 232 us with dots and fp32 out (dq) and 276 us backward
-// in time (dk); 65,536 x 48 heads: 386 us for the states at the cuts and 701 us
+// each): 127 us plain, 231 us with dots and fp32 out (dq) and 284 us backward
+// in time (dk); 65,536 x 48 heads: 335 us for the states at the cuts and 635 us
 // for the outputs.  A plain chunk
 // takes about 3900 cycles, its products 2060 of them (tensor pipe 33 % busy
 // over all SMs, 40 % where 148 are used); DRAM traffic is what the operands
