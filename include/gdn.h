@@ -39,7 +39,8 @@
  *     other than GDN_OK means nothing was enqueued, except GDN_ERR_CUDA
  *     raised by a launch, which reports the CUDA error of that launch.
  *   - The last error's detail text is kept per host thread
- *     (gdn_last_error_message).
+ *     (gdn_last_error_message).  Calls may be made from several host threads
+ *     at once, each with buffers and a workspace of its own.
  */
 #ifndef GDN_H_
 #define GDN_H_
@@ -525,13 +526,20 @@ GDN_API gdn_status_t gdn_decay_decode_step(int32_t num_seqs, int32_t num_qk_head
 /* Gradients of L = sum d_o . o + sum d_final_state . S_final for
  * gdn_decay_forward (without an output side):
  *   dq, dk           [tokens, Hk, d_k] dtype: summed over the value heads of
- *                    each group in 32 bits, rounded once
+ *                    each group in 32 bits, rounded once (bf16 on the tensor
+ *                    cores: the weights of pairs inside a chunk of 64 tokens
+ *                    are rounded to bf16 before they are summed, so where
+ *                    terms cancel the error goes by their size)
  *   dv               [tokens, Hv, d_v] dtype
  *   dg               g's layout, fp32, or NULL where the decays are not
  *                    learned (saves the pairwise sums); zero where g < -20
  *   d_initial_state  [N, Hv, d_v, d_k] fp32, or NULL
  *   d_final_state    NULL = zero
  * Every sum is taken in a fixed order: the same call gives the same bits.
+ * Each dg is within a few hundred half steps of fp32 of a_t |dS_t| |S_(t-1)|,
+ * however its decay compares with its neighbours'.  The workspace holds, beside
+ * fp32 parts of dq and dk for grouped heads, the state at the start of every
+ * chunk of 64 tokens (64 KB a value head at d = 128).
  * A rejected cu_seqlens leaves the gradients as they were. */
 GDN_API gdn_status_t gdn_decay_backward_workspace_size(const gdn_shape_t *shape, size_t *bytes);
 GDN_API gdn_status_t gdn_decay_backward(const gdn_shape_t *shape,
